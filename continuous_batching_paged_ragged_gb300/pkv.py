@@ -33,6 +33,13 @@ PKV_ALLOC_RESERVE = 1
 PKV_UNIT_PASS = 0
 PKV_UNIT_REQUEST = 1
 
+PKV_ROPE_HALF = 0
+PKV_ROPE_INTERLEAVED = 1
+PKV_ROPE_SCALE_NONE = 0
+PKV_ROPE_SCALE_LINEAR = 1
+PKV_ROPE_SCALE_BANDS = 2
+PKV_ROPE_SCALE_RAMP = 3
+
 PKV_KV_F16 = 0
 PKV_KV_E4M3 = 1
 
@@ -41,12 +48,19 @@ DEFAULT_SPLIT_BLOCKS = 32  # pkv_config.split_blocks = 0 selects this many block
 _p = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
+_f64 = ctypes.c_double
 _sz = ctypes.c_size_t
 
 
 class pkv_config(ctypes.Structure):
     _fields_ = [("num_layers", _i32), ("num_q_heads", _i32), ("num_kv_heads", _i32), ("head_dim", _i32),
                 ("block_size", _i32), ("num_blocks", _i32), ("split_blocks", _i32), ("kv_dtype", _i32)]
+
+
+class pkv_rope_config(ctypes.Structure):
+    _fields_ = [("head_dim", _i32), ("rot_dim", _i32), ("layout", _i32), ("scaling", _i32), ("base", _f64),
+                ("factor", _f64), ("original_context", _f64), ("low_turns", _f64), ("high_turns", _f64),
+                ("output_scale", _f64)]
 
 
 class pkv_sched_config(ctypes.Structure):
@@ -86,6 +100,15 @@ SIGNATURES = {
     "pkv_attention_noalloc": (ctypes.c_int, [_p, _i32, _p, _p, _i32, _p, _p, _i32, _i32, _p, _p]),
     "pkv_attention_append": (ctypes.c_int, [_p, _i32, _p, _p, _p, _p, _p, _i32, _p, _p, _i32, _i32, _p, _p, _sz,
                                             _p]),
+    "pkv_rope_create": (ctypes.c_int, [ctypes.POINTER(pkv_rope_config), ctypes.POINTER(_p)]),
+    "pkv_rope_destroy": (None, [_p]),
+    "pkv_rope_frequencies": (_i32, [_p, ctypes.POINTER(_f64), _i32]),
+    "pkv_positions": (ctypes.c_int, [_p, _p, _p, _i32, _i32, _p, _p]),
+    "pkv_rope_append": (ctypes.c_int, [_p, _i32, _p, _p, _i64, _p, _i64, _p, _i64, _p, _p, _i32, _p, _p]),
+    "pkv_copy_blocks": (ctypes.c_int, [_p, _p, _i32, _p]),
+    "pkv_fork_rows": (ctypes.c_int, [_p, _p, _i32, _p, _i32, _p, _i32, _p]),
+    "pkv_compact_workspace_bytes": (_sz, [_p]),
+    "pkv_compact": (ctypes.c_int, [_p, _p, _i32, _i32, _p, _p, _p, _p, _sz, _p]),
     "pkv_debug_expire_wait": (ctypes.c_int, [_p, _i64, _p]),
     "pkv_last_launch_count": (_i32, [_p]),
     "pkv_last_error": (ctypes.c_char_p, []),
@@ -216,6 +239,55 @@ def pkv_attention_append(pool: int, layer: int, q, k, v, slot_mapping, block_tab
            "pkv_attention_append")
 
 
+def pkv_rope_create(cfg: pkv_rope_config) -> int:
+    h = _p()
+    _check(load().pkv_rope_create(ctypes.byref(cfg), ctypes.byref(h)), "pkv_rope_create")
+    return h.value
+
+
+def pkv_rope_destroy(rope: int) -> None:
+    load().pkv_rope_destroy(rope)
+
+
+def pkv_rope_frequencies(rope: int) -> np.ndarray:
+    out = np.empty(load().pkv_rope_frequencies(rope, None, 0), dtype=np.float64)
+    load().pkv_rope_frequencies(rope, out.ctypes.data_as(ctypes.POINTER(_f64)), out.size)
+    return out
+
+
+def pkv_positions(pool: int, context_lens, query_start_loc, num_seqs: int, num_tokens: int, positions,
+                  stream=None) -> None:
+    _check(load().pkv_positions(pool, _ptr(context_lens), _ptr(query_start_loc), num_seqs, num_tokens, _ptr(positions),
+                                _stream(stream)), "pkv_positions")
+
+
+def pkv_rope_append(pool: int, layer: int, rope: int, q, q_stride: int, k, k_stride: int, v, v_stride: int, positions,
+                    slot_mapping, num_tokens: int, q_out, stream=None) -> None:
+    _check(load().pkv_rope_append(pool, layer, rope, _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+                                  _ptr(positions), _ptr(slot_mapping), num_tokens, _ptr(q_out), _stream(stream)),
+           "pkv_rope_append")
+
+
+def pkv_copy_blocks(pool: int, pairs, num_pairs: int, stream=None) -> None:
+    _check(load().pkv_copy_blocks(pool, _ptr(pairs), num_pairs, _stream(stream)), "pkv_copy_blocks")
+
+
+def pkv_fork_rows(pool: int, block_tables, max_blocks_per_seq: int, context_lens, num_seqs: int, forks, num_forks: int,
+                  stream=None) -> None:
+    _check(load().pkv_fork_rows(pool, _ptr(block_tables), max_blocks_per_seq, _ptr(context_lens), num_seqs, _ptr(forks),
+                                num_forks, _stream(stream)), "pkv_fork_rows")
+
+
+def pkv_compact_workspace_bytes(pool: int) -> int:
+    return load().pkv_compact_workspace_bytes(pool)
+
+
+def pkv_compact(pool: int, block_tables, max_blocks_per_seq: int, num_seqs: int, new_tables, remap, num_live, workspace,
+                workspace_bytes: int, stream=None) -> None:
+    _check(load().pkv_compact(pool, _ptr(block_tables), max_blocks_per_seq, num_seqs, _ptr(new_tables), _ptr(remap),
+                              _ptr(num_live), _ptr(workspace), workspace_bytes, _stream(stream)), "pkv_compact")
+
+
 def pkv_debug_expire_wait(pool: int, limit_ns: int, stream=None) -> None:
     """Test hook (needs PKV_TEST_HOOKS=1): a bounded on-chip wait that runs out after limit_ns."""
     _check(load().pkv_debug_expire_wait(pool, limit_ns, _stream(stream)), "pkv_debug_expire_wait")
@@ -289,6 +361,37 @@ class Pool:
     def close(self):
         if self.handle:
             pkv_pool_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Rope:
+    """Rotary frequencies (pkv_rope_*): pass ``handle`` to pkv_rope_append."""
+
+    SCALINGS = {"none": PKV_ROPE_SCALE_NONE, "linear": PKV_ROPE_SCALE_LINEAR, "bands": PKV_ROPE_SCALE_BANDS,
+                "ramp": PKV_ROPE_SCALE_RAMP}
+
+    def __init__(self, head_dim: int, rot_dim: int = 0, interleaved: bool = False, base: float = 10000.0,
+                 scaling: str = "none", factor: float = 1.0, original_context: float = 0.0, low_turns: float = 0.0,
+                 high_turns: float = 0.0, output_scale: float = 1.0):
+        self.handle = 0
+        self.cfg = pkv_rope_config(head_dim, rot_dim, PKV_ROPE_INTERLEAVED if interleaved else PKV_ROPE_HALF,
+                                   self.SCALINGS[scaling], base, factor, original_context, low_turns, high_turns,
+                                   output_scale)
+        self.handle = pkv_rope_create(self.cfg)
+
+    def frequencies(self) -> np.ndarray:
+        """Radians a token of each rotated pair."""
+        return pkv_rope_frequencies(self.handle)
+
+    def close(self):
+        if self.handle:
+            pkv_rope_destroy(self.handle)
             self.handle = 0
 
     def __del__(self):

@@ -264,6 +264,130 @@ pkv_status pkv_attention_noalloc(pkv_pool* pool, int32_t layer, const void* q, c
                                  const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens, void* out,
                                  void* stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Rotary positions and the append in one call
+ *
+ * A model with rotary positions turns pair i of every query and key head by the angle position * f_i
+ * before the key is cached.  The pages have no counterpart (their rows are positions in a cache); these
+ * calls put the rotation next to pkv_append, so that keys are rotated on their way into their slots and
+ * queries on their way into the packed rows pkv_attention reads.
+ *
+ * Of each head's head_dim values the first rot_dim are rotated, the others pass through.  Pair i
+ * (0 <= i < rot_dim / 2) is values (i, i + rot_dim / 2) with PKV_ROPE_HALF and (2i, 2i + 1) with
+ * PKV_ROPE_INTERLEAVED:
+ *     a' = output_scale * (a cos - b sin),   b' = output_scale * (b cos + a sin).
+ * Frequencies f_i = base^(-2i / rot_dim), then for long contexts, with t_i = original_context * f_i / (2 pi)
+ * the pair's turns over the original context:
+ *     PKV_ROPE_SCALE_NONE    f_i
+ *     PKV_ROPE_SCALE_LINEAR  f_i / factor
+ *     PKV_ROPE_SCALE_BANDS   f_i (w + (1 - w) / factor), w = clamp((t_i - low_turns) / (high_turns - low_turns), 0, 1)
+ *     PKV_ROPE_SCALE_RAMP    f_i (w + (1 - w) / factor), w = 1 - clamp((i - lo) / max(hi - lo, 0.001), 0, 1), where
+ *                            pair(t) = rot_dim ln(original_context / (2 pi t)) / (2 ln base),
+ *                            lo = max(floor(pair(high_turns)), 0), hi = min(ceil(pair(low_turns)), rot_dim - 1)
+ * Angles are reduced modulo a turn exactly: f_i (computed in 64-bit floating point) over 2 pi is held as a 64-bit
+ * binary fraction, and its product with the position wraps (below 2^-32 turns off at any int32 position).  cos, sin and the rotation are fp32;
+ * each result is rounded once to fp16.
+ * ---------------------------------------------------------------------------------------------- */
+#define PKV_ROPE_HALF         0
+#define PKV_ROPE_INTERLEAVED  1
+#define PKV_ROPE_SCALE_NONE   0
+#define PKV_ROPE_SCALE_LINEAR 1
+#define PKV_ROPE_SCALE_BANDS  2
+#define PKV_ROPE_SCALE_RAMP   3
+
+typedef struct {
+  int32_t head_dim;         /* 64, 128 or 256                                                          */
+  int32_t rot_dim;          /* values rotated, a multiple of 16 up to head_dim; 0 = head_dim             */
+  int32_t layout;           /* PKV_ROPE_HALF or PKV_ROPE_INTERLEAVED                                     */
+  int32_t scaling;          /* PKV_ROPE_SCALE_*                                                          */
+  double base;              /* > 1                                                                       */
+  double factor;            /* > 0 (unused with PKV_ROPE_SCALE_NONE)                                     */
+  double original_context;  /* > 0 (bands, ramp)                                                         */
+  double low_turns;         /* bands, ramp: 0 < low_turns < high_turns; both 0 = 1 and 4 (bands), 1 and 32 (ramp) */
+  double high_turns;
+  double output_scale;      /* factor on the rotated values; 0 = 1                                       */
+} pkv_rope_config;
+
+typedef struct pkv_rope pkv_rope;
+
+/* A host handle holding the frequencies (no device memory).  Any number of pools and threads may use one. */
+pkv_status pkv_rope_create(const pkv_rope_config* cfg, pkv_rope** out);
+void pkv_rope_destroy(pkv_rope* rope);
+
+/* The first n of the rot_dim / 2 frequencies, in radians a token, into out (may be NULL); returns rot_dim / 2. */
+int32_t pkv_rope_frequencies(const pkv_rope* rope, double* out, int32_t n);
+
+/* Absolute positions of a pass's tokens: token i of row b gets context_lens[b] - q_len_b + i (arguments as
+ * pkv_slot_mapping).  Tokens of a row whose metadata is out of range get 0 and set PKV_DEVERR_ROW_META. */
+pkv_status pkv_positions(pkv_pool* pool, const int32_t* context_lens, const int32_t* query_start_loc,
+                         int32_t num_seqs, int32_t num_tokens, int32_t* positions, void* stream);
+
+/* For every token t < num_tokens: q[t] rotated into q_out[t], k[t] rotated and v[t] as it is into slot
+ * slot_mapping[t] of `layer`, as pkv_append would store them (8-bit cache: quantized from the rotated key
+ * rounded to fp16, bit for bit what a rotation followed by pkv_append stores).  A slot of -1 is skipped (its
+ * query is rotated all the same); any other out-of-range slot is skipped and sets PKV_DEVERR_SLOT_RANGE.
+ * Duplicate slots in one call race (last writer unspecified).
+ *
+ * q, k, v       fp16, token t's heads at t * {q,k,v}_stride values from the pointer, [heads][head_dim] within a
+ *               token: separate tensors, or slices of one packed projection.  16-byte aligned; strides multiples of 8 and
+ *               at least heads * head_dim.  q may be NULL (and then q_out): keys and values alone.
+ * positions     int32 [num_tokens]   device; any value (negative ones turn backwards)
+ * slot_mapping  int64 [num_tokens]   device
+ * q_out         fp16 [num_tokens][num_q_heads][head_dim], 16-byte aligned; may be q itself when q_stride is
+ *               num_q_heads * head_dim; must not overlap q, k or v otherwise */
+pkv_status pkv_rope_append(pkv_pool* pool, int32_t layer, const pkv_rope* rope, const void* q, int64_t q_stride,
+                           const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens, void* q_out,
+                           void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Copying, forking and compacting blocks (device, every layer)
+ *
+ * [CB] "The allocator is the other half": requests hold blocks, and a freed block is another's.  These calls
+ * move what blocks hold: K and V of every layer and, on an 8-bit cache, the scale bytes, bit for bit.
+ * ---------------------------------------------------------------------------------------------- */
+
+/* pairs int32 [num_pairs][2] (source, destination), device: block `destination` becomes a copy of block
+ * `source`.  A pair with a -1 in it is skipped (padding); any other id outside [0, num_blocks) skips the
+ * pair and sets PKV_DEVERR_BLOCK_RANGE.  A source may be copied to several destinations; a block that is a
+ * destination must be in no other pair (its contents would depend on the order of the copies; under PKV_VALIDATE=1
+ * such a list is refused with PKV_ERR_INVALID_ARG). */
+pkv_status pkv_copy_blocks(pkv_pool* pool, const int32_t* pairs, int32_t num_pairs, void* stream);
+
+/* Rows that continue from a common prefix (several samples of one prompt, a beam's branches).
+ * forks int32 [num_forks][3] (parent row, child row, block), device.  For each fork, with c = context_lens[parent]:
+ *     the child's table row becomes the parent's first c / 16 entries (shared blocks), then, if c % 16 > 0,
+ *     `block`, then -1;  context_lens[child] = c;  the c % 16 tokens of the parent's last block are copied into
+ *     `block`, whose other rows are left as they were.
+ * The two rows then append without seeing each other: only full blocks are shared.  With c % 16 = 0 `block` is
+ * not used and may be -1.  A fork with a row outside [0, num_seqs), parent = child, or a context
+ * outside [0, 16 * max_blocks_per_seq] does nothing and sets PKV_DEVERR_ROW_META; one whose partial block or `block` is
+ * out of range does nothing and sets PKV_DEVERR_BLOCK_RANGE.  A fork whose parent row is -1 is skipped (padding).
+ * Several forks may share a parent; a child must be in no other fork of the call, and a `block` in no other fork
+ * nor in use (under PKV_VALIDATE=1 a repeated child or block, or a child that is a parent, is refused).
+ *
+ * block_tables int32 [num_seqs][max_blocks_per_seq], context_lens int32 [num_seqs]   device, updated in place */
+pkv_status pkv_fork_rows(pkv_pool* pool, int32_t* block_tables, int32_t max_blocks_per_seq, int32_t* context_lens,
+                         int32_t num_seqs, const int32_t* forks, int32_t num_forks, void* stream);
+
+/* Moves the blocks in use to the front of the pool, so that what is free is one range.  In use is every
+ * block named in block_tables [num_seqs][max_blocks_per_seq] (entries of -1 name none; a block in several rows
+ * counts once; any other id outside [0, num_blocks) names none and sets PKV_DEVERR_BLOCK_RANGE).  With n
+ * blocks in use, the k-th lowest used block of those at n or above is copied to the k-th lowest unused block
+ * below n; the others stay.  Written, all on the device:
+ *     new_tables  int32 [num_seqs][max_blocks_per_seq]  block_tables with every used block's new id (other
+ *                                                       entries as they were); may be block_tables itself
+ *     remap       int32 [num_blocks]                    a used block's new id, -1 for an unused one
+ *     num_live    int32 [1]                             n: blocks n .. num_blocks - 1 are free now
+ * Every table of the pool's requests must be in the call: a block named in none is free, and may be overwritten.
+ * Blocks moved away from keep their contents.
+ * workspace    device, >= pkv_compact_workspace_bytes(pool) bytes, 256-byte aligned; two calls on one workspace must
+ *              be ordered by the caller */
+size_t pkv_compact_workspace_bytes(const pkv_pool* pool);
+pkv_status pkv_compact(pkv_pool* pool, const int32_t* block_tables, int32_t max_blocks_per_seq, int32_t num_seqs,
+                       int32_t* new_tables, int32_t* remap, int32_t* num_live, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 /* Test hook, off by default: refused with PKV_ERR_UNSUPPORTED unless PKV_TEST_HOOKS=1 is in the environment.
  * The pages have no counterpart; it exercises the failure path of [ABL] "Counting jobs while they run" (a
  * job must not be left holding the device).  Launches one kernel whose thread waits on an on-chip barrier
