@@ -22,7 +22,8 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompil
               "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]
 
 LIBS = {
-    "libpkv.so": ["pool.cu", "attention.cu", "decode_e4m3.cu", "prefill.cu", "blocks.cu", "rope.cu",
+    "libpkv.so": ["pool.cu", "attention.cu", "decode_e4m3.cu", "decode_window.cu", "decode_window_e4m3.cu", "prefill.cu",
+                  "prefill_window.cu", "blocks.cu", "rope.cu",
                   "sched.cpp"],
     "libpkv_synth.so": ["synth.cu"],
 }

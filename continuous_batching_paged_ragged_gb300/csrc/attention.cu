@@ -58,6 +58,7 @@ struct MergeParams {
   int group;
   int split_blocks;
   int max_splits;
+  KeyWindow win;
 };
 
 constexpr int kMergeGroups = 32;  // split groups of the long-context merge
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const MergeParams p) {
   const int ctx = __ldg(p.tok_ctx + t);
   const int e0 = blockIdx.z * 32;  // the chunk's first element: head e0 / D, dims e0 % D ..
   if (ctx <= 0 || e0 >= p.group * D) return;
-  const int nblk = (ctx + kBS - 1) / kBS;
+  const int nblk = visible_blocks(ctx, p.win.window, p.win.sinks).n;
   const int nsplit = (nblk + p.split_blocks - 1) / p.split_blocks;
   if (nsplit <= kFusedMergeSplits) return;
   const int tid = threadIdx.x, e4 = tid & 7, sg = tid >> 3;
@@ -176,6 +177,7 @@ struct PlanParams {
                      // rows hold none), then the total; or null
   WsHeader* hdr;
   int32_t* err;
+  KeyWindow win;  // decode tasks, prefill tiles and shadow blocks count what this leaves visible
 };
 
 __device__ __forceinline__ bool row_meta_ok(int q_len, int ctx, int max_ctx) {
@@ -192,8 +194,14 @@ __device__ __forceinline__ void for_row_items(const PlanParams& p, int b, F fn) 
   for (int qb = 0; qb * p.prefill_pos < q_len; ++qb) {
     const int npos = min(p.prefill_pos, q_len - qb * p.prefill_pos);
     const int w = ctx - q_len + qb * p.prefill_pos;
-    fn((w + npos + p.prefill_keys - 1) / p.prefill_keys, npos, q0 + qb * p.prefill_pos, w);
+    const VisibleUnits vis = visible_units(w + npos, window_low(w + 1, p.win.window), p.win.sinks, p.prefill_keys);
+    fn(vis.n, npos, q0 + qb * p.prefill_pos, w);
   }
+}
+
+// The blocks of a row that some of its new tokens see: from its first new token's window on, and the sinks'.
+__device__ __forceinline__ VisibleUnits row_blocks(int ctx, int q_len, const KeyWindow& win) {
+  return visible_units(ctx, window_low(ctx - q_len + 1, win.window), win.sinks, kBS);
 }
 
 // K/V tiles of the two chunks of an item of n tiles (the first chunk takes the extra tile).
@@ -251,7 +259,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       p.tok_row[t] = b;
       p.tok_ctx[t] = c;  // 0: no decode work (prefill row or invalid metadata)
       row = b;
-      nblk = (c + kBS - 1) / kBS;
+      nblk = visible_blocks(c, p.win.window, p.win.sinks).n;
     }
     const int nfull = nblk / p.split_blocks, tail = nblk % p.split_blocks;
     if (tail > 0) atomicAdd(&tail_at[tail], p.num_kv_heads);
@@ -275,7 +283,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   __syncthreads();
   for (int t = threadIdx.x; t < p.num_tokens; t += blockDim.x) {
     const int c = p.tok_ctx[t];  // written by this thread above
-    const int nblk = (c + kBS - 1) / kBS, nfull = nblk / p.split_blocks, tail = nblk % p.split_blocks;
+    const int nblk = visible_blocks(c, p.win.window, p.win.sinks).n, nfull = nblk / p.split_blocks;
+    const int tail = nblk % p.split_blocks;
     if (tail > 0) {
       const int at = atomicAdd(&tail_at[tail], p.num_kv_heads), row = p.tok_row[t];
       for (int g = 0; g < p.num_kv_heads; ++g) p.tasks[at + g] = make_int4(t, g | (nfull << 8), row, c);
@@ -332,7 +341,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       if (b < p.num_seqs) {
         const int q_len = __ldg(p.qsl + b + 1) - __ldg(p.qsl + b), ctx = __ldg(p.context_lens + b);
         if (p.prefill_min_qlen > 0 && q_len >= p.prefill_min_qlen && row_meta_ok(q_len, ctx, p.max_ctx))
-          nb = (ctx + kBS - 1) / kBS;
+          nb = row_blocks(ctx, q_len, p.win).n;
       }
       int total = 0;
       const int off = nsh + block_exclusive_scan(nb, warp_sums, &total);
@@ -372,9 +381,12 @@ struct WsLayout {
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-static WsLayout ws_layout(const pkv_config& c, int num_seqs, int num_tokens, int max_blocks) {
+static WsLayout ws_layout(const pkv_config& c, int num_seqs, int num_tokens, int max_blocks, const KeyWindow& win = KeyWindow()) {
   WsLayout w;
-  w.max_splits = (max_blocks + c.split_blocks - 1) / c.split_blocks;
+  // a token sees at most the sinks' blocks and those that a window can touch
+  const int64_t seen = ((int64_t)win.sinks + kBS - 1) / kBS + ((int64_t)win.window + kBS - 2) / kBS + 1;
+  const int tok_blocks = (int)std::min<int64_t>(max_blocks, seen);
+  w.max_splits = (tok_blocks + c.split_blocks - 1) / c.split_blocks;
   w.max_tasks = (int64_t)num_tokens * c.num_kv_heads * w.max_splits;
   const int group = c.num_q_heads / c.num_kv_heads;
   // the tile kernel reads fp16 K/V: on an 8-bit cache it reads the prefill rows' blocks from an fp16 shadow
@@ -433,7 +445,8 @@ static WsLayout ws_layout(const pkv_config& c, int num_seqs, int num_tokens, int
 
 
 static cudaError_t launch_plan(pkv_pool* pool, char* ws, const WsLayout& w, const int32_t* context_lens,
-                               const int32_t* qsl, int num_seqs, int num_tokens, int max_blocks, cudaStream_t s) {
+                               const int32_t* qsl, int num_seqs, int num_tokens, int max_blocks, cudaStream_t s,
+                               const KeyWindow& win = KeyWindow()) {
   const pkv_config& c = pool->cfg;
   PlanParams p;
   p.context_lens = context_lens;
@@ -458,6 +471,7 @@ static cudaError_t launch_plan(pkv_pool* pool, char* ws, const WsLayout& w, cons
   p.pf_base = w.shadow_blocks > 0 ? reinterpret_cast<int32_t*>(ws + w.pf_base) : nullptr;
   p.hdr = reinterpret_cast<WsHeader*>(ws + w.hdr);
   p.err = pool->dev_error;
+  p.win = win;
   return launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, p);
 }
 
@@ -482,6 +496,8 @@ struct DequantParams {
   int32_t* err;
   int64_t shadow_blocks;
   int num_seqs, max_blocks, num_kv_heads, num_blocks;
+  const int32_t* qsl;
+  KeyWindow win;
 };
 
 constexpr int kDequantMaxRows = 48 * 1024 - 1;  // pf_base staged in shared memory: (rows + 1) x 4 bytes <= 192 KB
@@ -506,8 +522,10 @@ __global__ void __launch_bounds__(256) dequant_prefill_rows_kernel(const Dequant
       const int mid = (lo + hi + 1) >> 1;
       if (sbase[mid] <= sb) lo = mid; else hi = mid - 1;
     }
-    const int b = lo, j = sb - sbase[b];
+    const int b = lo;
     const int ctx = __ldg(p.context_lens + b);
+    const int q_len = __ldg(p.qsl + b + 1) - __ldg(p.qsl + b);
+    const int j = row_blocks(ctx, q_len, p.win).row_unit(sb - sbase[b]);
     const int id = __ldg(p.block_tables + (int64_t)b * p.max_blocks + j);
     const bool ok = id >= 0 && id < p.num_blocks;
     if (threadIdx.x == 0) {
@@ -554,7 +572,7 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
                                    const int32_t* context_lens, const int32_t* qsl, int max_blocks, int num_seqs,
                                    int num_tokens, void* out, char* ws,
                                    const WsLayout& w, cudaStream_t s, int* launches,
-                                   const FusedAppend& fa = FusedAppend()) {
+                                   const FusedAppend& fa = FusedAppend(), const KeyWindow& win = KeyWindow()) {
   const pkv_config& c = pool->cfg;
   DecodeParams p;
   p.kv_map = c.kv_dtype == PKV_KV_E4M3 ? pool->kv_map : pool->run_map;  // fp16: one copy per run
@@ -590,6 +608,8 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
   p.max_splits = w.max_splits;
   p.max_tasks = (int)w.max_tasks;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.head_dim));
+  p.win = win;
+  const bool windowed = win.window != kNoWindow;
   const int group = c.num_q_heads / c.num_kv_heads;
   // Prefill rows exist only if some row has at least prefill_min_qlen new tokens.  Their tile kernel goes
   // first; the decode kernel follows in its tail (late_wait).
@@ -623,6 +643,8 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
       dq.max_blocks = max_blocks;
       dq.num_kv_heads = c.num_kv_heads;
       dq.num_blocks = c.num_blocks;
+      dq.qsl = qsl;
+      dq.win = win;
       e = c.head_dim == 64    ? launch_dequant<64>(dq, pool->num_sms, s)
           : c.head_dim == 128 ? launch_dequant<128>(dq, pool->num_sms, s)
                               : launch_dequant<256>(dq, pool->num_sms, s);
@@ -649,12 +671,16 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
     a.head_dim = c.head_dim;
     a.num_sms = pool->num_sms;
     a.max_items = 2 * w.max_items;
-    e = launch_prefill(a, s);
+    a.win = win;
+    e = windowed ? launch_prefill_window(a, s) : launch_prefill(a, s);
     if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
     *launches += 1;
     p.late_wait = 1;
   }
-  if (f8) {
+  if (windowed) {
+    e = f8 ? launch_decode_window_e4m3(c.head_dim, group, p, pool->num_sms, w.max_tasks, s)
+           : launch_decode_window(c.head_dim, group, p, pool->num_sms, w.max_tasks, s);
+  } else if (f8) {
     e = launch_decode_e4m3(c.head_dim, group, p, pool->num_sms, w.max_tasks, s);
   } else {
     switch (c.head_dim) {
@@ -668,7 +694,7 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
   *launches += 1;
   if (w.max_splits > kFusedMergeSplits) {
     MergeParams m{p.part_o, p.part_ml, reinterpret_cast<const int32_t*>(ws + w.tok_ctx), p.out, c.num_q_heads, c.num_kv_heads, group, c.split_blocks,
-                  w.max_splits};
+                  w.max_splits, win};
     const dim3 grid(num_tokens, c.num_kv_heads, (group * c.head_dim) / 32);
     switch (c.head_dim) {
       case 64: e = launch_pdl(merge_kernel<64>, grid, dim3(256), 0, s, m); break;
@@ -709,11 +735,11 @@ static pkv_status check_common(pkv_pool* pool, const int32_t* context_lens, cons
 }
 
 static pkv_status check_workspace(pkv_pool* pool, void* workspace, size_t ws_bytes, int32_t num_seqs, int32_t num_tokens,
-                                  int32_t max_blocks) {
+                                  int32_t max_blocks, const KeyWindow& win) {
   if (num_tokens > 0 && !workspace) return fail(PKV_ERR_INVALID_ARG, "workspace must be non-NULL");
   if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
     return fail(PKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  const WsLayout w = ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks);
+  const WsLayout w = ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks, win);
   if (ws_bytes < w.total)
     return fail(PKV_ERR_INVALID_ARG, "workspace too small: need " + std::to_string(w.total) + " bytes");
   return PKV_OK;
@@ -732,6 +758,12 @@ static const PlanKey* find_plan(const pkv_pool* pool, const void* workspace) {
   for (auto it = pool->plans.rbegin(); it != pool->plans.rend(); ++it)
     if (it->workspace == workspace) return &*it;
   return nullptr;
+}
+
+// The window of the plan on `workspace` (none without a plan: the call is refused later).
+static KeyWindow planned_window(const pkv_pool* pool, const void* workspace) {
+  const PlanKey* k = pool ? find_plan(pool, workspace) : nullptr;
+  return k ? KeyWindow{k->window, k->sinks} : KeyWindow();
 }
 
 static void forget_plan(pkv_pool* pool, const void* workspace) {
@@ -787,32 +819,57 @@ static pkv_status prepare_prefill_shadow(pkv_pool* pool, char* ws, const WsLayou
   return PKV_OK;
 }
 
-extern "C" pkv_status pkv_attention_plan(pkv_pool* pool, const int32_t* context_lens, const int32_t* query_start_loc,
-                                         int32_t num_seqs, int32_t num_tokens, int32_t max_blocks_per_seq,
-                                         void* workspace, size_t workspace_bytes, void* stream) {
-  clear_error();
+static pkv_status plan_pass(pkv_pool* pool, const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+                            int32_t num_tokens, int32_t max_blocks_per_seq, const KeyWindow& win, void* workspace,
+                            size_t workspace_bytes, void* stream) {
   pkv_status st = check_common(pool, context_lens, query_start_loc, num_seqs, num_tokens, max_blocks_per_seq);
-  if (st == PKV_OK) st = check_workspace(pool, workspace, workspace_bytes, num_seqs, num_tokens, max_blocks_per_seq);
+  if (st == PKV_OK) st = check_workspace(pool, workspace, workspace_bytes, num_seqs, num_tokens, max_blocks_per_seq, win);
   MetaCheck mc;
   if (st == PKV_OK) st = validate_metadata(pool, nullptr, max_blocks_per_seq, context_lens, query_start_loc, num_seqs,
                                            num_tokens, nullptr, stream, &mc);
   if (st != PKV_OK) return st;
   pool->last_launches = 0;
   forget_plan(pool, workspace);
-  PlanKey key{workspace, context_lens, query_start_loc, num_seqs, num_tokens, max_blocks_per_seq, mc.ran, mc.sum};
+  PlanKey key{workspace, context_lens, query_start_loc, num_seqs, num_tokens, max_blocks_per_seq, mc.ran, mc.sum,
+              win.window, win.sinks};
   if (num_tokens == 0) {
     remember_plan(pool, key);
     return PKV_OK;
   }
-  const WsLayout w = ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks_per_seq);
+  const WsLayout w = ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks_per_seq, win);
   st = prepare_prefill_shadow(pool, static_cast<char*>(workspace), w, num_seqs, num_tokens);
   if (st != PKV_OK) return st;
   cudaError_t e = launch_plan(pool, static_cast<char*>(workspace), w, context_lens, query_start_loc, num_seqs,
-                              num_tokens, max_blocks_per_seq, (cudaStream_t)stream);
+                              num_tokens, max_blocks_per_seq, (cudaStream_t)stream, win);
   if (e != cudaSuccess) return cuda_fail(e, "plan launch");
   remember_plan(pool, key);
   pool->last_launches = 1;
   return PKV_OK;
+}
+
+extern "C" pkv_status pkv_attention_plan(pkv_pool* pool, const int32_t* context_lens, const int32_t* query_start_loc,
+                                         int32_t num_seqs, int32_t num_tokens, int32_t max_blocks_per_seq,
+                                         void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  return plan_pass(pool, context_lens, query_start_loc, num_seqs, num_tokens, max_blocks_per_seq, KeyWindow(), workspace,
+                   workspace_bytes, stream);
+}
+
+extern "C" size_t pkv_attention_window_workspace_bytes(const pkv_pool* pool, int32_t num_seqs, int32_t num_tokens,
+                                                       int32_t max_blocks_per_seq, int32_t window, int32_t sinks) {
+  if (!pool || num_seqs < 0 || num_tokens < 0 || max_blocks_per_seq < 1 || window < 1 || sinks < 0) return 0;
+  return ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks_per_seq, KeyWindow{window, sinks}).total;
+}
+
+extern "C" pkv_status pkv_attention_window_plan(pkv_pool* pool, const int32_t* context_lens,
+                                                const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                                                int32_t max_blocks_per_seq, int32_t window, int32_t sinks,
+                                                void* workspace, size_t workspace_bytes, void* stream) {
+  clear_error();
+  if (window < 1) return fail(PKV_ERR_INVALID_ARG, "window must be >= 1");
+  if (sinks < 0) return fail(PKV_ERR_INVALID_ARG, "sinks must be >= 0");
+  return plan_pass(pool, context_lens, query_start_loc, num_seqs, num_tokens, max_blocks_per_seq, KeyWindow{window, sinks},
+                   workspace, workspace_bytes, stream);
 }
 
 extern "C" pkv_status pkv_attention(pkv_pool* pool, int32_t layer, const void* q, const int32_t* block_tables,
@@ -821,7 +878,8 @@ extern "C" pkv_status pkv_attention(pkv_pool* pool, int32_t layer, const void* q
                                     void* workspace, size_t workspace_bytes, void* stream) {
   clear_error();
   pkv_status st = check_common(pool, context_lens, query_start_loc, num_seqs, num_tokens, max_blocks_per_seq);
-  if (st == PKV_OK) st = check_workspace(pool, workspace, workspace_bytes, num_seqs, num_tokens, max_blocks_per_seq);
+  const KeyWindow win = planned_window(pool, workspace);
+  if (st == PKV_OK) st = check_workspace(pool, workspace, workspace_bytes, num_seqs, num_tokens, max_blocks_per_seq, win);
   if (st != PKV_OK) return st;
   pool->last_launches = 0;
   if (layer < 0 || layer >= pool->cfg.num_layers) return fail(PKV_ERR_OUT_OF_RANGE, "layer out of range");
@@ -829,16 +887,16 @@ extern "C" pkv_status pkv_attention(pkv_pool* pool, int32_t layer, const void* q
   st = check_io(q, out, block_tables);
   MetaCheck mc;
   if (st == PKV_OK) st = validate_metadata(pool, block_tables, max_blocks_per_seq, context_lens, query_start_loc,
-                                           num_seqs, num_tokens, nullptr, stream, &mc);
+                                           num_seqs, num_tokens, nullptr, stream, &mc, win.window, win.sinks);
   if (st == PKV_OK) st = check_plan(pool, workspace, context_lens, query_start_loc, num_seqs, num_tokens,
                                     max_blocks_per_seq, mc);
   if (st != PKV_OK) return st;
-  const WsLayout w = ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks_per_seq);
+  const WsLayout w = ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks_per_seq, win);
   st = prepare_prefill_shadow(pool, static_cast<char*>(workspace), w, num_seqs, num_tokens);
   if (st != PKV_OK) return st;
   int launches = 0;
   st = launch_attention(pool, layer, q, block_tables, context_lens, query_start_loc, max_blocks_per_seq, num_seqs, num_tokens, out,
-                        static_cast<char*>(workspace), w, (cudaStream_t)stream, &launches);
+                        static_cast<char*>(workspace), w, (cudaStream_t)stream, &launches, FusedAppend(), win);
   pool->last_launches = launches;
   return st;
 }
@@ -857,7 +915,8 @@ extern "C" pkv_status pkv_attention_append(pkv_pool* pool, int32_t layer, const 
                                            void* out, void* workspace, size_t workspace_bytes, void* stream) {
   clear_error();
   pkv_status st = check_common(pool, context_lens, query_start_loc, num_seqs, num_tokens, max_blocks_per_seq);
-  if (st == PKV_OK) st = check_workspace(pool, workspace, workspace_bytes, num_seqs, num_tokens, max_blocks_per_seq);
+  const KeyWindow win = planned_window(pool, workspace);
+  if (st == PKV_OK) st = check_workspace(pool, workspace, workspace_bytes, num_seqs, num_tokens, max_blocks_per_seq, win);
   if (st != PKV_OK) return st;
   pool->last_launches = 0;
   if (layer < 0 || layer >= pool->cfg.num_layers) return fail(PKV_ERR_OUT_OF_RANGE, "layer out of range");
@@ -869,11 +928,11 @@ extern "C" pkv_status pkv_attention_append(pkv_pool* pool, int32_t layer, const 
     return fail(PKV_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
   MetaCheck mc;
   st = validate_metadata(pool, block_tables, max_blocks_per_seq, context_lens, query_start_loc, num_seqs, num_tokens,
-                         slot_mapping, stream, &mc);
+                         slot_mapping, stream, &mc, win.window, win.sinks);
   if (st == PKV_OK) st = check_plan(pool, workspace, context_lens, query_start_loc, num_seqs, num_tokens,
                                     max_blocks_per_seq, mc);
   if (st != PKV_OK) return st;
-  const WsLayout w = ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks_per_seq);
+  const WsLayout w = ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks_per_seq, win);
   st = prepare_prefill_shadow(pool, static_cast<char*>(workspace), w, num_seqs, num_tokens);
   if (st != PKV_OK) return st;
   int launches = 0;
@@ -885,14 +944,14 @@ extern "C" pkv_status pkv_attention_append(pkv_pool* pool, int32_t layer, const 
     if (st != PKV_OK) return st;
     launches = pool->last_launches;
     st = launch_attention(pool, layer, q, block_tables, context_lens, query_start_loc, max_blocks_per_seq, num_seqs, num_tokens,
-                          out, static_cast<char*>(workspace), w, (cudaStream_t)stream, &launches);
+                          out, static_cast<char*>(workspace), w, (cudaStream_t)stream, &launches, FusedAppend(), win);
   } else {
     FusedAppend fa;
     fa.k = k;
     fa.v = v;
     fa.slots = slot_mapping;
     st = launch_attention(pool, layer, q, block_tables, context_lens, query_start_loc, max_blocks_per_seq, num_seqs, num_tokens,
-                          out, static_cast<char*>(workspace), w, (cudaStream_t)stream, &launches, fa);
+                          out, static_cast<char*>(workspace), w, (cudaStream_t)stream, &launches, fa, win);
   }
   pool->last_launches = launches;
   return st;

@@ -30,6 +30,34 @@ __host__ __device__ constexpr int prefill_positions(int group) { return kPrefill
 // next 64 (a 128-key tile's would not fit beside them), and 64-key tiles keep the K/V rings in shared memory.
 __host__ __device__ constexpr int prefill_tile_keys(int head_dim) { return head_dim == 256 ? 64 : kPrefillKeys; }
 
+// What a query at position p sees of its row: every key k <= p with k > p - window, and the row's first `sinks`
+// keys whatever the window.  kNoWindow: all of them.
+constexpr int kNoWindow = 0x7FFFFFFF;
+struct KeyWindow {
+  int window = kNoWindow;
+  int sinks = 0;
+};
+
+// First key of the window of the query that sees `ctx` keys without one (position ctx - 1).
+__host__ __device__ constexpr int window_low(int ctx, int window) { return ctx > window ? ctx - window : 0; }
+
+// The units (blocks of 16 keys, or K/V tiles) that queries with windows from key `low` on and `kend` keys in all see:
+// the first `head` ones (the sinks'), then those from unit head + skip on; n of them.  Unit j of the n is unit
+// j of the row below `head` and unit j + skip above; without a gap between sinks and window skip is 0.
+struct VisibleUnits {
+  int head, skip, n;
+  __host__ __device__ int row_unit(int j) const { return j < head ? j : j + skip; }
+};
+__host__ __device__ constexpr VisibleUnits visible_units(int kend, int low, int sinks, int unit) {
+  const int all = (kend + unit - 1) / unit, first = low / unit;
+  const int head = ((sinks < kend ? sinks : kend) + unit - 1) / unit;
+  const int skip = first > head ? first - head : 0;
+  return VisibleUnits{head, skip, all - skip};
+}
+__host__ __device__ constexpr VisibleUnits visible_blocks(int ctx, int window, int sinks) {
+  return visible_units(ctx, window_low(ctx, window), sinks, kBS);
+}
+
 struct WsHeader {
   int32_t n_tasks;   // decode tasks of the pass
   int32_t work;      // dynamic decode tasks handed out so far (each CTA's first two are static)
@@ -68,10 +96,13 @@ struct PrefillArgs {
   int max_blocks, num_q_heads, num_kv_heads, num_blocks, head_dim;
   int num_sms;
   int64_t max_items;
+  KeyWindow win;
 };
 
 // Launch the prefill tile kernel for one layer (programmatic dependent launch on `stream`).
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
+// The same with a.win's window (its instances live in prefill_window.cu).
+cudaError_t launch_prefill_window(const PrefillArgs& a, cudaStream_t stream);
 // Whether the tile kernel serves this head shape (otherwise every row takes the decode path).
 bool prefill_supported(int head_dim, int group);
 // Query positions per prefill item (the Q tiles of one item share their K/V tiles).

@@ -133,7 +133,16 @@ struct DecodeParams {
   int max_splits;
   int max_tasks;     // entries of the task list (loads stay below it; n_tasks of them are this pass's)
   float scale_log2;  // log2(e) / sqrt(head_dim)
+  KeyWindow win;     // windowed instances (W): what a token sees of its context
 };
+
+// A windowed instance walks a token's visible blocks only: a split is `split_blocks` consecutive ones of them, and a
+// block's place in the row follows from the token's context (visible_blocks).
+template <bool W>
+__device__ __forceinline__ VisibleUnits token_blocks(const DecodeParams& p, int ctx) {
+  if constexpr (W) return visible_blocks(ctx, p.win.window, p.win.sinks);
+  return VisibleUnits{0, 0, (ctx + kBS - 1) / kBS};
+}
 
 // Byte offset of 16-byte chunk c (8 dims) of key row r inside a ring slot written by 64-value TMA boxes
 // with the 128-byte swizzle: box c / 8, row r at 128 bytes, chunk slot (c % 8) XOR (r % 8).
@@ -218,6 +227,9 @@ struct TaskView {
   int nbw;          // blocks of the split dealt to this warp: task-local blocks bw, bw + 4, ...
   int bw;
   int nlean;        // the warp's leading blocks that are full and hold no row of this pass (see Streamer)
+  int nhead;        // W: the warp's blocks ahead of the lean ones (the sinks', and the window's first)
+  int low;          // W: the window's first key
+  VisibleUnits vis; // W: which blocks of the row the token sees
   const int* ids;   // shared memory: the split's block ids
 };
 
@@ -231,7 +243,7 @@ __device__ __forceinline__ int warp_blocks(int nb, int bw) { return nb > bw ? (n
 // (scattered 4 KB runs): one issuing thread per CTA cannot keep HBM busy, many independent issuers per
 // SM can -- hence every streaming warp issues its own copies.
 // ---------------------------------------------------------------------------------------------------
-template <int D, int G, int KV>
+template <int D, int G, int KV, bool W>
 struct Streamer {
   using T = DecodeTraits<D, G, KV>;
   const DecodeParams& p;
@@ -286,8 +298,8 @@ struct Streamer {
     v.row = rec.z;
     v.ctx = rec.w;
     v.nst = e->nst;
-    const int nblk = (v.ctx + kBS - 1) / kBS;
-    v.nsplit = (nblk + p.split_blocks - 1) / p.split_blocks;
+    v.vis = token_blocks<W>(p, v.ctx);
+    v.nsplit = (v.vis.n + p.split_blocks - 1) / p.split_blocks;
     v.bw = (warp - e->rot) & 3;
     v.nbw = v.t >= 0 ? warp_blocks(e->nb, v.bw) : 0;
     v.ids = e->ids;
@@ -296,23 +308,40 @@ struct Streamer {
     // holds without the fused append, so both calls pair the same blocks and give the same bits.  Blocks rise
     // with j, so the lean ones are the warp's first nlean.
     const int from = min(v.nst, v.ctx);
-    const int first = v.s * p.split_blocks + v.bw;  // absolute index of the warp's block 0
-    const int nfull = from / kBS - first;             // blocks first, first + NW, ... below from / 16
+    const int first = v.s * p.split_blocks + v.bw;  // visible index of the warp's block 0 (unwindowed: its block of the row)
+    const int nfull = from / kBS - (W ? v.vis.skip : 0) - first;  // blocks first, first + NW, ... below from / 16
     v.nlean = (!T::PAIRS || nfull <= 0) ? 0 : min(v.nbw, (nfull + T::NW - 1) / T::NW);
+    v.nhead = 0;
+    if constexpr (W) {
+      // Lean blocks lie inside the window: from the first block that starts in it (a window that holds the whole
+      // context has no block ahead of them, and gives the unwindowed kernel's bits).
+      v.low = window_low(v.ctx, p.win.window);
+      const int inside = v.low > 0 ? (v.low + kBS - 1) / kBS - v.vis.skip - first : 0;
+      v.nhead = inside <= 0 ? 0 : min(v.nbw, (inside + T::NW - 1) / T::NW);
+      v.nlean = max(0, v.nlean - v.nhead);
+    }
   }
   static __device__ __forceinline__ int runs(const TaskView& v) { return v.t >= 0 ? 2 * v.nbw : 0; }
   __device__ __forceinline__ int block_pos(const TaskView& v, int j) const {
-    return (v.s * p.split_blocks + v.bw + T::NW * j) * kBS;
+    const int b = v.s * p.split_blocks + v.bw + T::NW * j;
+    return (W ? v.vis.row_unit(b) : b) * kBS;
   }
   // Run r of the warp's stream within a task: the lean blocks go in pairs, K of both then V of both; the rest
   // (an odd lean block, then the blocks holding the context's end or this pass's rows) one by one, K then V.
+  // A windowed task's blocks ahead of the lean ones come first, one by one.
   static __device__ __forceinline__ void run_of(const TaskView& v, int r, int& j, int& isv) {
-    const int pr = 4 * (v.nlean >> 1);
+    const int pr = 4 * (v.nlean >> 1), h = W ? v.nhead : 0;
+    if (W && r < 2 * h) {
+      j = r >> 1;
+      isv = r & 1;
+      return;
+    }
+    r -= 2 * h;
     if (r < pr) {
-      j = 2 * (r >> 2) + (r & 1);
+      j = h + 2 * (r >> 2) + (r & 1);
       isv = (r >> 1) & 1;
     } else {
-      j = 2 * (v.nlean >> 1) + ((r - pr) >> 1);
+      j = h + 2 * (v.nlean >> 1) + ((r - pr) >> 1);
       isv = (r - pr) & 1;
     }
   }
@@ -496,8 +525,8 @@ struct Streamer {
   }
 };
 
-template <int D, int G, int KV>
-__device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeSmem<D, G, KV>& sm, Streamer<D, G, KV>& w) {
+template <int D, int G, int KV, bool W>
+__device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeSmem<D, G, KV>& sm, Streamer<D, G, KV, W>& w) {
   using T = DecodeTraits<D, G, KV>;
   const int lane = w.lane, warp = w.warp;
   const int qh = lane >> 2;        // head whose q this lane feeds to the MMA (B operand column); key row too
@@ -539,9 +568,12 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
 
       // ---- the lean blocks, two at a time: both blocks' scores, one softmax step for the pair (one max
       // reduction, one rescale of O), then both blocks' products.  Their runs sit in the ring in that order. ----
+      // (W: first the blocks ahead of the lean ones, by the code for single blocks: stage 0.)
       int j = 0;
+      for (int stage = W && T::PAIRS ? 0 : 1; stage < 2; ++stage) {
+      const int jend = W && T::PAIRS && stage == 0 ? d.nhead : d.nbw;
       if constexpr (T::PAIRS) {
-        for (; j + 1 < d.nlean && w.ok; j += 2) {
+        for (; stage == 1 && j + 1 < (W ? d.nhead : 0) + d.nlean && w.ok; j += 2) {
           float x[2][4];            // scaled scores: [block][key qh head h0, key qh h0 + 1, key qh + 8 h0, .. h0 + 1]
           uint32_t evb[2][2];       // 8-bit: value scale bytes of keys qh, qh + 8
 #pragma unroll
@@ -652,7 +684,7 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
       }
       // ---- the rest one by one: an odd lean block, then the blocks holding the context's end or rows of
       // this pass (masking, the fused append's rows from the inputs, the token's own write to the cache) ----
-      for (; j < d.nbw && w.ok; ++j) {
+      for (; j < jend && w.ok; ++j) {
         const int bpos = w.block_pos(d, j);  // the block's first position
         const int ntok = min(kBS, d.ctx - bpos);
         // fused append: positions ov0 .. bpos + ntok - 1 of the block are this pass's tokens; their rows
@@ -784,7 +816,13 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
           w.release_run();
         }
         // ---- online softmax (log2 domain); the lane holds keys qh, qh + 8 for heads h0, h0 + 1 ----
-        const bool v0 = qh < ntok, v1 = qh + 8 < ntok;
+        bool v0 = qh < ntok, v1 = qh + 8 < ntok;
+        // W: the keys of this block that lie between the sinks and the window
+        const bool gap = W && bpos < d.low;
+        if constexpr (W) {
+          v0 = v0 && (bpos + qh >= d.low || bpos + qh < p.win.sinks);
+          v1 = v1 && (bpos + qh + 8 >= d.low || bpos + qh + 8 < p.win.sinks);
+        }
         const float s0 = v0 ? sc[0] * ks0 : -INFINITY;  // key qh,     head h0
         const float s1 = v0 ? sc[1] * ks0 : -INFINITY;  // key qh,     head h0 + 1
         const float s2 = v1 ? sc[2] * ks1 : -INFINITY;  // key qh + 8, head h0
@@ -844,6 +882,14 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
                 quant_rows(vs_base, p.v_in, true, nullptr, 0);
               }
             }
+            if (gap) {  // the gap's rows may hold anything too (those of this pass's tokens among them)
+              const int g0 = max(0, p.win.sinks - bpos), g1 = min(kBS, d.low - bpos);
+              for (int idx = lane; idx < (g1 - g0) * (D / 16); idx += 32)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vs_base + swz8<D>(g0 + idx / (D / 16), idx % (D / 16))),
+                             "r"(0)
+                             : "memory");
+              __syncwarp();
+            }
             // 16 keys x 32 dims per transposing ldmatrix: a lane's word holds keys 2t, 2t + 1 at dims 2g, 2g + 1;
             // regrouped by dim, the even dims feed one MMA (o[2i]) and the odd dims another (o[2i + 1])
 #pragma unroll
@@ -865,6 +911,14 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
               __syncwarp();
             }
             if (nov > 0) override_rows(vs_base, p.v_in, pv);
+            if (gap) {
+              const int g0 = max(0, p.win.sinks - bpos), g1 = min(kBS, d.low - bpos);
+              for (int idx = lane; idx < (g1 - g0) * (D / 8); idx += 32)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vs_base + swz(g0 + idx / (D / 8), idx % (D / 8))),
+                             "r"(0)
+                             : "memory");
+              __syncwarp();
+            }
 #pragma unroll
             for (int mt = 0; mt < T::MT; ++mt) {
               uint32_t a[4];
@@ -872,7 +926,7 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
               dev::mma_16816(o[mt], a, pb0, pb1);
             }
           }
-          if (ntok < kBS || nov > 0) dev::fence_proxy_async_smem();  // generic writes precede the next TMA write
+          if (ntok < kBS || nov > 0 || gap) dev::fence_proxy_async_smem();  // generic writes precede the next TMA write
           w.release_run();
         }
         w.prefetch_q();  // the next task's q, once the scheduler has published it
@@ -928,6 +982,7 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
             }
           }
         }
+      }
       }
     }
     if (!w.ok) break;
@@ -986,7 +1041,7 @@ __device__ __forceinline__ void frag_coord(int lane, int r, int& dim, int& head)
 // greedy longest-first schedule, which ends the launch more evenly than pairing two static tasks per CTA
 // (2 % on the 256-row decode).  A CTA holds one task it has not started.
 // ---------------------------------------------------------------------------------------------------
-template <int D, int G, int KV>
+template <int D, int G, int KV, bool W>
 struct Scheduler {
   using T = DecodeTraits<D, G, KV>;
   const DecodeParams& p;
@@ -1014,9 +1069,11 @@ struct Scheduler {
       id[j] = 0;
       q0[j] = 0;
       if (rec[j].x >= 0) {
-        const int s = rec[j].y >> 8, nblk = (rec[j].w + kBS - 1) / kBS;
-        if (lane < min(p.split_blocks, nblk - s * p.split_blocks))
-          id[j] = __ldcg(p.block_tables + (int64_t)rec[j].z * p.max_blocks + s * p.split_blocks + lane);
+        const int s = rec[j].y >> 8;
+        const VisibleUnits vis = token_blocks<W>(p, rec[j].w);
+        const int b = s * p.split_blocks + lane;  // the split's block `lane` among the visible ones
+        if (lane < min(p.split_blocks, vis.n - s * p.split_blocks))
+          id[j] = __ldcg(p.block_tables + (int64_t)rec[j].z * p.max_blocks + (W ? vis.row_unit(b) : b));
         q0[j] = __ldcg(p.qsl + rec[j].z);
       }
     }
@@ -1028,7 +1085,7 @@ struct Scheduler {
       int nb = 0, nst = 0, rot = 0;
       if (rec[j].x >= 0) {
         const int g = rec[j].y & 0xFF, s = rec[j].y >> 8, ctx = rec[j].w;
-        nb = min(p.split_blocks, (ctx + kBS - 1) / kBS - s * p.split_blocks);
+        nb = min(p.split_blocks, token_blocks<W>(p, ctx).n - s * p.split_blocks);
         if (lane < nb) {
           int v = id[j];
           if (v < 0 || v >= p.num_blocks) {
@@ -1051,7 +1108,7 @@ struct Scheduler {
       // inputs (and its slot) in the middle of its last block, where the load's latency is exposed; bring
       // them into L2 now, a task or more before they are needed.
       if (p.k_in != nullptr && rec[j].x >= 0 && nb > 0 &&
-          (rec[j].y >> 8) == ((rec[j].w + kBS - 1) / kBS - 1) / p.split_blocks) {
+          (rec[j].y >> 8) == (token_blocks<W>(p, rec[j].w).n - 1) / p.split_blocks) {
         constexpr int LINES = D * 2 / 128;  // 128-byte lines of one row
         const size_t row = ((size_t)rec[j].x * p.num_kv_heads + (rec[j].y & 0xFF)) * D;
         if (lane < LINES) dev::prefetch_l2(p.k_in + row + lane * 64);
@@ -1138,7 +1195,7 @@ __device__ __forceinline__ void fold_weights(float& M, float& L, float2 ml, floa
 }
 __device__ __forceinline__ float fold_value(float acc, float a, float v, float f) { return fmaf(v, f, acc * a); }
 
-template <int D, int G, int KV>
+template <int D, int G, int KV, bool W>
 struct Combiner {
   using T = DecodeTraits<D, G, KV>;
   static constexpr int NG = G * D / 4;         // groups of 4 consecutive dims of one head (the G heads)
@@ -1307,8 +1364,7 @@ struct Combiner {
       if (rec.x < 0) break;
       if (lane == 0) dev::mbar_arrive(&sm.qempty[k % T::QD]);
       const int t = rec.x, g = rec.y & 0xFF, s = rec.y >> 8, ctx = rec.w;
-      const int nblk = (ctx + kBS - 1) / kBS;
-      const int nsplit = (nblk + p.split_blocks - 1) / p.split_blocks;
+      const int nsplit = (token_blocks<W>(p, ctx).n + p.split_blocks - 1) / p.split_blocks;
       const int tg = t * p.num_kv_heads + g;
       const bool multi = nsplit > 1 && nsplit <= kFusedMergeSplits;
       int done_lane0 = 0;  // splits of the token counted so far
@@ -1441,7 +1497,7 @@ struct Combiner {
   }
 };
 
-template <int D, int G, int KV>
+template <int D, int G, int KV, bool W>
 __global__ void __launch_bounds__(DecodeTraits<D, G, KV>::NTHREADS, DecodeTraits<D, G, KV>::MINB)
 decode_kernel(const __grid_constant__ DecodeParams p) {
   using T = DecodeTraits<D, G, KV>;
@@ -1474,8 +1530,8 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   // final before the plan; they are read through L2, never a possibly stale L1 line.  So are the first K/V
   // runs wherever no appended token can be in them.  q, the task counter and the partials are touched only
   // after the wait.
-  Streamer<D, G, KV> w(p, sm, warp, lane);
-  Scheduler<D, G, KV> sch(p, sm, lane);
+  Streamer<D, G, KV, W> w(p, sm, warp, lane);
+  Scheduler<D, G, KV, W> sch(p, sm, lane);
   if (warp < T::NW) w.prologue(); else if (warp == T::NW + 1) sch.prologue();
   if (!p.late_wait) dev::griddep_wait();
   dev::griddep_launch_dependents();
@@ -1487,10 +1543,10 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   __syncwarp();
   const bool poisoned = __syncthreads_or(pz);
   if (warp < T::NW) {
-    if (!poisoned) stream_loop<D, G, KV>(p, sm, w);
+    if (!poisoned) stream_loop<D, G, KV, W>(p, sm, w);
     w.drain();
   } else if (!poisoned) {
-    if (warp == T::NW) Combiner<D, G, KV>(p, sm, lane).run();
+    if (warp == T::NW) Combiner<D, G, KV, W>(p, sm, lane).run();
     else sch.run();
   }
   // The last CTA out resets the task counter for the next launch on this plan.  No fence on either side: a
@@ -1508,33 +1564,33 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   if (p.late_wait) dev::griddep_wait();  // complete only after the prefill kernel ahead of it
 }
 
-template <int D, int G, int KV>
+template <int D, int G, int KV, bool W = false>
 static cudaError_t launch_decode(const DecodeParams& p, int num_sms, int64_t max_tasks, cudaStream_t stream) {
   using T = DecodeTraits<D, G, KV>;
   static int per_sm = 0;
   if (per_sm == 0) {
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, G, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, G, KV, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
     if (e != cudaSuccess) return e;
     int n = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<D, G, KV>, T::NTHREADS, T::SMEM);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<D, G, KV, W>, T::NTHREADS, T::SMEM);
     if (e != cudaSuccess) return e;
     per_sm = n > 0 ? n : 1;
   }
   int64_t grid = (int64_t)num_sms * per_sm;  // persistent: one CTA per resident slot, one task at a time
   if (grid > max_tasks) grid = max_tasks;
   if (grid < 1) grid = 1;
-  return launch_pdl(decode_kernel<D, G, KV>, dim3((unsigned)grid), dim3(T::NTHREADS), T::SMEM, stream, p);
+  return launch_pdl(decode_kernel<D, G, KV, W>, dim3((unsigned)grid), dim3(T::NTHREADS), T::SMEM, stream, p);
 }
 
-template <int D, int KV>
+template <int D, int KV, bool W = false>
 static cudaError_t launch_decode_g(int group, const DecodeParams& p, int num_sms, int64_t max_tasks,
                                    cudaStream_t stream) {
   switch (group) {
-    case 1: return launch_decode<D, 1, KV>(p, num_sms, max_tasks, stream);
-    case 2: return launch_decode<D, 2, KV>(p, num_sms, max_tasks, stream);
-    case 4: return launch_decode<D, 4, KV>(p, num_sms, max_tasks, stream);
-    case 6: return launch_decode<D, 6, KV>(p, num_sms, max_tasks, stream);
-    case 8: return launch_decode<D, 8, KV>(p, num_sms, max_tasks, stream);
+    case 1: return launch_decode<D, 1, KV, W>(p, num_sms, max_tasks, stream);
+    case 2: return launch_decode<D, 2, KV, W>(p, num_sms, max_tasks, stream);
+    case 4: return launch_decode<D, 4, KV, W>(p, num_sms, max_tasks, stream);
+    case 6: return launch_decode<D, 6, KV, W>(p, num_sms, max_tasks, stream);
+    case 8: return launch_decode<D, 8, KV, W>(p, num_sms, max_tasks, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1542,5 +1598,10 @@ static cudaError_t launch_decode_g(int group, const DecodeParams& p, int num_sms
 // The 8-bit cache's instances live in their own translation unit (decode_e4m3.cu).
 cudaError_t launch_decode_e4m3(int head_dim, int group, const DecodeParams& p, int num_sms, int64_t max_tasks,
                                cudaStream_t stream);
+// The windowed instances of both formats in theirs (decode_window.cu, decode_window_e4m3.cu).
+cudaError_t launch_decode_window(int head_dim, int group, const DecodeParams& p, int num_sms, int64_t max_tasks,
+                                 cudaStream_t stream);
+cudaError_t launch_decode_window_e4m3(int head_dim, int group, const DecodeParams& p, int num_sms, int64_t max_tasks,
+                                      cudaStream_t stream);
 
 }  // namespace pkv

@@ -33,6 +33,10 @@ struct PlanKey {
   // Under PKV_VALIDATE=1: a hash of the context_lens and query_start_loc contents the plan was built from.
   bool summed = false;
   uint64_t meta_sum = 0;
+  // The plan's window (pkv_attention_window_plan): the calls on the workspace attend through it.  Without one,
+  // a window longer than any context.
+  int32_t window = 0x7FFFFFFF;
+  int32_t sinks = 0;
 };
 
 // Plans remembered per pool: one per workspace, the most recently planned last.  A plan on a workspace
@@ -80,11 +84,14 @@ pkv_status encode_f16_rows(CUtensorMap* map, void* base, uint64_t rows, int head
 // sub-tiles of 16 rows x 64 values (128-byte swizzle), sub-tile h at 2048 h bytes -- the layout of head_dim / 64
 // boxes of the 2-D map side by side, in one copy.
 pkv_status encode_f16_runs(CUtensorMap* map, void* base, uint64_t rows, int head_dim);
-// The PKV_VALIDATE=1 host check of a call's device metadata (a no-op otherwise); null pointers are skipped.
+// The PKV_VALIDATE=1 host check of a call's device metadata (a no-op otherwise); null pointers are skipped.  Blocks
+// that no new token of their row sees behind `window` and `sinks` are not looked at; with none_ok (the slot mapping,
+// which knows no window) an entry of -1 in front of the row's new tokens passes.
 // When `check` is given and the check ran, it receives a hash of the context_lens and query_start_loc contents.
 pkv_status validate_metadata(const pkv_pool* pool, const int32_t* block_tables, int32_t max_blocks,
                              const int32_t* context_lens, const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
-                             const int64_t* slots, void* stream, MetaCheck* check = nullptr);
+                             const int64_t* slots, void* stream, MetaCheck* check = nullptr,
+                             int32_t window = 0x7FFFFFFF, int32_t sinks = 0, bool none_ok = false);
 }  // namespace pkv
 
 namespace pkv {

@@ -170,7 +170,8 @@ static uint64_t fnv1a_words(uint64_t h, const std::vector<int32_t>& words) {
 
 pkv_status validate_metadata(const pkv_pool* pool, const int32_t* block_tables, int32_t max_blocks,
                              const int32_t* context_lens, const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
-                             const int64_t* slots, void* stream, MetaCheck* check) {
+                             const int64_t* slots, void* stream, MetaCheck* check, int32_t window, int32_t sinks,
+                             bool none_ok) {
   const char* env = std::getenv("PKV_VALIDATE");
   if (!env || std::strcmp(env, "1") != 0 || num_tokens <= 0) return PKV_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -214,6 +215,9 @@ pkv_status validate_metadata(const pkv_pool* pool, const int32_t* block_tables, 
       const int64_t nblk = std::min<int64_t>(((int64_t)ctx[b] + c.block_size - 1) / c.block_size, max_blocks);
       for (int64_t j = 0; j < nblk; ++j) {
         const int32_t id = bt[(size_t)b * max_blocks + j];
+        const int64_t low = qsl ? (int64_t)ctx[b] - (q[b + 1] - q[b]) + 1 - window : 0;  // the first new token's window
+        if ((j + 1) * c.block_size <= low && j * c.block_size >= sinks) continue;
+        if (none_ok && id == -1 && (j + 1) * c.block_size <= (int64_t)ctx[b] - (q[b + 1] - q[b])) continue;
         if (id < 0 || id >= c.num_blocks)
           return fail(PKV_ERR_OUT_OF_RANGE, "PKV_VALIDATE: row " + std::to_string(b) + " block " + std::to_string(j) +
                                                 " is " + std::to_string(id));
@@ -523,7 +527,7 @@ extern "C" pkv_status pkv_slot_mapping(pkv_pool* pool, const int32_t* block_tabl
   if (!block_tables || !context_lens || !query_start_loc || !slot_mapping)
     return fail(PKV_ERR_INVALID_ARG, "metadata pointers must be non-NULL");
   pkv_status vst = validate_metadata(pool, block_tables, max_blocks_per_seq, context_lens, query_start_loc, num_seqs,
-                                     num_tokens, nullptr, stream);
+                                     num_tokens, nullptr, stream, nullptr, 0x7FFFFFFF, 0, /*none_ok=*/true);
   if (vst != PKV_OK) return vst;
   const int threads = 256;
   int blocks = (num_tokens + threads - 1) / threads;

@@ -96,6 +96,8 @@ SIGNATURES = {
     "pkv_append": (ctypes.c_int, [_p, _i32, _p, _p, _p, _i32, _p]),
     "pkv_attention_workspace_bytes": (_sz, [_p, _i32, _i32, _i32]),
     "pkv_attention_plan": (ctypes.c_int, [_p, _p, _p, _i32, _i32, _i32, _p, _sz, _p]),
+    "pkv_attention_window_workspace_bytes": (_sz, [_p, _i32, _i32, _i32, _i32, _i32]),
+    "pkv_attention_window_plan": (ctypes.c_int, [_p, _p, _p, _i32, _i32, _i32, _i32, _i32, _p, _sz, _p]),
     "pkv_attention": (ctypes.c_int, [_p, _i32, _p, _p, _i32, _p, _p, _i32, _i32, _p, _p, _sz, _p]),
     "pkv_attention_noalloc": (ctypes.c_int, [_p, _i32, _p, _p, _i32, _p, _p, _i32, _i32, _p, _p]),
     "pkv_attention_append": (ctypes.c_int, [_p, _i32, _p, _p, _p, _p, _p, _i32, _p, _p, _i32, _i32, _p, _p, _sz,
@@ -221,6 +223,19 @@ def pkv_attention_plan(pool: int, context_lens, query_start_loc, num_seqs: int, 
     _check(load().pkv_attention_plan(pool, _ptr(context_lens), _ptr(query_start_loc), num_seqs, num_tokens,
                                      max_blocks_per_seq, _ptr(workspace), workspace_bytes, _stream(stream)),
            "pkv_attention_plan")
+
+
+def pkv_attention_window_workspace_bytes(pool: int, num_seqs: int, num_tokens: int, max_blocks_per_seq: int, window: int,
+                                         sinks: int) -> int:
+    return load().pkv_attention_window_workspace_bytes(pool, num_seqs, num_tokens, max_blocks_per_seq, window, sinks)
+
+
+def pkv_attention_window_plan(pool: int, context_lens, query_start_loc, num_seqs: int, num_tokens: int,
+                              max_blocks_per_seq: int, window: int, sinks: int, workspace, workspace_bytes: int,
+                              stream=None) -> None:
+    _check(load().pkv_attention_window_plan(pool, _ptr(context_lens), _ptr(query_start_loc), num_seqs, num_tokens,
+                                            max_blocks_per_seq, window, sinks, _ptr(workspace), workspace_bytes,
+                                            _stream(stream)), "pkv_attention_window_plan")
 
 
 def pkv_attention(pool: int, layer: int, q, block_tables, max_blocks_per_seq: int, context_lens, query_start_loc,

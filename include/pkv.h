@@ -239,6 +239,33 @@ pkv_status pkv_attention_append(pkv_pool* pool, int32_t layer, const void* q, co
                                 int32_t num_tokens, void* out, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Attention behind a sliding window, with sinks
+ *
+ * As pkv_attention, but a query at position p sees only the keys k <= p of its row with k > p - window (the last
+ * `window` ones, its own among them) or k < sinks (the row's first tokens, which stay visible however far the
+ * window has moved).  The pages attend a row's whole context; this bounds what a long row reads and
+ * what it must hold.
+ *
+ * Use: size the workspace with pkv_attention_window_workspace_bytes and plan the pass with
+ * pkv_attention_window_plan instead of pkv_attention_plan; then call pkv_attention or pkv_attention_append as ever:
+ * the plan on their workspace carries the window.  A model with windowed and full layers plans two workspaces.
+ * Everything said of pkv_attention_plan holds, and:
+ *   - context_lens still count the whole row, and block tables still have an entry for every 16 tokens.  Entries
+ *     of blocks that no new token of the row sees -- every key at or past the sinks, and in front of
+ *     the window of the row's first new token -- are never read: they may be -1 and the blocks freed.
+ *   - Keys and values that a query does not see have no part in its result, whatever they hold, with one
+ *     exception: in a row of 16 or more new tokens, a non-finite value (of V) that is seen by one of the row's
+ *     queries, or shares a 16-token block with one that is, may reach the row's other queries.
+ *   - A window at least as long as every context gives the bits of a plan without one.
+ * window >= 1, sinks >= 0 (else PKV_ERR_INVALID_ARG, and 0 bytes). */
+size_t pkv_attention_window_workspace_bytes(const pkv_pool* pool, int32_t num_seqs, int32_t num_tokens,
+                                            int32_t max_blocks_per_seq, int32_t window, int32_t sinks);
+pkv_status pkv_attention_window_plan(pkv_pool* pool, const int32_t* context_lens, const int32_t* query_start_loc,
+                                     int32_t num_seqs, int32_t num_tokens, int32_t max_blocks_per_seq,
+                                     int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
 /* Allocation-free attention.  The pages have no counterpart to this call; it exists for callers that
  * cannot give the library a workspace -- an engine whose device memory is already carved up by its
  * own allocator, or code that must not call cudaMalloc (a device-wide synchronisation) mid-pass.

@@ -30,6 +30,7 @@ routine, a closed form, values the pages print, or brute force); see ``tests/tes
 from .attention import attention_row, attention_batch, round_fp16
 from .paging import (kv_bytes_per_token, kv_bytes_for_window, pool_blocks_for_bytes, blocks_for_tokens,
                      max_resident_sequences, cache_bytes, slot_of, slot_mapping_for_batch, append_reference)
+from .window import visible_keys, window_attention_row
 from . import fp8
 from .scheduler import ON_DEMAND, PASS, REQUEST, RESERVE, Request, Scheduler, StepRows
 
@@ -37,5 +38,5 @@ __all__ = [
     "attention_row", "attention_batch", "round_fp16",
     "kv_bytes_per_token", "kv_bytes_for_window", "pool_blocks_for_bytes", "blocks_for_tokens",
     "max_resident_sequences", "cache_bytes", "slot_of", "slot_mapping_for_batch", "append_reference",
-    "fp8", "Request", "Scheduler", "StepRows", "ON_DEMAND", "RESERVE", "PASS", "REQUEST",
+    "visible_keys", "window_attention_row", "fp8", "Request", "Scheduler", "StepRows", "ON_DEMAND", "RESERVE", "PASS", "REQUEST",
 ]
