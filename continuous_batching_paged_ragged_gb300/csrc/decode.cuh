@@ -35,7 +35,7 @@ struct TaskEntry {
   int nst;   // the row's first position appended this pass
   int nb;    // blocks in the split
   int rot;   // block i of the split goes to streaming warp (i + rot) % 4 (a function of the row alone)
-  int pad;
+  int jump;  // windowed: split blocks ahead of the gap behind the sinks (5 bits) | row blocks in the gap << 5
   int ids[kMaxSplitBlocks];  // the split's physical block ids
 };
 
@@ -223,13 +223,11 @@ struct DecodeSmem {
 
 // A task as a streaming warp sees it.
 struct TaskView {
-  int t, g, s, row, ctx, nsplit, nst;
+  int t, g, s, row, ctx, nst;
   int nbw;          // blocks of the split dealt to this warp: task-local blocks bw, bw + 4, ...
   int bw;
   int nlean;        // the warp's leading blocks that are full and hold no row of this pass (see Streamer)
-  int nhead;        // W: the warp's blocks ahead of the lean ones (the sinks', and the window's first)
-  int low;          // W: the window's first key
-  VisibleUnits vis; // W: which blocks of the row the token sees
+  int jump;         // W: TaskEntry::jump
   const int* ids;   // shared memory: the split's block ids
 };
 
@@ -298,8 +296,7 @@ struct Streamer {
     v.row = rec.z;
     v.ctx = rec.w;
     v.nst = e->nst;
-    v.vis = token_blocks<W>(p, v.ctx);
-    v.nsplit = (v.vis.n + p.split_blocks - 1) / p.split_blocks;
+    if constexpr (W) v.jump = e->jump;
     v.bw = (warp - e->rot) & 3;
     v.nbw = v.t >= 0 ? warp_blocks(e->nb, v.bw) : 0;
     v.ids = e->ids;
@@ -309,39 +306,25 @@ struct Streamer {
     // with j, so the lean ones are the warp's first nlean.
     const int from = min(v.nst, v.ctx);
     const int first = v.s * p.split_blocks + v.bw;  // visible index of the warp's block 0 (unwindowed: its block of the row)
-    const int nfull = from / kBS - (W ? v.vis.skip : 0) - first;  // blocks first, first + NW, ... below from / 16
+    const int skip = W ? token_blocks<W>(p, v.ctx).skip : 0;
+    const int nfull = from / kBS - skip - first;  // blocks first, first + NW, ... below from / 16
     v.nlean = (!T::PAIRS || nfull <= 0) ? 0 : min(v.nbw, (nfull + T::NW - 1) / T::NW);
-    v.nhead = 0;
-    if constexpr (W) {
-      // Lean blocks lie inside the window: from the first block that starts in it (a window that holds the whole
-      // context has no block ahead of them, and gives the unwindowed kernel's bits).
-      v.low = window_low(v.ctx, p.win.window);
-      const int inside = v.low > 0 ? (v.low + kBS - 1) / kBS - v.vis.skip - first : 0;
-      v.nhead = inside <= 0 ? 0 : min(v.nbw, (inside + T::NW - 1) / T::NW);
-      v.nlean = max(0, v.nlean - v.nhead);
-    }
   }
   static __device__ __forceinline__ int runs(const TaskView& v) { return v.t >= 0 ? 2 * v.nbw : 0; }
   __device__ __forceinline__ int block_pos(const TaskView& v, int j) const {
-    const int b = v.s * p.split_blocks + v.bw + T::NW * j;
-    return (W ? v.vis.row_unit(b) : b) * kBS;
+    const int b = v.bw + T::NW * j;  // of the split
+    const int gap = W && b >= (v.jump & 31) ? v.jump >> 5 : 0;
+    return (v.s * p.split_blocks + b + gap) * kBS;
   }
   // Run r of the warp's stream within a task: the lean blocks go in pairs, K of both then V of both; the rest
   // (an odd lean block, then the blocks holding the context's end or this pass's rows) one by one, K then V.
-  // A windowed task's blocks ahead of the lean ones come first, one by one.
   static __device__ __forceinline__ void run_of(const TaskView& v, int r, int& j, int& isv) {
-    const int pr = 4 * (v.nlean >> 1), h = W ? v.nhead : 0;
-    if (W && r < 2 * h) {
-      j = r >> 1;
-      isv = r & 1;
-      return;
-    }
-    r -= 2 * h;
+    const int pr = 4 * (v.nlean >> 1);
     if (r < pr) {
-      j = h + 2 * (r >> 2) + (r & 1);
+      j = 2 * (r >> 2) + (r & 1);
       isv = (r >> 1) & 1;
     } else {
-      j = h + 2 * (v.nlean >> 1) + ((r - pr) >> 1);
+      j = 2 * (v.nlean >> 1) + ((r - pr) >> 1);
       isv = (r - pr) & 1;
     }
   }
@@ -534,24 +517,17 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
   int shares = 0;                  // shares this warp has handed to the combiner warp
   float* my_o = sm.sh_o + warp * T::OV * T::SHL;
   float2* my_ml = sm.sh_ml + warp * kHeadsTile;
-  // This lane's ldmatrix row offsets inside a ring slot, hoisted out of the block loop.  fp16: chunk c of a
-  // 64-value box sits at swz(r, c); the chunks 2x + hi of the four k-steps of one box differ only in x, and
-  // the next box adds 2048.  8-bit: one offset per 32 dims of codes.
-  uint32_t koff[4], voff[4];
-  uint32_t k8off[T::F8 ? D / 32 : 1], v8off[T::F8 ? D / 32 : 1];
+  // This lane's ldmatrix address inside a ring slot for the first 16-byte chunk pair of its key row; chunk pair i (16 fp16
+  // dims, or 32 codes) differs from it in two address bits, and the next 64-value box (128 codes) adds 2048.  Slots
+  // are 1024-byte aligned, so the bits can be flipped in the slot's address: two registers hold what a table of
+  // D / 16 offsets did.
+  uint32_t kbase, vbase;
   {
     const int kr = (lane & 7) + ((lane >> 3) & 1) * 8, vmat = lane >> 3, vr = (lane & 7) + ((vmat >> 1) << 3);
-#pragma unroll
-    for (int x4 = 0; x4 < 4; ++x4) {
-      koff[x4] = swz(kr, 2 * x4 + (lane >> 4));
-      voff[x4] = swz(vr, 2 * x4 + (vmat & 1));
-    }
-#pragma unroll
-    for (int i = 0; i < (T::F8 ? D / 32 : 1); ++i) {
-      k8off[i] = T::F8 ? swz8<D>(kr, 2 * i + (lane >> 4)) : 0u;
-      v8off[i] = T::F8 ? swz8<D>(vr, 2 * i + (vmat & 1)) : 0u;
-    }
+    kbase = T::F8 ? swz8<D>(kr, lane >> 4) : swz(kr, lane >> 4);
+    vbase = T::F8 ? swz8<D>(vr, vmat & 1) : swz(vr, vmat & 1);
   }
+  auto chunk = [](uint32_t addr, int i) { return (addr ^ ((i & 3) << 5)) + (i >> 2) * 2048; };
   while (w.ok && w.cur.t >= 0) {
     const TaskView d = w.cur;
     w.task_start();
@@ -561,6 +537,22 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
 #pragma unroll
     for (int mt = 0; mt < T::MT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 
+    // W: the window's first key, and whether the token sees the key at a position of its context
+    const int low = W ? window_low(d.ctx, p.win.window) : 0;
+    auto sees = [&](int pos) { return !W || pos >= low || pos < p.win.sinks; };
+    // W: zeros over the values that lie between the sinks and the window in the block at position bpos, whose run is at
+    // `base` (they may be anything, and 0 * NaN would reach O)
+    auto zero_gap = [&](uint32_t base, int bpos) {
+      constexpr int CPR = T::RUN / (kBS * 16);  // 16-byte chunks per row
+      const int g0 = max(0, p.win.sinks - bpos), g1 = min(kBS, low - bpos);
+      for (int idx = lane; idx < (g1 - g0) * CPR; idx += 32) {
+        const int r = g0 + idx / CPR, c = idx % CPR;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(base + (T::F8 ? swz8<D>(r, c) : swz(r, c))), "r"(0)
+                     : "memory");
+      }
+      __syncwarp();
+    };
+
     if (d.nbw > 0 && w.ok) {
       // ---- q as the MMA B operand (Q^T: k = dims, n = heads) ----
       uint32_t qb[T::KS][2];
@@ -568,12 +560,9 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
 
       // ---- the lean blocks, two at a time: both blocks' scores, one softmax step for the pair (one max
       // reduction, one rescale of O), then both blocks' products.  Their runs sit in the ring in that order. ----
-      // (W: first the blocks ahead of the lean ones, by the code for single blocks: stage 0.)
       int j = 0;
-      for (int stage = W && T::PAIRS ? 0 : 1; stage < 2; ++stage) {
-      const int jend = W && T::PAIRS && stage == 0 ? d.nhead : d.nbw;
       if constexpr (T::PAIRS) {
-        for (; stage == 1 && j + 1 < (W ? d.nhead : 0) + d.nlean && w.ok; j += 2) {
+        for (; j + 1 < d.nlean && w.ok; j += 2) {
           float x[2][4];            // scaled scores: [block][key qh head h0, key qh h0 + 1, key qh + 8 h0, .. h0 + 1]
           uint32_t evb[2][2];       // 8-bit: value scale bytes of keys qh, qh + 8
 #pragma unroll
@@ -591,7 +580,7 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
 #pragma unroll
               for (int i = 0; i < D / 32; ++i) {
                 uint32_t r[4];
-                dev::ldsm_x4(kb + k8off[i], r);
+                dev::ldsm_x4(chunk(kb + kbase, i), r);
                 uint32_t a0[4], a1[4];
                 dev::e4m3x4_to_f16x2x2(r[0], a0[0], a0[2]);
                 dev::e4m3x4_to_f16x2x2(r[1], a0[1], a0[3]);
@@ -604,7 +593,7 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
 #pragma unroll
               for (int ks = 0; ks < T::KS; ++ks) {
                 uint32_t a[4];
-                dev::ldsm_x4(kb + koff[ks & 3] + (ks >> 2) * 2048, a);
+                dev::ldsm_x4(chunk(kb + kbase, ks), a);
                 dev::mma_16816((ks & 1) ? sd : sc, a, qb[ks][0], qb[ks][1]);
               }
             }
@@ -612,6 +601,10 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
             x[u][1] = (sc[1] + sd[1]) * ks0;
             x[u][2] = (sc[2] + sd[2]) * ks1;
             x[u][3] = (sc[3] + sd[3]) * ks1;
+            if (W && w.block_pos(d, j + u) < low) {
+              if (!sees(w.block_pos(d, j + u) + qh)) x[u][0] = x[u][1] = -INFINITY;
+              if (!sees(w.block_pos(d, j + u) + qh + 8)) x[u][2] = x[u][3] = -INFINITY;
+            }
             w.release_run();
           }
           if (!w.ok) break;
@@ -658,11 +651,13 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
             const uint32_t pb1 = dev::movmatrix_t(*reinterpret_cast<const uint32_t*>(&pk1));
             const uint32_t vb = w.wait_run();
             if (!w.ok) break;
+            const bool gap = W && w.block_pos(d, j + u) < low;
+            if (gap) zero_gap(vb, w.block_pos(d, j + u));
             if constexpr (T::F8) {
 #pragma unroll
               for (int i = 0; i < D / 32; ++i) {
                 uint32_t r[4];
-                dev::ldsm_x4_t(vb + v8off[i], r);
+                dev::ldsm_x4_t(chunk(vb + vbase, i), r);
                 uint32_t ae[4], ao[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) dev::e4m3x4_to_f16x2x2(__byte_perm(r[q], 0, 0x3120), ae[q], ao[q]);
@@ -673,10 +668,11 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
 #pragma unroll
               for (int mt = 0; mt < T::MT; ++mt) {
                 uint32_t a[4];
-                dev::ldsm_x4_t(vb + voff[mt & 3] + (mt >> 2) * 2048, a);
+                dev::ldsm_x4_t(chunk(vb + vbase, mt), a);
                 dev::mma_16816(o[mt], a, pb0, pb1);
               }
             }
+            if (gap) dev::fence_proxy_async_smem();  // the zeros precede the slot's next TMA write
             w.release_run();
           }
           w.prefetch_q();  // the next task's q, once the scheduler has published it
@@ -684,7 +680,7 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
       }
       // ---- the rest one by one: an odd lean block, then the blocks holding the context's end or rows of
       // this pass (masking, the fused append's rows from the inputs, the token's own write to the cache) ----
-      for (; j < jend && w.ok; ++j) {
+      for (; j < d.nbw && w.ok; ++j) {
         const int bpos = w.block_pos(d, j);  // the block's first position
         const int ntok = min(kBS, d.ctx - bpos);
         // fused append: positions ov0 .. bpos + ntok - 1 of the block are this pass's tokens; their rows
@@ -759,7 +755,6 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
         {
           const uint32_t ks_base = w.wait_run();
           if (!w.ok) break;
-          const int kr = (lane & 7) + ((lane >> 3) & 1) * 8;  // key row this lane addresses for ldmatrix
           if constexpr (T::F8) {
             unsigned char* rec = w.run_scales();  // the block's K and V scales arrived with the K run
             if (nov > 0) {
@@ -792,7 +787,7 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
               uint32_t r[4];
-              dev::ldsm_x4(ks_base + swz8<D>(kr, 2 * i + (lane >> 4)), r);
+              dev::ldsm_x4(chunk(ks_base + kbase, i), r);
               uint32_t a0[4], a1[4];  // {key g lo, key g + 8 lo, key g hi, key g + 8 hi}
               dev::e4m3x4_to_f16x2x2(r[0], a0[0], a0[2]);
               dev::e4m3x4_to_f16x2x2(r[1], a0[1], a0[3]);
@@ -806,7 +801,7 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
 #pragma unroll
             for (int ks = 0; ks < T::KS; ++ks) {
               uint32_t a[4];
-              dev::ldsm_x4(ks_base + swz(kr, 2 * ks + (lane >> 4)), a);
+              dev::ldsm_x4(chunk(ks_base + kbase, ks), a);
               dev::mma_16816((ks & 1) ? sd : sc, a, qb[ks][0], qb[ks][1]);
             }
           }
@@ -816,13 +811,8 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
           w.release_run();
         }
         // ---- online softmax (log2 domain); the lane holds keys qh, qh + 8 for heads h0, h0 + 1 ----
-        bool v0 = qh < ntok, v1 = qh + 8 < ntok;
-        // W: the keys of this block that lie between the sinks and the window
-        const bool gap = W && bpos < d.low;
-        if constexpr (W) {
-          v0 = v0 && (bpos + qh >= d.low || bpos + qh < p.win.sinks);
-          v1 = v1 && (bpos + qh + 8 >= d.low || bpos + qh + 8 < p.win.sinks);
-        }
+        const bool v0 = qh < ntok && sees(bpos + qh), v1 = qh + 8 < ntok && sees(bpos + qh + 8);
+        const bool gap = W && bpos < low;
         const float s0 = v0 ? sc[0] * ks0 : -INFINITY;  // key qh,     head h0
         const float s1 = v0 ? sc[1] * ks0 : -INFINITY;  // key qh,     head h0 + 1
         const float s2 = v1 ? sc[2] * ks1 : -INFINITY;  // key qh + 8, head h0
@@ -861,8 +851,6 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
         {
           const uint32_t vs_base = w.wait_run();
           if (!w.ok) break;
-          const int mat = lane >> 3;                      // ldmatrix matrix this lane addresses
-          const int vr = (lane & 7) + ((mat >> 1) << 3);  // its key row
           if constexpr (T::F8) {
             if (ntok < kBS) {  // rows past the context may hold anything (NaN codes): zero them
               for (int idx = lane; idx < (kBS - ntok) * (D / 16); idx += 32) {
@@ -882,20 +870,13 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
                 quant_rows(vs_base, p.v_in, true, nullptr, 0);
               }
             }
-            if (gap) {  // the gap's rows may hold anything too (those of this pass's tokens among them)
-              const int g0 = max(0, p.win.sinks - bpos), g1 = min(kBS, d.low - bpos);
-              for (int idx = lane; idx < (g1 - g0) * (D / 16); idx += 32)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vs_base + swz8<D>(g0 + idx / (D / 16), idx % (D / 16))),
-                             "r"(0)
-                             : "memory");
-              __syncwarp();
-            }
+            if (gap) zero_gap(vs_base, bpos);  // (rows of this pass's tokens may lie in it too)
             // 16 keys x 32 dims per transposing ldmatrix: a lane's word holds keys 2t, 2t + 1 at dims 2g, 2g + 1;
             // regrouped by dim, the even dims feed one MMA (o[2i]) and the odd dims another (o[2i + 1])
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
               uint32_t r[4];
-              dev::ldsm_x4_t(vs_base + swz8<D>(vr, 2 * i + (mat & 1)), r);
+              dev::ldsm_x4_t(chunk(vs_base + vbase, i), r);
               uint32_t ae[4], ao[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j) dev::e4m3x4_to_f16x2x2(__byte_perm(r[j], 0, 0x3120), ae[j], ao[j]);
@@ -911,18 +892,11 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
               __syncwarp();
             }
             if (nov > 0) override_rows(vs_base, p.v_in, pv);
-            if (gap) {
-              const int g0 = max(0, p.win.sinks - bpos), g1 = min(kBS, d.low - bpos);
-              for (int idx = lane; idx < (g1 - g0) * (D / 8); idx += 32)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vs_base + swz(g0 + idx / (D / 8), idx % (D / 8))),
-                             "r"(0)
-                             : "memory");
-              __syncwarp();
-            }
+            if (gap) zero_gap(vs_base, bpos);
 #pragma unroll
             for (int mt = 0; mt < T::MT; ++mt) {
               uint32_t a[4];
-              dev::ldsm_x4_t(vs_base + swz(vr, 2 * mt + (mat & 1)), a);
+              dev::ldsm_x4_t(chunk(vs_base + vbase, mt), a);
               dev::mma_16816(o[mt], a, pb0, pb1);
             }
           }
@@ -982,7 +956,6 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
             }
           }
         }
-      }
       }
     }
     if (!w.ok) break;
@@ -1082,10 +1055,15 @@ struct Scheduler {
     for (int j = 0; j < N; ++j) {
       if (ended) break;
       TaskEntry* e = &sm.queue[filled % T::QD];
-      int nb = 0, nst = 0, rot = 0;
+      int nb = 0, nst = 0, rot = 0, jump = 0;
       if (rec[j].x >= 0) {
         const int g = rec[j].y & 0xFF, s = rec[j].y >> 8, ctx = rec[j].w;
-        nb = min(p.split_blocks, token_blocks<W>(p, ctx).n - s * p.split_blocks);
+        const VisibleUnits vis = token_blocks<W>(p, ctx);
+        nb = min(p.split_blocks, vis.n - s * p.split_blocks);
+        if constexpr (W) {  // the split's blocks ahead of the gap: none, some, or all (then it has no gap)
+          const int ahead = max(0, vis.head - s * p.split_blocks);
+          if (ahead < nb) jump = ahead | vis.skip << 5;
+        }
         if (lane < nb) {
           int v = id[j];
           if (v < 0 || v >= p.num_blocks) {
@@ -1102,6 +1080,7 @@ struct Scheduler {
         e->rec = rec[j];
         e->nst = nst;
         e->nb = nb;
+        if (W) e->jump = jump;
         e->rot = rot;
       }
       // Append fused: the split holding the token's own position reads its key and value rows from the

@@ -366,6 +366,30 @@ __device__ void mma_warp(const PfParams& p, unsigned char* smem, const Bars& sh,
   }
 }
 
+// The lowest n bits of a word (n below 0: none, above 32: all).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  uint32_t m;
+  asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(m) : "r"(max(n, 0)));
+  return m;
+}
+
+// W: -infinity over the scores that this thread's row (TMEM lane) does not see: of its tile's keys e it sees those with
+// e <= lim and (e >= low or e < sinks).
+__device__ __forceinline__ void mask_scores(uint32_t taddr, int keys, int lim, int low, int sinks) {
+#pragma unroll 1
+  for (int c = 0; c < keys; c += 32) {
+    const uint32_t sees = low_bits(lim + 1 - c) & (~low_bits(low - c) | low_bits(sinks - c));
+    if (__all_sync(0xffffffffu, sees == 0xffffffffu)) continue;
+    uint32_t s[32];
+    dev::tmem_ld32(taddr + c, s);
+    dev::tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) s[e] = sees >> e & 1 ? s[e] : 0xff800000u;
+    dev::tmem_st32(taddr + c, s);
+  }
+  dev::tmem_wait_st();
+}
+
 // ---- softmax warpgroups: one S / O row per thread ---------------------------------------------------
 template <int D, int G, bool W>
 __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars& sh, int wg, int warp, int lane) {
@@ -418,9 +442,6 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
       // (zero q) score 0 on each.  A warp of padding rows alone keeps the mask (key 0 only).
       const bool all = kb + T::KEYS - 1 <= lim && (!W || kb >= low || kb + T::KEYS <= p.win.sinks);
       const bool full = __any_sync(0xffffffffu, valid) && __all_sync(0xffffffffu, !valid || all);
-      // whether this row sees key kb + e of the tile
-      const int e_lim = lim - kb, e_low = low - kb, e_sink = p.win.sinks - kb;
-      auto sees = [&](int e) { return e <= e_lim && (!W || e >= e_low || e < e_sink); };
       float sum4[4] = {0.f, 0.f, 0.f, 0.f};
       auto tile = [&](auto full_tag) {
         constexpr bool kFull = decltype(full_tag)::value;
@@ -432,7 +453,7 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const float x = __uint_as_float(s[k][e]);
-              mx4[e & 3] = fmaxf(mx4[e & 3], (kFull || sees(64 * h + 32 * k + e)) ? x : -INFINITY);
+              mx4[e & 3] = fmaxf(mx4[e & 3], (kFull || kb + 64 * h + 32 * k + e <= lim) ? x : -INFINITY);
             }
           return fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
         };
@@ -444,8 +465,8 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
             const int k = 2 * e;  // key 64 h + k of the tile
             float x0 = __uint_as_float(s[k >> 5][k & 31]), x1 = __uint_as_float(s[(k + 1) >> 5][(k + 1) & 31]);
             if constexpr (!kFull) {
-              if (!sees(64 * h + k)) x0 = -INFINITY;
-              if (!sees(64 * h + k + 1)) x1 = -INFINITY;
+              if (kb + 64 * h + k > lim) x0 = -INFINITY;
+              if (kb + 64 * h + k + 1 > lim) x1 = -INFINITY;
             }
             const float p0 = dev::ex2_approx(fmaf(x0, p.scale_log2, nm));
             const float p1 = dev::ex2_approx(fmaf(x1, p.scale_log2, nm));
@@ -544,7 +565,14 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
           }
         }
       };
-      if (full) tile(std::true_type{}); else tile(std::false_type{});
+      if constexpr (W) {
+        // A windowed row's mask has up to three edges; it is laid over S in tensor memory ahead of the tile's one
+        // code path.
+        if (!full) mask_scores(tl, T::KEYS, lim - kb, low - kb, p.win.sinks - kb);
+        tile(std::true_type{});
+      } else {
+        if (full) tile(std::true_type{}); else tile(std::false_type{});
+      }
       l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
       // ---- the item's last tile: V rows past its keys hold stale bytes; zero them (0 * NaN = NaN) ----
       if (wg == it.zfill_wg && j == it.n_all - 1) {

@@ -160,11 +160,21 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+_torch = None
+
+
 def _stream(stream) -> Optional[int]:
+    """The stream's handle; the current stream's without one (looked up without building a Stream object, which
+    costs more than a kernel launch)."""
+    global _torch
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    if _torch is None:
+        import torch
+        _torch = torch
+    if not _torch.cuda.is_initialized():
+        _torch.cuda.init()
+    return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
 
 
 def _check(status: int, fn: str) -> None:
