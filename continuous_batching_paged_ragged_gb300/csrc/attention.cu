@@ -74,7 +74,8 @@ __global__ void __launch_bounds__(256) merge_kernel(const MergeParams p) {
   const int e0 = blockIdx.z * 32;  // the chunk's first element: head e0 / D, dims e0 % D ..
   if (ctx <= 0 || e0 >= p.group * D) return;
   const int nblk = visible_blocks(ctx, p.win.window, p.win.sinks).n;
-  const int nsplit = (nblk + p.split_blocks - 1) / p.split_blocks;
+  const int size = token_split(ctx, p.split_blocks, p.win);
+  const int nsplit = (nblk + size - 1) / size;
   if (nsplit <= kFusedMergeSplits) return;
   const int tid = threadIdx.x, e4 = tid & 7, sg = tid >> 3;
   const int h = e0 / D;
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   int carry = 0;
   for (int base = 0; base < p.num_tokens; base += blockDim.x) {
     const int t = base + threadIdx.x;
-    int nblk = 0, row = 0, c = 0;
+    int nblk = 0, row = 0, c = 0, size = p.split_blocks;
     if (t < p.num_tokens) {
       const int b = dev::row_of_token(p.qsl, p.num_seqs, t);
       const int q0 = __ldg(p.qsl + b), q1 = __ldg(p.qsl + b + 1), ctx = __ldg(p.context_lens + b);
@@ -260,8 +261,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       p.tok_ctx[t] = c;  // 0: no decode work (prefill row or invalid metadata)
       row = b;
       nblk = visible_blocks(c, p.win.window, p.win.sinks).n;
+      size = token_split(c, p.split_blocks, p.win);
     }
-    const int nfull = nblk / p.split_blocks, tail = nblk % p.split_blocks;
+    const int nfull = nblk / size, tail = nblk % size;
     if (tail > 0) atomicAdd(&tail_at[tail], p.num_kv_heads);
     const int cnt = nfull * p.num_kv_heads;
     int total = 0;
@@ -283,8 +285,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   __syncthreads();
   for (int t = threadIdx.x; t < p.num_tokens; t += blockDim.x) {
     const int c = p.tok_ctx[t];  // written by this thread above
-    const int nblk = visible_blocks(c, p.win.window, p.win.sinks).n, nfull = nblk / p.split_blocks;
-    const int tail = nblk % p.split_blocks;
+    const int size = token_split(c, p.split_blocks, p.win);
+    const int nblk = visible_blocks(c, p.win.window, p.win.sinks).n, nfull = nblk / size, tail = nblk % size;
     if (tail > 0) {
       const int at = atomicAdd(&tail_at[tail], p.num_kv_heads), row = p.tok_row[t];
       for (int g = 0; g < p.num_kv_heads; ++g) p.tasks[at + g] = make_int4(t, g | (nfull << 8), row, c);
@@ -383,10 +385,12 @@ static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 static WsLayout ws_layout(const pkv_config& c, int num_seqs, int num_tokens, int max_blocks, const KeyWindow& win = KeyWindow()) {
   WsLayout w;
-  // a token sees at most the sinks' blocks and those that a window can touch
-  const int64_t seen = ((int64_t)win.sinks + kBS - 1) / kBS + ((int64_t)win.window + kBS - 2) / kBS + 1;
-  const int tok_blocks = (int)std::min<int64_t>(max_blocks, seen);
-  w.max_splits = (tok_blocks + c.split_blocks - 1) / c.split_blocks;
+  // a token sees its whole context, or behind a window at most so many blocks
+  w.max_splits = (max_blocks + c.split_blocks - 1) / c.split_blocks;
+  if (win.window != kNoWindow) {
+    const int seen = std::min(max_blocks, window_blocks_at_most(win.window, std::min(win.sinks, kNoWindow - kBS)));
+    w.max_splits = (seen + win.split - 1) / win.split;  // (win.split is at most split_blocks)
+  }
   w.max_tasks = (int64_t)num_tokens * c.num_kv_heads * w.max_splits;
   const int group = c.num_q_heads / c.num_kv_heads;
   // the tile kernel reads fp16 K/V: on an 8-bit cache it reads the prefill rows' blocks from an fp16 shadow
@@ -740,6 +744,7 @@ static pkv_status check_workspace(pkv_pool* pool, void* workspace, size_t ws_byt
   if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
     return fail(PKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   const WsLayout w = ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks, win);
+  if (w.max_tasks >= (1ll << 31)) return fail(PKV_ERR_UNSUPPORTED, "too many splits in one pass; raise split_blocks");
   if (ws_bytes < w.total)
     return fail(PKV_ERR_INVALID_ARG, "workspace too small: need " + std::to_string(w.total) + " bytes");
   return PKV_OK;
@@ -763,7 +768,7 @@ static const PlanKey* find_plan(const pkv_pool* pool, const void* workspace) {
 // The window of the plan on `workspace` (none without a plan: the call is refused later).
 static KeyWindow planned_window(const pkv_pool* pool, const void* workspace) {
   const PlanKey* k = pool ? find_plan(pool, workspace) : nullptr;
-  return k ? KeyWindow{k->window, k->sinks} : KeyWindow();
+  return k && k->window != kNoWindow ? make_window(k->window, k->sinks, pool->cfg.split_blocks) : KeyWindow();
 }
 
 static void forget_plan(pkv_pool* pool, const void* workspace) {
@@ -858,7 +863,8 @@ extern "C" pkv_status pkv_attention_plan(pkv_pool* pool, const int32_t* context_
 extern "C" size_t pkv_attention_window_workspace_bytes(const pkv_pool* pool, int32_t num_seqs, int32_t num_tokens,
                                                        int32_t max_blocks_per_seq, int32_t window, int32_t sinks) {
   if (!pool || num_seqs < 0 || num_tokens < 0 || max_blocks_per_seq < 1 || window < 1 || sinks < 0) return 0;
-  return ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks_per_seq, KeyWindow{window, sinks}).total;
+  return ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks_per_seq,
+                   make_window(window, sinks, pool->cfg.split_blocks)).total;
 }
 
 extern "C" pkv_status pkv_attention_window_plan(pkv_pool* pool, const int32_t* context_lens,
@@ -868,8 +874,9 @@ extern "C" pkv_status pkv_attention_window_plan(pkv_pool* pool, const int32_t* c
   clear_error();
   if (window < 1) return fail(PKV_ERR_INVALID_ARG, "window must be >= 1");
   if (sinks < 0) return fail(PKV_ERR_INVALID_ARG, "sinks must be >= 0");
-  return plan_pass(pool, context_lens, query_start_loc, num_seqs, num_tokens, max_blocks_per_seq, KeyWindow{window, sinks},
-                   workspace, workspace_bytes, stream);
+  if (!pool) return fail(PKV_ERR_INVALID_ARG, "pool is NULL");
+  return plan_pass(pool, context_lens, query_start_loc, num_seqs, num_tokens, max_blocks_per_seq,
+                   make_window(window, sinks, pool->cfg.split_blocks), workspace, workspace_bytes, stream);
 }
 
 extern "C" pkv_status pkv_attention(pkv_pool* pool, int32_t layer, const void* q, const int32_t* block_tables,

@@ -36,7 +36,27 @@ constexpr int kNoWindow = 0x7FFFFFFF;
 struct KeyWindow {
   int window = kNoWindow;
   int sinks = 0;
+  int split = 0;  // blocks per split of a token that the window cuts (make_window)
 };
+
+// A windowed plan's tokens mostly see the same number of blocks, a little more than a power of two of them: full splits
+// of 32 would leave each token a last split of a few blocks, whose cost is that of a task and not of its blocks.  So a
+// token cut by its window runs in equal splits, rounded up to eight blocks (two for each streaming warp, a pair on the
+// 8-bit d 256 path): 66 blocks as 24 + 24 + 18 take 49.7 us, as 32 + 32 + 2 54.6 (256 rows, 12 / 2 heads, d 128); 34 as
+// 24 + 10 32.5 against 36.2; 261 stay at 32 (104 us on the 8-bit cache at d 256, 120 in splits of 28).  The window
+// alone decides, and a token whose whole context is visible keeps the unwindowed partition.
+__host__ __device__ constexpr int window_blocks_at_most(int window, int sinks) {
+  return (sinks + kBS - 1) / kBS + (window > kNoWindow - kBS ? kNoWindow / kBS : (window + kBS - 2) / kBS) + 1;
+}
+__host__ constexpr KeyWindow make_window(int window, int sinks, int split_blocks) {
+  const int seen = window_blocks_at_most(window, sinks < kNoWindow - kBS ? sinks : kNoWindow - kBS);
+  const int n = (seen + split_blocks - 1) / split_blocks, even = ((seen + n - 1) / n + 7) / 8 * 8;
+  return KeyWindow{window, sinks, even < split_blocks ? even : split_blocks};
+}
+// Blocks per split of a token that sees ctx keys without the window.
+__host__ __device__ constexpr int token_split(int ctx, int split_blocks, const KeyWindow& win) {
+  return ctx > win.window ? win.split : split_blocks;
+}
 
 // First key of the window of the query that sees `ctx` keys without one (position ctx - 1).
 __host__ __device__ constexpr int window_low(int ctx, int window) { return ctx > window ? ctx - window : 0; }

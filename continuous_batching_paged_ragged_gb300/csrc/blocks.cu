@@ -49,39 +49,46 @@ BlockGeo geo_of(const pkv_pool* pool) {
 }
 
 // The first `rows` rows of every head of block src into block dst, planes [p0, p1) of the planes + scale_planes,
-// by all threads of the CTA.
+// by all threads of the CTA.  The copied chunks of all planes and heads are one index range, so that every thread has
+// loads in flight however short the pieces are (a tail of one row is 64 bytes a plane and head).
 __device__ void copy_rows(const BlockGeo& g, int src, int dst, int rows, int p0, int p1) {
-  const int head_chunks = kBS * g.row_bytes / 16;           // 16-byte chunks of a head's run
-  const int live = rows * g.row_bytes / 16;                 // of which copied
-  const int per = g.num_kv_heads * live;                    // chunks of a plane
-  const int64_t piece = (int64_t)g.num_kv_heads * head_chunks, plane = g.plane_bytes / 16;
+  const uint32_t run = kBS * g.row_bytes / 16;              // 16-byte chunks of a head's run
+  const uint32_t live = rows * g.row_bytes / 16;            // of which copied
+  const int64_t piece = (int64_t)g.num_kv_heads * run, plane = g.plane_bytes / 16;
   const int v1 = min(p1, g.planes);
   const uint4* in = reinterpret_cast<const uint4*>(g.values) + src * piece;
   uint4* out = reinterpret_cast<uint4*>(g.values) + dst * piece;
-  const int64_t n = p0 < v1 ? (int64_t)(v1 - p0) * per : 0;
+  const uint32_t per = live * g.num_kv_heads, n = p0 < v1 ? (v1 - p0) * per : 0;
   constexpr int U = 4;  // chunks in flight a thread
-  for (int64_t i0 = threadIdx.x; i0 < n; i0 += (int64_t)U * blockDim.x) {
+  for (uint32_t i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
     uint4 v[U];
     int64_t off[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t i = i0 + (int64_t)u * blockDim.x;
+      const uint32_t i = i0 + u * kThreads;
       off[u] = -1;
       if (i >= n) continue;
-      const int p = (int)(i / per), r = (int)(i - (int64_t)p * per), h = r / live;
-      off[u] = (p0 + p) * plane + (int64_t)h * head_chunks + (r - h * live);
+      const uint32_t p = i / per, r = i - p * per, h = r / live;
+      off[u] = (int64_t)(p0 + p) * plane + h * run + (r - h * live);
       v[u] = __ldcs(in + off[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (off[u] >= 0) __stcs(out + off[u], v[u]);
   }
-  // scale records [K: 16 slots][V: 16 slots]: the first `rows` bytes of each half
-  for (int p = max(p0, g.planes); p < p1; ++p) {
-    const unsigned char* si = g.scales + (p - g.planes) * g.scale_bytes + (int64_t)src * g.num_kv_heads * 32;
-    unsigned char* so = g.scales + (p - g.planes) * g.scale_bytes + (int64_t)dst * g.num_kv_heads * 32;
-    for (int i = threadIdx.x; i < g.num_kv_heads * 32; i += blockDim.x)
-      if ((i & 15) < rows) so[i] = si[i];
+  // 8-bit: one thread a scale record (16 slots of K or V of a head), the first `rows` bytes of it
+  const int s0 = max(p0, g.planes) - g.planes, s1 = p1 - g.planes;
+  const int recs = 2 * g.num_kv_heads;
+  for (int i = threadIdx.x; i < (s1 - s0) * recs; i += kThreads) {
+    const int p = s0 + i / recs, r = i % recs;
+    const int64_t off = p * g.scale_bytes + (int64_t)r * 16;
+    const uint4 v = *reinterpret_cast<const uint4*>(g.scales + off + (int64_t)src * recs * 16);
+    unsigned char* to = g.scales + off + (int64_t)dst * recs * 16;
+    if (rows & 8) *reinterpret_cast<uint2*>(to) = make_uint2(v.x, v.y);
+    const uint32_t four = rows & 8 ? v.z : v.x, rest = rows & 8 ? (rows & 4 ? v.w : v.z) : (rows & 4 ? v.y : v.x);
+    if (rows & 4) *reinterpret_cast<uint32_t*>(to + (rows & 8)) = four;
+    if (rows & 2) *reinterpret_cast<uint16_t*>(to + (rows & 12)) = (uint16_t)rest;
+    if (rows & 1) to[rows & 14] = (unsigned char)(rest >> (rows & 2 ? 16 : 0));
   }
 }
 
@@ -102,23 +109,138 @@ __device__ __forceinline__ void slice_planes(const BlockGeo& g, int s, int slice
   p1 = (int)((int64_t)all * (s + 1) / slices);
 }
 
-__global__ void __launch_bounds__(kThreads) copy_blocks_kernel(const BlockGeo g, const int32_t* __restrict__ pairs,
-                                                               int num_pairs, int slices) {
-  dev::griddep_wait();
-  const int64_t units = (int64_t)num_pairs * slices;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int64_t pair = u / slices;
-    const int s = (int)(u - pair * slices);
-    const int src = __ldg(pairs + 2 * pair), dst = __ldg(pairs + 2 * pair + 1);
-    if (src == -1 || dst == -1) continue;
-    if (bad_block(g, src) || bad_block(g, dst)) {
-      if (s == 0 && threadIdx.x == 0) dev::set_error(g.err, PKV_DEVERR_BLOCK_RANGE);
-      continue;
-    }
-    int p0, p1;
-    slice_planes(g, s, slices, p0, p1);
-    copy_rows(g, src, dst, kBS, p0, p1);
+// ---------------------------------------------------------------------------------------------------
+// Whole blocks, by the bulk copy engine.  A worker (one thread of a warp of its own) takes pieces of up to kPiece bytes
+// of one plane of one move, every worker its own sequence over all moves and planes, through a ring of kSlots buffers
+// in shared memory: the load of a piece is issued kSlots - 1 pieces ahead of its store, and nothing passes through
+// registers.  Plain 16-byte loads and stores keep 64 KB in flight an SM and empty it at every unit of work: 1 GB in
+// blocks of 1 MB took 343 us with them.
+// ---------------------------------------------------------------------------------------------------
+constexpr int kPiece = 8192;
+constexpr int kSlots = 3;
+constexpr int kWorkers = 4;  // per CTA
+constexpr int kBulkSmem = kWorkers * kSlots * kPiece;
+constexpr int kBulkCtas = 2;  // per SM
+
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src_smem, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(dev::smem_addr(src_smem)), "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the latest N stores have read their buffers.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Where a worker's piece comes from and goes to (bytes 0: nothing to copy).
+struct Piece {
+  const char* src;
+  char* dst;
+  uint32_t bytes;
+};
+
+// The pieces of a block: every value plane in `parts` parts, then the scale planes whole (in parts of kPiece too).
+struct PieceGeo {
+  int value_bytes, value_parts;   // of one block in a value plane
+  int scale_bytes, scale_parts;
+  __device__ explicit PieceGeo(const BlockGeo& g) {
+    value_bytes = g.num_kv_heads * kBS * g.row_bytes;
+    value_parts = (value_bytes + kPiece - 1) / kPiece;
+    scale_bytes = g.num_kv_heads * 32;
+    scale_parts = (scale_bytes + kPiece - 1) / kPiece;
   }
+  __device__ int per_block(const BlockGeo& g) const { return g.planes * value_parts + g.scale_planes * scale_parts; }
+  __device__ Piece piece(const BlockGeo& g, int src, int dst, int q) const {
+    const int nv = g.planes * value_parts;
+    const bool value = q < nv;
+    const int parts = value ? value_parts : scale_parts, block = value ? value_bytes : scale_bytes;
+    const int r = value ? q : q - nv, plane = r / parts, at = (r - plane * parts) * kPiece;
+    char* base = value ? g.values + plane * g.plane_bytes : reinterpret_cast<char*>(g.scales) + plane * g.scale_bytes;
+    return Piece{base + (int64_t)src * block + at, base + (int64_t)dst * block + at, (uint32_t)min(kPiece, block - at)};
+  }
+};
+
+// Copies `moves` blocks; ends(m, src, dst) gives move m's blocks, or false to skip it.  Called by all threads of a CTA of
+// kWorkers warps.
+template <typename F>
+__device__ void bulk_copy(const BlockGeo& g, int64_t moves, unsigned char* smem, F ends) {
+  __shared__ __align__(8) uint64_t full[kWorkers][kSlots];
+  const int w = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) != 0) return;
+  for (int s = 0; s < kSlots; ++s) dev::mbar_init(&full[w][s], 1);
+  dev::fence_mbar_init();
+  dev::fence_proxy_async_smem();
+  unsigned char* ring = smem + w * kSlots * kPiece;
+  const PieceGeo pg(g);
+  const int per = pg.per_block(g);
+  const int step = gridDim.x * kWorkers, step_m = step / per, step_q = step % per;
+  int64_t m = (blockIdx.x * kWorkers + w) / per;  // the next piece to load: of move m,
+  int q = (blockIdx.x * kWorkers + w) % per;      // its piece q
+  char* to[kSlots];
+  uint32_t bytes[kSlots];
+  // the worker's next piece into slot s; none (bytes 0) at the end of its sequence
+  auto load = [&](int s) {
+    bytes[s] = 0;
+    while (m < moves && bytes[s] == 0) {
+      int src, dst;
+      if (ends(m, q == 0, src, dst)) {
+        const Piece p = pg.piece(g, src, dst, q);
+        to[s] = p.dst;
+        bytes[s] = p.bytes;
+        dev::mbar_arrive_expect_tx(&full[w][s], p.bytes);
+        dev::bulk_g2s_plain(ring + s * kPiece, p.src, p.bytes, &full[w][s]);
+      }
+      m += step_m;
+      q += step_q;
+      if (q >= per) {
+        q -= per;
+        ++m;
+      }
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kSlots; ++s) load(s);
+  bool ok = true;
+  for (uint32_t round = 0; ok; ++round) {
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+      if (bytes[s] == 0) {
+        ok = false;
+        break;
+      }
+      if (!dev::mbar_wait(&full[w][s], round & 1)) {
+        dev::set_error(g.err, PKV_DEVERR_WAIT_TIMEOUT);
+        for (int t = 0; t < kSlots; ++t)  // the copies still in flight
+          if (t != s && bytes[t]) dev::mbar_wait(&full[w][t], (t > s ? round : round + 1) & 1);
+        ok = false;
+        break;
+      }
+      bulk_s2g(to[s], ring + s * kPiece, bytes[s]);
+      // refill the slot before this one: its store is the one issued last but one
+      const int e = (s + kSlots - 1) % kSlots;
+      if (round > 0 || s > 0) {
+        bulk_wait_read<1>();
+        load(e);
+      }
+    }
+  }
+  bulk_wait_all();
+}
+
+__global__ void __launch_bounds__(kWorkers * 32) copy_blocks_kernel(const BlockGeo g, const int32_t* __restrict__ pairs,
+                                                                    int num_pairs) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  dev::griddep_wait();
+  bulk_copy(g, num_pairs, smem, [&](int64_t m, bool first, int& src, int& dst) {
+    src = __ldg(pairs + 2 * m);
+    dst = __ldg(pairs + 2 * m + 1);
+    if (src == -1 || dst == -1) return false;
+    if (!bad_block(g, src) && !bad_block(g, dst)) return true;
+    if (first) dev::set_error(g.err, PKV_DEVERR_BLOCK_RANGE);
+    return false;
+  });
   publish();
 }
 
@@ -313,19 +435,18 @@ __global__ void __launch_bounds__(kPlanThreads) compact_mark_kernel(const Compac
   if (last) plan_moves(p, p.bits);
 }
 
-__global__ void __launch_bounds__(kThreads) compact_move_kernel(const BlockGeo g, const CompactParams p, int slices) {
+__global__ void __launch_bounds__(kWorkers * 32) compact_move_kernel(const BlockGeo g, const CompactParams p) {
+  extern __shared__ __align__(128) unsigned char smem[];
   dev::griddep_wait();
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < p.entries; i += (int64_t)gridDim.x * kThreads) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < p.entries; i += (int64_t)gridDim.x * blockDim.x) {
     const int id = p.tables[i];
     p.new_tables[i] = id >= 0 && id < p.num_blocks ? p.remap[id] : id;
   }
-  const int64_t units = (int64_t)p.hdr->n_moves * slices;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int m = (int)(u / slices), s = (int)(u - (int64_t)m * slices);
-    int p0, p1;
-    slice_planes(g, s, slices, p0, p1);
-    copy_rows(g, p.src[m], p.dst[m], kBS, p0, p1);
-  }
+  bulk_copy(g, p.hdr->n_moves, smem, [&](int64_t m, bool, int& src, int& dst) {
+    src = p.src[m];
+    dst = p.dst[m];
+    return true;
+  });
   publish();
 }
 
@@ -355,6 +476,20 @@ pkv_status fetch_for_validation(const int32_t* src, size_t n, void* stream, std:
   if (e != cudaSuccess) return cuda_fail(e, "PKV_VALIDATE: copy");
   *ran = true;
   return PKV_OK;
+}
+
+template <typename K>
+cudaError_t allow_bulk_smem(K kernel, bool* done) {
+  if (*done) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBulkSmem);
+  *done = e == cudaSuccess;
+  return e;
+}
+
+// CTAs for up to `moves` block copies: a worker for every piece, up to what is resident at once.
+int64_t bulk_grid(const pkv_pool* pool, const BlockGeo& g, int64_t moves) {
+  const int64_t pieces = moves * (g.planes + g.scale_planes);  // at least
+  return std::max<int64_t>(1, std::min<int64_t>((pieces + kWorkers - 1) / kWorkers, (int64_t)pool->num_sms * kBulkCtas));
 }
 
 // Units of work for `items` block copies: a block's planes are cut into slices so that every CTA slot of the GPU
@@ -398,11 +533,11 @@ extern "C" pkv_status pkv_copy_blocks(pkv_pool* pool, const int32_t* pairs, int3
     }
   }
   const BlockGeo g = geo_of(pool);
-  const int64_t ctas = (int64_t)pool->num_sms * 8;
-  const int slices = slices_for(g, num_pairs, ctas);
-  const int64_t grid = std::min<int64_t>((int64_t)num_pairs * slices, ctas);
-  const cudaError_t e = launch_pdl(copy_blocks_kernel, dim3((unsigned)grid), dim3(kThreads), 0, (cudaStream_t)stream, g, pairs,
-                                   (int)num_pairs, slices);
+  static bool smem_set = false;
+  cudaError_t e = allow_bulk_smem(copy_blocks_kernel, &smem_set);
+  if (e == cudaSuccess)
+    e = launch_pdl(copy_blocks_kernel, dim3((unsigned)bulk_grid(pool, g, num_pairs)), dim3(kWorkers * 32), kBulkSmem,
+                   (cudaStream_t)stream, g, pairs, (int)num_pairs);
   if (e != cudaSuccess) return cuda_fail(e, "copy_blocks launch");
   pool->last_launches = 1;
   return PKV_OK;
@@ -443,7 +578,7 @@ extern "C" pkv_status pkv_fork_rows(pkv_pool* pool, int32_t* block_tables, int32
         return fail(PKV_ERR_INVALID_ARG, "PKV_VALIDATE: row " + std::to_string(host[3 * i]) + " is a child and a parent");
   }
   const BlockGeo g = geo_of(pool);
-  const int64_t ctas = (int64_t)pool->num_sms * 8;
+  const int64_t ctas = (int64_t)pool->num_sms * 4;
   const int slices = slices_for(g, num_forks, ctas);
   const int64_t grid = std::min<int64_t>((int64_t)num_forks * slices, ctas);
   const cudaError_t e = launch_pdl(fork_rows_kernel, dim3((unsigned)grid), dim3(kThreads), 0, (cudaStream_t)stream, g,
@@ -506,9 +641,10 @@ extern "C" pkv_status pkv_compact(pkv_pool* pool, const int32_t* block_tables, i
   }
   if (e != cudaSuccess) return cuda_fail(e, "compact plan launch");
   const BlockGeo g = geo_of(pool);
-  const int64_t ctas = (int64_t)pool->num_sms * 8;
-  const int slices = slices_for(g, 64, ctas);  // the number of moves is known on the device alone
-  e = launch_pdl(compact_move_kernel, dim3((unsigned)ctas), dim3(kThreads), 0, s, g, p, slices);
+  static bool smem_set = false;
+  e = allow_bulk_smem(compact_move_kernel, &smem_set);
+  if (e == cudaSuccess)  // the number of moves is known on the device alone
+    e = launch_pdl(compact_move_kernel, dim3((unsigned)bulk_grid(pool, g, nb)), dim3(kWorkers * 32), kBulkSmem, s, g, p);
   if (e != cudaSuccess) return cuda_fail(e, "compact move launch");
   pool->last_launches = launches + 1;
   return PKV_OK;

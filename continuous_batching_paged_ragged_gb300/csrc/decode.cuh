@@ -143,6 +143,11 @@ __device__ __forceinline__ VisibleUnits token_blocks(const DecodeParams& p, int 
   if constexpr (W) return visible_blocks(ctx, p.win.window, p.win.sinks);
   return VisibleUnits{0, 0, (ctx + kBS - 1) / kBS};
 }
+template <bool W>
+__device__ __forceinline__ int split_size(const DecodeParams& p, int ctx) {
+  if constexpr (W) return token_split(ctx, p.split_blocks, p.win);
+  return p.split_blocks;
+}
 
 // Byte offset of 16-byte chunk c (8 dims) of key row r inside a ring slot written by 64-value TMA boxes
 // with the 128-byte swizzle: box c / 8, row r at 128 bytes, chunk slot (c % 8) XOR (r % 8).
@@ -223,7 +228,8 @@ struct DecodeSmem {
 
 // A task as a streaming warp sees it.
 struct TaskView {
-  int t, g, s, row, ctx, nst;
+  int t, g, row, ctx, nst;
+  int base;         // the split's first block among the token's (visible) blocks
   int nbw;          // blocks of the split dealt to this warp: task-local blocks bw, bw + 4, ...
   int bw;
   int nlean;        // the warp's leading blocks that are full and hold no row of this pass (see Streamer)
@@ -292,9 +298,9 @@ struct Streamer {
     const int4 rec = e->rec;
     v.t = rec.x;
     v.g = rec.y & 0xFF;
-    v.s = rec.y >> 8;
     v.row = rec.z;
     v.ctx = rec.w;
+    v.base = (rec.y >> 8) * split_size<W>(p, v.ctx);
     v.nst = e->nst;
     if constexpr (W) v.jump = e->jump;
     v.bw = (warp - e->rot) & 3;
@@ -305,7 +311,7 @@ struct Streamer {
     // holds without the fused append, so both calls pair the same blocks and give the same bits.  Blocks rise
     // with j, so the lean ones are the warp's first nlean.
     const int from = min(v.nst, v.ctx);
-    const int first = v.s * p.split_blocks + v.bw;  // visible index of the warp's block 0 (unwindowed: its block of the row)
+    const int first = v.base + v.bw;  // visible index of the warp's block 0 (unwindowed: its block of the row)
     const int skip = W ? token_blocks<W>(p, v.ctx).skip : 0;
     const int nfull = from / kBS - skip - first;  // blocks first, first + NW, ... below from / 16
     v.nlean = (!T::PAIRS || nfull <= 0) ? 0 : min(v.nbw, (nfull + T::NW - 1) / T::NW);
@@ -314,7 +320,7 @@ struct Streamer {
   __device__ __forceinline__ int block_pos(const TaskView& v, int j) const {
     const int b = v.bw + T::NW * j;  // of the split
     const int gap = W && b >= (v.jump & 31) ? v.jump >> 5 : 0;
-    return (v.s * p.split_blocks + b + gap) * kBS;
+    return (v.base + b + gap) * kBS;
   }
   // Run r of the warp's stream within a task: the lean blocks go in pairs, K of both then V of both; the rest
   // (an odd lean block, then the blocks holding the context's end or this pass's rows) one by one, K then V.
@@ -1044,8 +1050,9 @@ struct Scheduler {
       if (rec[j].x >= 0) {
         const int s = rec[j].y >> 8;
         const VisibleUnits vis = token_blocks<W>(p, rec[j].w);
-        const int b = s * p.split_blocks + lane;  // the split's block `lane` among the visible ones
-        if (lane < min(p.split_blocks, vis.n - s * p.split_blocks))
+        const int size = split_size<W>(p, rec[j].w);
+        const int b = s * size + lane;  // the split's block `lane` among the visible ones
+        if (lane < min(size, vis.n - s * size))
           id[j] = __ldcg(p.block_tables + (int64_t)rec[j].z * p.max_blocks + (W ? vis.row_unit(b) : b));
         q0[j] = __ldcg(p.qsl + rec[j].z);
       }
@@ -1059,9 +1066,10 @@ struct Scheduler {
       if (rec[j].x >= 0) {
         const int g = rec[j].y & 0xFF, s = rec[j].y >> 8, ctx = rec[j].w;
         const VisibleUnits vis = token_blocks<W>(p, ctx);
-        nb = min(p.split_blocks, vis.n - s * p.split_blocks);
+        const int size = split_size<W>(p, ctx);
+        nb = min(size, vis.n - s * size);
         if constexpr (W) {  // the split's blocks ahead of the gap: none, some, or all (then it has no gap)
-          const int ahead = max(0, vis.head - s * p.split_blocks);
+          const int ahead = max(0, vis.head - s * size);
           if (ahead < nb) jump = ahead | vis.skip << 5;
         }
         if (lane < nb) {
@@ -1087,7 +1095,7 @@ struct Scheduler {
       // inputs (and its slot) in the middle of its last block, where the load's latency is exposed; bring
       // them into L2 now, a task or more before they are needed.
       if (p.k_in != nullptr && rec[j].x >= 0 && nb > 0 &&
-          (rec[j].y >> 8) == (token_blocks<W>(p, rec[j].w).n - 1) / p.split_blocks) {
+          (rec[j].y >> 8) == (token_blocks<W>(p, rec[j].w).n - 1) / split_size<W>(p, rec[j].w)) {
         constexpr int LINES = D * 2 / 128;  // 128-byte lines of one row
         const size_t row = ((size_t)rec[j].x * p.num_kv_heads + (rec[j].y & 0xFF)) * D;
         if (lane < LINES) dev::prefetch_l2(p.k_in + row + lane * 64);
@@ -1343,7 +1351,8 @@ struct Combiner {
       if (rec.x < 0) break;
       if (lane == 0) dev::mbar_arrive(&sm.qempty[k % T::QD]);
       const int t = rec.x, g = rec.y & 0xFF, s = rec.y >> 8, ctx = rec.w;
-      const int nsplit = (token_blocks<W>(p, ctx).n + p.split_blocks - 1) / p.split_blocks;
+      const int size = split_size<W>(p, ctx);
+      const int nsplit = (token_blocks<W>(p, ctx).n + size - 1) / size;
       const int tg = t * p.num_kv_heads + g;
       const bool multi = nsplit > 1 && nsplit <= kFusedMergeSplits;
       int done_lane0 = 0;  // splits of the token counted so far
