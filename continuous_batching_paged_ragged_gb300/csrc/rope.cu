@@ -48,13 +48,14 @@ struct RopeParams {
   unsigned char* scales;
   int64_t num_slots;
   int num_tokens, num_q_heads, num_kv_heads;
-  int lanes_heads;          // head slots per token: a thread does heads hs, hs + lanes_heads, ...
+  int tokens;               // per CTA
   int rot_dim;
   float out_scale;
   int32_t* err;
 };
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kMaxTokens = 4;  // per CTA
 
 __device__ __forceinline__ uint4 ld16(const __half* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
@@ -83,95 +84,115 @@ __device__ __forceinline__ void rotate8_interleaved(uint4& a, uint4& b, const fl
   }
 }
 
-// A thread: one token, 16 values of a head (two 16-byte chunks holding 8 whole pairs, or 16 values past the rotated
-// part), and every lanes_heads-th head.  Its 8 angles serve all of its heads, and no thread waits for another.
+// A CTA rotates `tokens` tokens.  Every angle is computed once, by one thread, into shared memory (a sincospif costs
+// more than the loads and stores of a chunk: with the 8 angles of a 16-value piece computed where they were used, once
+// for every few heads, 8192 tokens took 15 to 21 us).  The unit of the rest is an item: 16 values of a q or KV head (two
+// 16-byte chunks that hold 8 whole pairs, or 16 values past the rotated part; of a KV head the key's and the value's).
+// A thread loads its first items before it computes its angles, so that neither waits for the other.
 template <int D, bool F8, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams p, const __grid_constant__ RopeTurns turns) {
-  constexpr int PC = D / 16;  // threads per (token, head slot): a power of two within a warp
-  __shared__ uint64_t step[D / 2];
-  const int half = p.rot_dim / 2;
-  for (int i = threadIdx.x; i < half; i += kThreads) step[i] = turns.turn[i];
-  __syncthreads();
+  constexpr int PC = D / 16;  // items per head: a power of two within a warp
+  constexpr int U = 2;        // items in flight a thread
+  // (cos, sin) of pairs 2j and 2j + 1 of a token's rotated 16-value piece pc at [token][j][pc]: consecutive lanes read
+  // consecutive 16 bytes
+  __shared__ float4 angle[kMaxTokens][4][PC];
+  const int half = p.rot_dim / 2, pieces = p.rot_dim / 16;
+  const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
+  const int n = (int)min((int64_t)p.tokens, p.num_tokens - t0);
+  const int heads = p.num_q_heads + p.num_kv_heads;  // q heads, then KV heads
+  const uint32_t per = heads * PC, items = n * per;
   dev::griddep_wait();
   dev::griddep_launch_dependents();
-  const int heads = p.num_q_heads + p.num_kv_heads;  // q heads, then KV heads (their keys and values)
-  const int64_t total = (int64_t)p.num_tokens * p.lanes_heads * PC;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const bool in = i < total;
-  const int pc = (int)(i % PC);
-  const int64_t th = in ? i / PC : 0;
-  const int64_t t = th / p.lanes_heads;
-  const int hs = (int)(th - t * p.lanes_heads);
-  const bool rot = 16 * pc < p.rot_dim;
-  // the thread's two chunks (in 8-value units) of a q or k row
-  const int c0 = rot && !INTER ? pc : 2 * pc, c1 = rot && !INTER ? pc + half / 8 : 2 * pc + 1;
-  float cs[8], sn[8];
-  if (rot) {
-    const uint64_t pos = (uint64_t)(int64_t)(in ? __ldg(p.positions + t) : 0);
+  for (uint32_t i0 = 0; i0 < items; i0 += U * kThreads) {  // the same number of rounds in every thread
+    uint4 a[U], b[U], va[U], vb[U];
+    int64_t slot[U];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int32_t turn = (int32_t)((pos * step[8 * pc + j]) >> 32);
-      sincospif((float)turn * 0x1p-31f, &sn[j], &cs[j]);
-      sn[j] *= p.out_scale;
-      cs[j] *= p.out_scale;
-    }
-  }
-  const int64_t slot = in ? __ldg(p.slots + t) : -1;
-  const bool store = slot >= 0 && slot < p.num_slots;
-  if (in && slot != -1 && !store && pc == 0 && hs == 0) dev::set_error(p.err, PKV_DEVERR_SLOT_RANGE);
-  auto turn2 = [&](uint4& a, uint4& b) {
-    if (!rot) return;
-    if constexpr (INTER) rotate8_interleaved(a, b, cs, sn); else rotate8(a, b, cs, sn);
-  };
-  for (int h = hs; h - hs < heads; h += p.lanes_heads) {  // the same number of rounds in every lane
-    const bool mine = in && h < heads;
-    if (mine && h < p.num_q_heads) {
-      const __half* src = p.q + t * p.q_stride + (int64_t)h * D;
-      __half* dst = p.q_out + (t * p.num_q_heads + h) * D;
-      // (plain loads: q_out may be q)
-      uint4 a = reinterpret_cast<const uint4*>(src)[c0], b = reinterpret_cast<const uint4*>(src)[c1];
-      turn2(a, b);
-      reinterpret_cast<uint4*>(dst)[c0] = a;
-      reinterpret_cast<uint4*>(dst)[c1] = b;
-    }
-    const bool kv = mine && h >= p.num_q_heads && store;
-    const int g = h - p.num_q_heads;
-    uint4 ka = make_uint4(0, 0, 0, 0), kb = ka, va = ka, vb = ka;
-    if (kv) {
-      const __half* ks = p.k + t * p.k_stride + (int64_t)g * D;
-      const __half* vs = p.v + t * p.v_stride + (int64_t)g * D;
-      ka = ld16(ks + 8 * c0);
-      kb = ld16(ks + 8 * c1);
-      va = ld16(vs + 16 * pc);
-      vb = ld16(vs + 16 * pc + 8);
-      turn2(ka, kb);
-    }
-    const int64_t row = kv ? ((slot >> 4) * p.num_kv_heads + g) * 16 + (slot & 15) : 0;
-    if constexpr (F8) {
-      // a row's PC lanes are consecutive and lane-aligned; every lane of the warp takes part
-      const uint32_t ak = dev::row_amax_bits<PC>(max(dev::f16x8_amax_bits(ka), dev::f16x8_amax_bits(kb)));
-      const uint32_t av = dev::row_amax_bits<PC>(max(dev::f16x8_amax_bits(va), dev::f16x8_amax_bits(vb)));
-      if (kv) {
-        const int sbk = dev::e4m3_scale_byte(ak), sbv = dev::e4m3_scale_byte(av);
-        uint2* dk = reinterpret_cast<uint2*>(p.cache_k + row * D);
-        uint2* dv = reinterpret_cast<uint2*>(p.cache_v + row * D);
-        dk[c0] = dev::e4m3_encode8(ka, sbk);
-        dk[c1] = dev::e4m3_encode8(kb, sbk);
-        dv[2 * pc] = dev::e4m3_encode8(va, sbv);
-        dv[2 * pc + 1] = dev::e4m3_encode8(vb, sbv);
-        if (pc == 0) {
-          unsigned char* rec = p.scales + ((slot >> 4) * p.num_kv_heads + g) * 32;
-          rec[slot & 15] = (unsigned char)sbk;
-          rec[16 + (slot & 15)] = (unsigned char)sbv;
-        }
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = i0 + u * kThreads + threadIdx.x, tb = i / per;
+      const int h = (int)((i - tb * per) / PC), pc = (int)(i % PC), g = h - p.num_q_heads;
+      const int64_t t = t0 + tb;
+      const int c0 = !INTER && pc < pieces ? pc : 2 * pc, c1 = !INTER && pc < pieces ? pc + half / 8 : 2 * pc + 1;
+      a[u] = b[u] = va[u] = vb[u] = make_uint4(0, 0, 0, 0);
+      slot[u] = -1;
+      if (i >= items) continue;
+      if (g < 0) {  // plain loads: q_out may be q
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + t * p.q_stride + (int64_t)h * D);
+        a[u] = src[c0];
+        b[u] = src[c1];
+      } else {
+        const __half* ks = p.k + t * p.k_stride + (int64_t)g * D;
+        const __half* vs = p.v + t * p.v_stride + (int64_t)g * D;
+        slot[u] = __ldg(p.slots + t);
+        a[u] = ld16(ks + 8 * c0);
+        b[u] = ld16(ks + 8 * c1);
+        va[u] = ld16(vs + 16 * pc);
+        vb[u] = ld16(vs + 16 * pc + 8);
       }
-    } else if (kv) {
-      uint4* dk = reinterpret_cast<uint4*>(p.cache_k + row * (2 * D));
-      uint4* dv = reinterpret_cast<uint4*>(p.cache_v + row * (2 * D));
-      dk[c0] = ka;
-      dk[c1] = kb;
-      dv[2 * pc] = va;
-      dv[2 * pc + 1] = vb;
+    }
+    if (i0 == 0) {
+      for (int i = threadIdx.x; i < n * half; i += kThreads) {
+        const int tb = i / half, k = i - tb * half;  // pair k: of piece k / 8, its pair k % 8
+        const uint64_t pos = (uint64_t)(int64_t)__ldg(p.positions + t0 + tb);
+        const int32_t turn = (int32_t)((pos * turns.turn[k]) >> 32);
+        float s, c;
+        sincospif((float)turn * 0x1p-31f, &s, &c);
+        reinterpret_cast<float2*>(&angle[tb][(k & 7) >> 1][k >> 3])[k & 1] = make_float2(c * p.out_scale, s * p.out_scale);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t i = i0 + u * kThreads + threadIdx.x, tb = i / per;
+      const int h = (int)((i - tb * per) / PC), pc = (int)(i % PC), g = h - p.num_q_heads;
+      const int64_t t = t0 + tb;
+      const bool in = i < items, rot = pc < pieces;
+      const int c0 = !INTER && rot ? pc : 2 * pc, c1 = !INTER && rot ? pc + half / 8 : 2 * pc + 1;
+      const bool kv = in && g >= 0 && slot[u] >= 0 && slot[u] < p.num_slots;
+      if (in && g == 0 && pc == 0 && slot[u] != -1 && !kv) dev::set_error(p.err, PKV_DEVERR_SLOT_RANGE);
+      if (in && rot) {
+        float cs[8], sn[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 x = angle[tb][j][pc];
+          cs[2 * j] = x.x;
+          sn[2 * j] = x.y;
+          cs[2 * j + 1] = x.z;
+          sn[2 * j + 1] = x.w;
+        }
+        if constexpr (INTER) rotate8_interleaved(a[u], b[u], cs, sn); else rotate8(a[u], b[u], cs, sn);
+      }
+      if (in && g < 0) {
+        uint4* dst = reinterpret_cast<uint4*>(p.q_out + (t * p.num_q_heads + h) * D);
+        dst[c0] = a[u];
+        dst[c1] = b[u];
+      }
+      const int64_t row = kv ? ((slot[u] >> 4) * p.num_kv_heads + g) * 16 + (slot[u] & 15) : 0;
+      if constexpr (F8) {
+        // a row's PC lanes are consecutive and lane-aligned; every lane of the warp takes part
+        const uint32_t ak = dev::row_amax_bits<PC>(max(dev::f16x8_amax_bits(a[u]), dev::f16x8_amax_bits(b[u])));
+        const uint32_t av = dev::row_amax_bits<PC>(max(dev::f16x8_amax_bits(va[u]), dev::f16x8_amax_bits(vb[u])));
+        if (kv) {
+          const int sbk = dev::e4m3_scale_byte(ak), sbv = dev::e4m3_scale_byte(av);
+          uint2* dk = reinterpret_cast<uint2*>(p.cache_k + row * D);
+          uint2* dv = reinterpret_cast<uint2*>(p.cache_v + row * D);
+          dk[c0] = dev::e4m3_encode8(a[u], sbk);
+          dk[c1] = dev::e4m3_encode8(b[u], sbk);
+          dv[2 * pc] = dev::e4m3_encode8(va[u], sbv);
+          dv[2 * pc + 1] = dev::e4m3_encode8(vb[u], sbv);
+          if (pc == 0) {
+            unsigned char* rec = p.scales + ((slot[u] >> 4) * p.num_kv_heads + g) * 32;
+            rec[slot[u] & 15] = (unsigned char)sbk;
+            rec[16 + (slot[u] & 15)] = (unsigned char)sbv;
+          }
+        }
+      } else if (kv) {
+        uint4* dk = reinterpret_cast<uint4*>(p.cache_k + row * (2 * D));
+        uint4* dv = reinterpret_cast<uint4*>(p.cache_v + row * (2 * D));
+        dk[c0] = a[u];
+        dk[c1] = b[u];
+        dv[2 * pc] = va[u];
+        dv[2 * pc + 1] = vb[u];
+      }
     }
   }
 }
@@ -192,8 +213,7 @@ __global__ void __launch_bounds__(256) positions_kernel(const int32_t* __restric
 
 template <int D>
 cudaError_t launch_rope(const RopeParams& p, const RopeTurns& turns, bool f8, bool inter, cudaStream_t s) {
-  const int64_t total = (int64_t)p.num_tokens * p.lanes_heads * (D / 16);
-  const dim3 grid((unsigned)((total + kThreads - 1) / kThreads)), block(kThreads);
+  const dim3 grid((unsigned)((p.num_tokens + p.tokens - 1) / p.tokens)), block(kThreads);
   if (f8) return inter ? launch_pdl(rope_append_kernel<D, true, true>, grid, block, 0, s, p, turns)
                        : launch_pdl(rope_append_kernel<D, true, false>, grid, block, 0, s, p, turns);
   return inter ? launch_pdl(rope_append_kernel<D, false, true>, grid, block, 0, s, p, turns)
@@ -337,13 +357,12 @@ extern "C" pkv_status pkv_rope_append(pkv_pool* pool, int32_t layer, const pkv_r
   p.rot_dim = rope->cfg.rot_dim;
   p.out_scale = (float)rope->cfg.output_scale;
   p.err = pool->dev_error;
-  // Head slots a token: one thread for all heads computes each angle once; with few tokens that leaves the GPU
-  // empty, so the heads are spread over more threads until every SM has two CTAs.
-  const int heads = p.num_q_heads + p.num_kv_heads;
-  const int64_t want = (int64_t)pool->num_sms * 2 * kThreads, one = (int64_t)num_tokens * (c.head_dim / 16);
-  p.lanes_heads = (int)std::min<int64_t>(heads, std::max<int64_t>(1, (want + one - 1) / one));
-  if ((int64_t)num_tokens * p.lanes_heads * (c.head_dim / 16) / kThreads >= (1ll << 31) - 1)
-    return fail(PKV_ERR_UNSUPPORTED, "too many tokens in one call");
+  // Two items a thread, in up to four tokens a CTA (larger CTAs start and end in coarser steps: 256 threads and twice
+  // the items took 13.3 us where these take 12.4, 8192 tokens of 12 / 2 heads at d 128); fewer while that would leave
+  // SMs without two CTAs.
+  const int64_t per = (int64_t)(p.num_q_heads + p.num_kv_heads) * (c.head_dim / 16);
+  const int64_t fill = std::max<int64_t>(1, 2 * 128 / per), spread = std::max<int64_t>(1, num_tokens / (2 * (int64_t)pool->num_sms));
+  p.tokens = (int)std::min<int64_t>(4, std::min(fill, spread));
   RopeTurns turns;
   std::copy(rope->turn, rope->turn + kMaxPairs, turns.turn);
   const bool f8 = c.kv_dtype == PKV_KV_E4M3, inter = rope->cfg.layout == PKV_ROPE_INTERLEAVED;
