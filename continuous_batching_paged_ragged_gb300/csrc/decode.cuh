@@ -1110,11 +1110,20 @@ struct Scheduler {
     if (lane == 0)
       for (int f = first; f < filled; ++f) dev::mbar_arrive(&sm.qfull[f % T::QD]);
   }
-  // Before the dependency wait: the static entries (they touch no counter).
+  // Tasks given out without the counter.  Behind a prefill kernel (late_wait) none: this CTA starts when that kernel
+  // leaves an SM, much later than others on short prompts, and a task of its own would wait for it (a pass of 83
+  // decode rows and two chunks, half of whose items are short, ended 14 us after its prefill).
+  __device__ __forceinline__ int given() const { return p.late_wait ? 0 : kStaticTasks * (int)gridDim.x; }
+  // Before the dependency wait: the static entries (they touch no counter); or, with no wait to come, a claim.
   __device__ void prologue() {
     n_tasks = __ldcg(&p.hdr->n_tasks);
     static_assert(kStaticTasks == 1, "one static task");
-    const int idx[kStaticTasks] = {(int)blockIdx.x};
+    int c = blockIdx.x;
+    if (p.late_wait) {
+      if (lane == 0) c = atomicAdd(&p.hdr->work, 1);
+      c = __shfl_sync(0xffffffffu, c, 0);
+    }
+    const int idx[kStaticTasks] = {c};
     last_idx = idx[0];
     publish(idx);
   }
@@ -1140,14 +1149,14 @@ struct Scheduler {
       if (last_idx + 2 * (int)gridDim.x >= n_tasks) {
         int seen = 0;
         if (lane == 0) seen = dev::ld_relaxed_gpu(&p.hdr->work);
-        out = kStaticTasks * (int)gridDim.x + __shfl_sync(0xffffffffu, seen, 0) >= n_tasks;
+        out = given() + __shfl_sync(0xffffffffu, seen, 0) >= n_tasks;
       }
       if (!out && !small && !cta_wait(&sm.qmid[(m - 1) % T::QD], ((m - 1) / T::QD) & 1, sm.abort, p.err)) return;
       const int gate = m - T::QD;
       if (gate >= 0 && !cta_wait(&sm.qempty[gate % T::QD], (gate / T::QD) & 1, sm.abort, p.err)) return;
       int c = 0;
       if (lane == 0 && !out) c = atomicAdd(&p.hdr->work, 1);
-      const int idx[1] = {out ? n_tasks : kStaticTasks * (int)gridDim.x + __shfl_sync(0xffffffffu, c, 0)};
+      const int idx[1] = {out ? n_tasks : given() + __shfl_sync(0xffffffffu, c, 0)};
       last_idx = idx[0];
       publish(idx);
     }

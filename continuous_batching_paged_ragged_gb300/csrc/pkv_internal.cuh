@@ -329,6 +329,14 @@ __device__ __forceinline__ void named_bar_arrive(int id, int count) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
+// True in one lane of the (converged) warp, the same one every time.  Code it guards is known to run in a single thread,
+// so that operands which are the same in every lane stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ---- 5th-generation tensor cores (tcgen05) and tensor memory -----------------------------------
 // Tensor memory (TMEM) is 128 lanes x 512 columns of 32-bit cells per SM.  An MMA with M = 128 writes
 // its fp32 accumulator row m to lane m, column n.  Warp w of a CTA may read or write lanes

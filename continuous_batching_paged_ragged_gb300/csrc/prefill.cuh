@@ -21,9 +21,11 @@
 //    store P as fp16 over the S they just read (tcgen05.st); the product takes P straight from tensor
 //    memory.  Per group the order is S(j), P(j)V, S(j + 1), P(j + 1)V, ...: while one group runs its
 //    softmax the tensor core works on the other group's products and scores.
-//  * Measured on GB300: one thread issues a 128 x 128 x 16 tcgen05.mma about every 113 cycles whatever N up
-//    to 128, two issuing warps one every ~64 (the tensor core's rate).  Hence one issuing warp per Q tile,
-//    and 128-wide score tiles (not 64).
+//  * Measured on GB300, cycles per 128 x 128 x 16 tcgen05.mma (64 at the tensor core's rate): one thread picked by its
+//    lane number issues one every 142 from shared memory (scores) and 96 with A in tensor memory (products),
+//    whatever N up to 128 -- the compiler moves every operand to the uniform registers again for each; picked by
+//    elect.sync, 107 and 70; two warps together 88 and 66 (both operands from shared memory are bound by its
+//    bandwidth).  Hence one issuing warp per Q tile, an elected thread, and 128-wide score tiles (not 64).
 //  * The running max is lazy: O (in TMEM) and the running sum are rescaled only when a row's max grows
 //    by more than 8 (a factor 256), which keeps P <= 256 and the arithmetic exact up to rounding.
 //  * Windowed instances (W): an item walks the K/V tiles that some of its positions see -- the sinks' tiles, then from
@@ -46,7 +48,7 @@ namespace {
 constexpr int kKSlots = 3;             // K ring depth
 constexpr int kVSlots = 2;             // V ring depth
 constexpr int kWG = 2;                 // softmax warpgroups (Q tiles per item) at most
-constexpr int kBarItem = 1, kBarQ = 2, kBarEpi = 3;  // named barriers (0 is __syncthreads)
+constexpr int kBarItem = 1, kBarQ = 2, kBarEpi = 3, kBarOut = 4;  // named barriers (0 is __syncthreads; kBarOut per group)
 constexpr float kRescaleLog2 = 8.f;    // lazy rescale threshold (log2 units)
 constexpr float kNoKeyMax = -1e30f;    // W: a row's running max while it has seen none of its keys (below any score)
 
@@ -256,12 +258,12 @@ __device__ void tma_warp(const PfParams& p, unsigned char* smem, const Bars& sh,
 }
 
 // ---- MMA warps: one per Q-tile group, each issuing its group's MMAs from one thread ------------------
-// Measured on GB300: one issuing thread sustains one 128 x 128 x 16 MMA per ~113 cycles, two issuing warps
-// together one per ~64 (the tensor core's rate).  So each group's scores and products come from its own warp;
+// Each group's scores and products come from its own warp (the issue rates are at the head of the file);
 // the K and V ring slots are released once both warps' MMAs that read them have completed (two arrivals).
 // The first MMA warp also hands out the items.
 template <int D, int G, int w, bool W>
-__device__ void mma_warp(const PfParams& p, unsigned char* smem, const Bars& sh, int lane, int n_items) {
+__device__ void mma_warp(const PfParams& p, unsigned char* smem, const Bars& sh, int lane, int n_items, int4 first_rec,
+                         int first_slot) {
   using T = PfTraits<D, G>;
   const uint32_t sbase = dev::smem_addr(smem);
   const uint32_t tmem = *sh.tmem_base;
@@ -280,8 +282,8 @@ __device__ void mma_warp(const PfParams& p, unsigned char* smem, const Bars& sh,
         const int idx = first ? (int)blockIdx.x : (int)gridDim.x + atomicAdd(&p.hdr->pwork, 1);
         int slot = -1;
         if (idx < n_items) {
-          rec = __ldg(p.items + idx);
-          slot = __ldg(p.items_slot + idx);
+          rec = first ? first_rec : __ldg(p.items + idx);
+          slot = first ? first_slot : __ldg(p.items_slot + idx);
         }
         *sh.item = rec;
         *sh.slot = slot;
@@ -310,7 +312,7 @@ __device__ void mma_warp(const PfParams& p, unsigned char* smem, const Bars& sh,
 
     auto issue_s = [&](int j) {  // S_w(u = j) = Q_w K^T; commits every earlier MMA of this warp too
       const uint64_t dk = dk0 + (uint64_t)((((gt + j) % kKSlots) * T::KVTILE) >> 4);
-      if (lane == 0) {
+      if (dev::elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           dev::umma_f16_ss(tmem + T::s_col(w), dq + (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
@@ -321,7 +323,7 @@ __device__ void mma_warp(const PfParams& p, unsigned char* smem, const Bars& sh,
     };
     auto issue_pv = [&](int j) {  // O_w (+)= P_w(j) V(j), P from tensor memory
       const uint64_t dv = dv0 + (uint64_t)((((gt + j) % kVSlots) * T::KVTILE) >> 4);
-      if (lane == 0) {
+      if (dev::elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < T::KEYS / 16; ++kk)
           dev::umma_f16_ts(tmem + T::s_col(w) + T::SO, tmem + T::s_col(w) + 8 * kk, dv + (uint64_t)((kk * 2048) >> 4),
@@ -331,7 +333,7 @@ __device__ void mma_warp(const PfParams& p, unsigned char* smem, const Bars& sh,
       __syncwarp();
     };
     auto commit = [&](uint64_t* bar) {
-      if (lane == 0) dev::umma_commit(bar);
+      if (dev::elect_one()) dev::umma_commit(bar);
       __syncwarp();
     };
 
@@ -407,21 +409,28 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
     const ItemGeo it = item_geo<T, W>(p, rec);
     const int slot = *sh.slot;
     const int n = max(0, min(it.te, wg ? it.n[1] : it.n[0]) - it.tb);  // this group's tiles of the entry
-    const int pos = r / G, hq = r % G;
+    const int pos = r / G;
     const int npos = wg ? it.npos[1] : it.npos[0];
     const bool valid = r < T::P * G && pos < npos;
     const int first_pos = wg * T::P;
     const int lim = valid ? it.w0 + first_pos + pos : 0;  // last key this row sees (padding rows: key 0)
     const int low = W && valid ? window_low(lim + 1, p.win.window) : 0;  // first key of its window
-    const size_t tok = (size_t)(it.t0 + first_pos + pos);
 
-    // ---- Q tile: row r = (position, head), 128-byte swizzle ----
+    // ---- Q tile: row = (position, head), 128-byte swizzle.  Consecutive lanes take consecutive chunks of a row (a
+    // row per lane would touch 32 lines a load, and the few KB of L1 beside the tiles hold none of them until the
+    // next: 2.8 us an item, against 1) ----
+    const int tr = threadIdx.x & 127;
+    // tile row x's place in q and out
+    auto row_at = [&](int x) {
+      return ((size_t)(it.t0 + first_pos + x / G) * p.num_q_heads + (size_t)it.g * G + x % G) * D;
+    };
     if (n > 0) {
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (tok * p.num_q_heads + (size_t)it.g * G + hq) * D);
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sQa + qtile_off(r, c)), "r"(v.x), "r"(v.y),
+      for (int i = 0; i < D / 8; ++i) {
+        const int x = (i * 128 + tr) / (D / 8), c = tr % (D / 8);
+        const bool live = x < T::P * G && x / G < npos;
+        const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(p.q + row_at(x)) + c) : make_uint4(0, 0, 0, 0);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sQa + qtile_off(x, c)), "r"(v.x), "r"(v.y),
                      "r"(v.z), "r"(v.w)
                      : "memory");
       }
@@ -483,6 +492,88 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
         // Common case (the reference is settled): one pass over S, both halves' P kept in registers and
         // stored only once neither half moves the row max past the lazy threshold, so S is still intact
         // for the two-pass path when one does.
+        if constexpr (W) {
+          // The one pass alone, its reference set ahead of the first tile and moved when a tile fails the check: the
+          // maximum comes from a loop of its own over S and the rescale runs as a loop too.  Most windowed work is a
+          // few tiles an item, where code run for the first time costs more than the second look at S.
+          auto one_pass = [&]() {
+            constexpr int NQ = T::KEYS / 32;  // 32-column quarters: the next one is on its way while one is computed
+            uint32_t s[2][32], pk[NQ][16];
+            const float nm = -m_ref;
+            bool ok = true;
+            dev::tmem_ld32(tl, s[0]);
+#pragma unroll
+            for (int c = 0; c < NQ; ++c) {
+              dev::tmem_wait_ld();
+              if (c + 1 < NQ) dev::tmem_ld32(tl + 32 * (c + 1), s[(c + 1) & 1]);
+              if (!ok) continue;
+              const uint32_t (&x)[32] = s[c & 1];
+              float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int e = 0; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], __uint_as_float(x[e]));
+              const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
+              ok = !__any_sync(0xffffffffu, mx > m_ref + kRescaleLog2);
+              if (!ok) continue;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float p0 = dev::ex2_approx(fmaf(__uint_as_float(x[2 * e]), p.scale_log2, nm));
+                const float p1 = dev::ex2_approx(fmaf(__uint_as_float(x[2 * e + 1]), p.scale_log2, nm));
+                sum4[e & 3] += p0 + p1;
+                const __half2 hh = __floats2half2_rn(p0, p1);
+                pk[c][e] = *reinterpret_cast<const uint32_t*>(&hh);
+              }
+            }
+            if (ok) {
+#pragma unroll
+              for (int c = 0; c < NQ; c += 2) {
+                uint32_t v[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = pk[c + (e >> 4)][e & 15];
+                dev::tmem_st32(tl + 16 * c, v);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sum4[i] = 0.f;
+            }
+            return ok;
+          };
+          auto row_max = [&]() {
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < T::KEYS; c += 32) {
+              uint32_t s[32];
+              dev::tmem_ld32(tl + c, s);
+              dev::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[e]));
+            }
+            return mx * p.scale_log2;
+          };
+          if (u == 0) m_ref = fmaxf(row_max(), kNoKeyMax);  // (the window of a row may begin in a later tile)
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) {  // with the reference moved the second passes
+            if (one_pass()) break;
+            const float mx = row_max();
+            const bool need = mx > m_ref + kRescaleLog2;
+            const float alpha = need ? exp2f(m_ref - mx) : 1.f;
+            if (u > 0) {
+#pragma unroll 1
+              for (int k = 0; k < D / 32; ++k) {
+                uint32_t o[32];
+                dev::tmem_ld32(tl + T::SO + 32 * k, o);
+                dev::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                dev::tmem_st32(tl + T::SO + 32 * k, o);
+              }
+            }
+            if (need) {
+              l *= alpha;
+              m_ref = mx;
+            }
+          }
+          return;
+        }
         bool done = false;
         if (u > 0) {
           bool ok;
@@ -534,7 +625,7 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
             }
           }
           if (u == 0) {
-            m_ref = W ? fmaxf(mx, kNoKeyMax) : mx;  // (the window of a row may begin in a later tile)
+            m_ref = mx;
           } else {
             const bool need = mx > m_ref + kRescaleLog2;
             if (__any_sync(0xffffffffu, need)) {
@@ -598,12 +689,13 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
       dev::mbar_arrive(&sh.p_ready[wg]);
     }
     // ---- epilogue: O / l -> fp16, or for a split item the chunk handshake ----
-    __half* dst = p.out + (tok * p.num_q_heads + (size_t)it.g * G + hq) * D;
     if (n > 0) {
       pf_wait(sh, &sh.pv_done[wg], (cw + n - 1) & 1, p.err);
       dev::tc_fence_after();
     }
-    auto store_row = [&](int k, const float (&v)[32]) {  // 32 output columns of this row, fp16
+    // The rows go out through the Q tile's shared memory (every product that read it has completed), so that
+    // consecutive lanes write consecutive chunks of a row.
+    auto stage_row = [&](int k, const float (&v)[32]) {  // 32 output columns of this row, fp16
 #pragma unroll
       for (int c8 = 0; c8 < 4; ++c8) {
         uint32_t h2[4];
@@ -612,7 +704,22 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
           const __half2 hh = __floats2half2_rn(v[c8 * 8 + 2 * e], v[c8 * 8 + 2 * e + 1]);
           h2[e] = *reinterpret_cast<const uint32_t*>(&hh);
         }
-        *reinterpret_cast<uint4*>(dst + 32 * k + 8 * c8) = make_uint4(h2[0], h2[1], h2[2], h2[3]);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(sQa + qtile_off(r, 4 * k + c8)), "r"(h2[0]),
+                     "r"(h2[1]), "r"(h2[2]), "r"(h2[3])
+                     : "memory");
+      }
+    };
+    auto write_rows = [&]() {
+      dev::named_bar_sync(kBarOut + wg, 128);
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        const int x = (i * 128 + tr) / (D / 8), c = tr % (D / 8);
+        if (x >= T::P * G || x / G >= npos) continue;
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(sQa + qtile_off(x, c)));
+        reinterpret_cast<uint4*>(p.out + row_at(x))[c] = v;
       }
     };
     if (!it.split) {
@@ -626,8 +733,9 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
           float v[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * il;
-          if (valid) store_row(k, v);
+          stage_row(k, v);
         }
+        write_rows();
       }
     } else {
       // The chunk that finishes first publishes its unnormalised (m, l, O); the other merges them in
@@ -699,8 +807,9 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
             const float a0 = it.chunk ? ot[e] : own, a1 = it.chunk ? own : ot[e];
             v[e] = (a0 * f0 + a1 * f1) * il;
           }
-          if (valid) store_row(k, v);
+          stage_row(k, v);
         }
+        if (npos > 0) write_rows();
         dev::named_bar_sync(kBarEpi, T::SOFTMAX_THREADS);
         if (threadIdx.x == 0) *const_cast<int2*>(sync) = make_int2(0, 0);  // ready for the next launch
       }
@@ -755,14 +864,24 @@ __global__ void __launch_bounds__(PfTraits<D, G>::THREADS, 1) prefill_kernel(con
     dev::tmem_alloc(sh.tmem_base, T::TMEM_COLS);
     dev::tmem_relinquish();
   }
+  // The plan's results are read before the dependency wait: the plan released its dependents only after its writes
+  // (and a fence), and every kernel between it and this one waited for it first.  An entry past the plan's items (the
+  // grid is no larger than the list) is never used.
+  const int planned = __ldcg(&p.hdr->n_items);
+  int4 first_rec = make_int4(-1, 0, 0, 0);
+  int first_slot = -1;
+  if (warp == T::MMA0 && lane == 0) {
+    first_rec = __ldcg(p.items + blockIdx.x);
+    first_slot = __ldcg(p.items_slot + blockIdx.x);
+  }
   dev::tc_fence_before();
   dev::griddep_wait();
   dev::griddep_launch_dependents();
   const bool poisoned = __syncthreads_or(threadIdx.x == 0 && dev::pool_poisoned(p.err));
   dev::tc_fence_after();
-  const int n_items = poisoned ? 0 : p.hdr->n_items;
-  if (warp == T::MMA0) mma_warp<D, G, 0, W>(p, smem, sh, lane, n_items);
-  else if (warp == T::MMA1) mma_warp<D, G, T::WG - 1, W>(p, smem, sh, lane, n_items);  // only with two groups
+  const int n_items = poisoned ? 0 : planned;
+  if (warp == T::MMA0) mma_warp<D, G, 0, W>(p, smem, sh, lane, n_items, first_rec, first_slot);
+  else if (warp == T::MMA1) mma_warp<D, G, T::WG - 1, W>(p, smem, sh, lane, n_items, first_rec, first_slot);  // only with two groups
   else if (warp == T::TMA) tma_warp<D, G, W>(p, smem, sh, lane);
   else softmax_group<D, G, W>(p, smem, sh, warp >> 2, warp, lane);
   dev::tc_fence_before();
