@@ -26,6 +26,10 @@
 // not evicted): a preempted request's full blocks stay registered while free (returned last block first,
 // so its prefix is evicted last); handing a block out evicts it; on readmission the request takes back the
 // longest registered prefix, leaving at least one token to compute.
+//
+// Forks: a running request may be continued by another from the tokens it has computed.  The two share its full blocks,
+// which are counted and return to the free list with their last holder.  Compaction: pkv_sched_tables lists every
+// block that requests hold, pkv_sched_remap takes over the blocks' new ids.
 #include <algorithm>
 #include <cstdint>
 #include <deque>
@@ -75,6 +79,7 @@ struct pkv_sched {
   bool prefix_caching = false;
   std::map<std::pair<int64_t, int64_t>, int32_t> cached;  // (request, block j) -> free block still holding it
   std::unordered_map<int32_t, std::pair<int64_t, int64_t>> block_key;  // the reverse map
+  std::unordered_map<int32_t, int32_t> shared;  // blocks that several requests hold -> how many
   std::deque<int32_t> free_list;
   std::vector<Req*> running;       // arrival (admission) order; back = newest
   std::deque<Req*> waiting;        // front = next to admit
@@ -146,6 +151,22 @@ struct pkv_sched {
   // Blocks back to the free list's tail; keep registers a preempted request's full blocks for prefix
   // caching and returns them last block first.
   void release(Req* r, bool keep = false) {
+    if (!shared.empty()) {  // blocks that another request still holds stay its
+      std::vector<int32_t> mine;
+      size_t kept = 0;
+      for (int32_t b : r->blocks) {
+        auto it = shared.find(b);
+        if (it == shared.end()) {
+          mine.push_back(b);
+          continue;
+        }
+        ++kept;
+        if (--it->second == 1) shared.erase(it);
+      }
+      // a prefix cache entry is the request's block number j: with blocks missing in front it keeps none
+      if (kept > 0) keep = false;
+      r->blocks.swap(mine);
+    }
     if (keep && prefix_caching) {
       for (size_t j = 0; j < r->blocks.size(); ++j) {
         if ((int64_t)(j + 1) * cfg.block_size <= r->num_computed) {
@@ -373,6 +394,85 @@ extern "C" pkv_status pkv_sched_abort(pkv_sched* s, int64_t req_id) {
   s->release(r);
   s->live.erase(it);
   delete r;
+  return PKV_OK;
+}
+
+extern "C" pkv_status pkv_sched_fork(pkv_sched* s, int64_t parent_id, int64_t child_id, int32_t max_output, int32_t* block) {
+  pkv::clear_error();
+  if (!s || !block) return fail(PKV_ERR_INVALID_ARG, "scheduler and block must be non-NULL");
+  if (s->alloc != PKV_ALLOC_ON_DEMAND || s->unit != PKV_UNIT_PASS)
+    return fail(PKV_ERR_UNSUPPORTED, "forks need blocks on demand and passes as the unit");
+  auto it = s->live.find(parent_id);
+  if (it == s->live.end()) return fail(PKV_ERR_NOT_FOUND, "unknown request id");
+  if (s->live.count(child_id)) return fail(PKV_ERR_INVALID_ARG, "duplicate request id");
+  Req* p = it->second;
+  if (p->status != Status::kRunning) return fail(PKV_ERR_INVALID_ARG, "the parent must be running");
+  if (max_output <= p->num_output) return fail(PKV_ERR_INVALID_ARG, "max_output must leave the child an output");
+  if ((int64_t)s->running.size() >= s->cfg.max_num_seqs) return fail(PKV_ERR_OUT_OF_RANGE, "max_num_seqs requests are running");
+  const int64_t bs = s->cfg.block_size;
+  if (((int64_t)p->prompt_len + max_output + bs - 1) / bs > s->cfg.num_blocks)
+    return fail(PKV_ERR_NO_BLOCKS, "request can never fit the pool");
+  const int64_t full = p->num_computed / bs;
+  const bool tail = p->num_computed % bs > 0;
+  if (tail && s->free_list.empty()) return fail(PKV_ERR_NO_BLOCKS, "no free block for the child's last tokens");
+  Req* c = new (std::nothrow) Req(*p);
+  if (!c) return fail(PKV_ERR_INVALID_ARG, "out of host memory");
+  c->id = child_id;
+  c->max_output = c->declared_output = max_output;
+  c->blocks.resize(full);
+  for (int32_t b : c->blocks) {
+    auto sh = s->shared.emplace(b, 1).first;
+    ++sh->second;
+  }
+  *block = -1;
+  if (tail) {
+    *block = s->take();
+    c->blocks.push_back(*block);
+  }
+  s->live[child_id] = c;
+  s->running.push_back(c);
+  return PKV_OK;
+}
+
+extern "C" int32_t pkv_sched_tables(const pkv_sched* s, int32_t max_rows, int32_t max_blocks_per_seq, int64_t* req_ids,
+                                    int32_t* block_tables, int32_t* width) {
+  if (!s) return 0;
+  size_t most = 1;
+  for (const Req* r : s->running) most = std::max(most, r->blocks.size());
+  if (width) *width = (int32_t)most;
+  const int32_t rows = (int32_t)s->running.size();
+  if (!block_tables || max_rows < rows || (size_t)std::max(max_blocks_per_seq, 0) < most) return rows;
+  for (int32_t b = 0; b < rows; ++b) {
+    const Req* r = s->running[b];
+    if (req_ids) req_ids[b] = r->id;
+    int32_t* row = block_tables + (size_t)b * max_blocks_per_seq;
+    std::copy(r->blocks.begin(), r->blocks.end(), row);
+    std::fill(row + r->blocks.size(), row + max_blocks_per_seq, -1);
+  }
+  return rows;
+}
+
+extern "C" pkv_status pkv_sched_remap(pkv_sched* s, const int32_t* remap) {
+  pkv::clear_error();
+  if (!s || !remap) return fail(PKV_ERR_INVALID_ARG, "scheduler and remap must be non-NULL");
+  std::vector<int32_t> from(s->cfg.num_blocks, -1);  // new id -> old id of the blocks held
+  for (const Req* r : s->running)
+    for (int32_t b : r->blocks) {
+      const int32_t n = remap[b];
+      if (n < 0 || n >= s->cfg.num_blocks || (from[n] != -1 && from[n] != b))
+        return fail(PKV_ERR_INVALID_ARG, "remap must give every held block a block of its own");
+      from[n] = b;
+    }
+  for (Req* r : s->running)
+    for (int32_t& b : r->blocks) b = remap[b];
+  std::unordered_map<int32_t, int32_t> shared;
+  for (const auto& kv : s->shared) shared[remap[kv.first]] = kv.second;
+  s->shared.swap(shared);
+  s->cached.clear();  // free blocks may have been written over
+  s->block_key.clear();
+  s->free_list.clear();
+  for (int32_t n = 0; n < s->cfg.num_blocks; ++n)
+    if (from[n] == -1) s->free_list.push_back(n);
   return PKV_OK;
 }
 

@@ -122,6 +122,9 @@ SIGNATURES = {
     "pkv_sched_set_prefix_caching": (ctypes.c_int, [_p, _i32]),
     "pkv_sched_step": (ctypes.c_int, [_p, ctypes.POINTER(pkv_step)]),
     "pkv_sched_abort": (ctypes.c_int, [_p, _i64]),
+    "pkv_sched_fork": (ctypes.c_int, [_p, _i64, _i64, _i32, ctypes.POINTER(_i32)]),
+    "pkv_sched_tables": (_i32, [_p, _i32, _i32, _p, _p, ctypes.POINTER(_i32)]),
+    "pkv_sched_remap": (ctypes.c_int, [_p, _p]),
     "pkv_sched_set_max_num_seqs": (ctypes.c_int, [_p, _i32]),
     "pkv_sched_get_stats": (None, [_p, ctypes.POINTER(pkv_sched_stats)]),
     "pkv_sched_done": (_i32, [_p]),
@@ -475,6 +478,24 @@ class Scheduler:
 
     def abort(self, req_id: int) -> None:
         _check(load().pkv_sched_abort(self.handle, req_id), "pkv_sched_abort")
+
+    def fork(self, parent_id: int, child_id: int, max_output: int) -> int:
+        """The child's own block for the parent's last tokens (to be copied), or -1."""
+        block = _i32(-1)
+        _check(load().pkv_sched_fork(self.handle, parent_id, child_id, max_output, ctypes.byref(block)), "pkv_sched_fork")
+        return block.value
+
+    def tables(self):
+        """(request ids, block tables [rows, width] padded with -1) of everything the running requests hold."""
+        width = _i32(0)
+        rows = load().pkv_sched_tables(self.handle, 0, 0, None, None, ctypes.byref(width))
+        ids, tables = np.empty(rows, dtype=np.int64), np.full((rows, width.value), -1, dtype=np.int32)
+        load().pkv_sched_tables(self.handle, rows, width.value, ids.ctypes.data, tables.ctypes.data, None)
+        return ids, tables
+
+    def remap(self, remap) -> None:
+        arr = np.ascontiguousarray(np.asarray(remap, dtype=np.int32))
+        _check(load().pkv_sched_remap(self.handle, arr.ctypes.data), "pkv_sched_remap")
 
     def set_max_num_seqs(self, n: int) -> None:
         _check(load().pkv_sched_set_max_num_seqs(self.handle, n), "pkv_sched_set_max_num_seqs")

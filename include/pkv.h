@@ -530,6 +530,27 @@ pkv_status pkv_sched_set_prefix_caching(pkv_sched* s, int32_t enable);
 /* Run one pass; fills *out (num_seqs may be 0 when nothing is left to do). */
 pkv_status pkv_sched_step(pkv_sched* s, pkv_step* out);
 pkv_status pkv_sched_abort(pkv_sched* s, int64_t req_id);
+/* Continue running request parent_id as child_id as well, between passes: the child has the parent's prompt,
+ * outputs so far and computed tokens, and runs from the next pass on to max_output outputs in all (more than the
+ * parent has).  They share the parent's full blocks, counted: a shared block is freed with its last holder.  If the
+ * parent's computed tokens end inside a block, *block is the child's own block for them, whose rows have to be copied
+ * before the next pass (pkv_fork_rows, or pkv_copy_blocks), else -1.  On demand and UNIT_PASS only
+ * (PKV_ERR_UNSUPPORTED).  Refused, with nothing changed: an unknown parent (PKV_ERR_NOT_FOUND), one that is
+ * not running or a child id in use (PKV_ERR_INVALID_ARG), max_num_seqs requests running already
+ * (PKV_ERR_OUT_OF_RANGE), no free block or a child that could never fit (PKV_ERR_NO_BLOCKS).  A preempted request
+ * that shared blocks keeps none of them registered for prefix caching; the statistics count a shared block for each
+ * of its holders. */
+pkv_status pkv_sched_fork(pkv_sched* s, int64_t parent_id, int64_t child_id, int32_t max_output, int32_t* block);
+/* Every running request's blocks (reserved ones included), for pkv_compact: returns the number of running requests and
+ * sets *width (may be NULL) to the most blocks one holds (at least 1); if block_tables is non-NULL and
+ * max_rows and max_blocks_per_seq hold them, fills block_tables [rows][max_blocks_per_seq] (-1 padded) and req_ids
+ * [rows] (may be NULL). */
+int32_t pkv_sched_tables(const pkv_sched* s, int32_t max_rows, int32_t max_blocks_per_seq, int64_t* req_ids,
+                         int32_t* block_tables, int32_t* width);
+/* Take over a compaction's remap (host copy, [num_blocks]): every held block b becomes remap[b], the others are free in
+ * ascending order, and prefix caching forgets what free blocks held.  A remap that does not give every held block a
+ * block of its own is refused (PKV_ERR_INVALID_ARG) with nothing changed. */
+pkv_status pkv_sched_remap(pkv_sched* s, const int32_t* remap);
 pkv_status pkv_sched_set_max_num_seqs(pkv_sched* s, int32_t max_num_seqs);
 void pkv_sched_get_stats(const pkv_sched* s, pkv_sched_stats* out);
 /* 1 when no request is running or waiting. */
