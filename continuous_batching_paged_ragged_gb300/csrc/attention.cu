@@ -195,8 +195,10 @@ __device__ __forceinline__ void for_row_items(const PlanParams& p, int b, F fn) 
   for (int qb = 0; qb * p.prefill_pos < q_len; ++qb) {
     const int npos = min(p.prefill_pos, q_len - qb * p.prefill_pos);
     const int w = ctx - q_len + qb * p.prefill_pos;
-    const VisibleUnits vis = visible_units(w + npos, window_low(w + 1, p.win.window), p.win.sinks, p.prefill_keys);
-    fn(vis.n, npos, q0 + qb * p.prefill_pos, w);
+    int keys = w + npos;
+    if (p.win.window != kNoWindow)  // the item's tiles are packed from the blocks it sees
+      keys = visible_units(w + npos, window_low(w + 1, p.win.window), p.win.sinks, kBS).n * kBS;
+    fn((keys + p.prefill_keys - 1) / p.prefill_keys, npos, q0 + qb * p.prefill_pos, w);
   }
 }
 

@@ -28,9 +28,9 @@
 //    bandwidth).  Hence one issuing warp per Q tile, an elected thread, and 128-wide score tiles (not 64).
 //  * The running max is lazy: O (in TMEM) and the running sum are rescaled only when a row's max grows
 //    by more than 8 (a factor 256), which keeps P <= 256 and the arithmetic exact up to rounding.
-//  * Windowed instances (W): an item walks the K/V tiles that some of its positions see -- the sinks' tiles, then from
-//    the window of its first position on -- and masks each row's own window.  Blocks that none of them sees are not
-//    read (their table entries may name none): their boxes are loaded from outside the tensor map, as zeros.
+//  * Windowed instances (W): an item's K/V tiles are packed from the blocks that some of its positions see -- the
+//    sinks' blocks, then those from the window of its first position on -- and each row's own window is masked.  The
+//    other blocks are not read (their table entries may name none), and a few sinks cost a block and not a tile.
 //  * Items are taken longest first (the plan sorts them by K/V tile count) from a global counter.
 #pragma once
 
@@ -149,13 +149,9 @@ struct ItemGeo {
   int split, chunk;     // split-KV: this entry is chunk `chunk` of 2
   int tb, te;           // K/V tiles [tb, te) of the item that this entry processes
   int low;              // W: first key of the first position's window
-  VisibleUnits vis;     // W: which K/V tiles of the row are the item's tiles 0 .. n_all - 1
+  VisibleUnits vis;     // W: the row's blocks that make up the item's tiles, in order
   int tail;             // keys in the item's last tile
 };
-
-// The row's K/V tile that is the item's tile j.
-template <bool W>
-__device__ __forceinline__ int row_tile(const ItemGeo& it, int j) { return W ? it.vis.row_unit(j) : j; }
 
 
 template <class T, bool W>
@@ -173,19 +169,20 @@ __device__ __forceinline__ ItemGeo item_geo(const PfParams& p, const int4 rec) {
   it.kend_all = 0;
   it.zfill_wg = 0;
   it.low = W ? window_low(it.w0 + 1, p.win.window) : 0;
-  it.vis = W ? visible_units(it.w0 + npos, it.low, p.win.sinks, T::KEYS) : VisibleUnits{0, 0, 0};
+  it.vis = W ? visible_units(it.w0 + npos, it.low, p.win.sinks, kBS) : VisibleUnits{0, 0, 0};
 #pragma unroll
   for (int w = 0; w < kWG; ++w) {
     it.npos[w] = w < T::WG ? max(0, min(P, npos - w * P)) : 0;
     const int kend = it.w0 + w * P + it.npos[w];
-    it.n[w] = it.npos[w] > 0 ? (kend + T::KEYS - 1) / T::KEYS - it.vis.skip : 0;
+    const int keys = W ? ((kend + kBS - 1) / kBS - it.vis.skip) * kBS : kend;  // (W: of whole blocks)
+    it.n[w] = it.npos[w] > 0 ? (keys + T::KEYS - 1) / T::KEYS : 0;
     if (it.npos[w] > 0) {
       it.n_all = it.n[w];
       it.kend_all = kend;
       it.zfill_wg = w;
     }
   }
-  it.tail = it.kend_all - (it.n_all - 1 + it.vis.skip) * T::KEYS;
+  it.tail = it.kend_all - it.vis.skip * kBS - (it.n_all - 1) * T::KEYS;
   const int h = (it.n_all + 1) / 2;  // the first chunk takes the extra tile
   it.tb = it.split && it.chunk ? h : 0;
   it.te = it.split && !it.chunk ? h : it.n_all;
@@ -207,15 +204,14 @@ __device__ void tma_warp(const PfParams& p, unsigned char* smem, const Bars& sh,
     if (rec.x < 0) break;
     const ItemGeo it = item_geo<T, W>(p, rec);
     const int n = it.te - it.tb;  // tiles of this entry: item tiles tb .. te - 1
-    const int nblk = (it.kend_all + kBS - 1) / kBS;
+    const int nblk = W ? it.vis.n : (it.kend_all + kBS - 1) / kBS;
     const int32_t* bt = p.block_tables + (int64_t)it.row * p.max_blocks;
     auto load_ids = [&](int u) {
-      const int j = row_tile<W>(it, it.tb + u);  // lane i < blocks of tile j: physical id of the tile's block i
+      const int j = it.tb + u;  // lane i < blocks of tile j: physical id of the tile's block i
       int id = 0;
-      const int b = j * BPT + lane;
-      if (W && (b + 1) * kBS <= it.low && b * kBS >= p.win.sinks) return -1;  // no position of the item sees it
       if (lane < min(BPT, nblk - j * BPT)) {
-        id = __ldg(bt + j * BPT + lane);
+        const int b = j * BPT + lane;
+        id = __ldg(bt + (W ? it.vis.row_unit(b) : b));
         if (id < 0 || id >= p.num_blocks) {
           dev::set_error(p.err, PKV_DEVERR_BLOCK_RANGE);
           id = 0;
@@ -227,7 +223,7 @@ __device__ void tma_warp(const PfParams& p, unsigned char* smem, const Bars& sh,
     // a ring-length earlier from that slot have completed.  One 2 KB box (16 keys x 64 columns) per lane:
     // a single issuing thread would be the bottleneck.
     auto issue = [&](int u, bool v, int id) {
-      const int j = row_tile<W>(it, it.tb + u), gi = gt + u;
+      const int j = it.tb + u, gi = gt + u;
       const int slots = v ? kVSlots : kKSlots;
       const int slot = gi % slots;
       if (gi >= slots) pf_wait(sh, v ? &sh.vfree[slot] : &sh.kfree[slot], ((gi - slots) / slots) & 1, p.err);
@@ -239,10 +235,9 @@ __device__ void tma_warp(const PfParams& p, unsigned char* smem, const Bars& sh,
       __syncwarp();
       const int blk = lane / T::DH, h = lane % T::DH;
       const int bid = __shfl_sync(0xffffffffu, id, blk & 31);
-      // (rows below the map's first are outside it and arrive as zeros, all 16)
-      const int row = W && bid < 0 ? -kBS : row0 + (bid * p.num_kv_heads + it.g) * kBS;
       if (lane < nb * T::DH)
-        dev::tma_load_2d(dst + h * (T::KEYS * 128) + blk * 2048, &p.kv_map, h * 64, row, full, pol);
+        dev::tma_load_2d(dst + h * (T::KEYS * 128) + blk * 2048, &p.kv_map, h * 64,
+                         row0 + (bid * p.num_kv_heads + it.g) * kBS, full, pol);
     };
     // K runs one tile ahead of V: a K slot is released by the scores, earlier than a V slot by the products
     int id_next = n > 0 ? load_ids(0) : 0, id_prev = 0;
@@ -375,21 +370,32 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
   return m;
 }
 
-// W: -infinity over the scores that this thread's row (TMEM lane) does not see: of its tile's keys e it sees those with
-// e <= lim and (e >= low or e < sinks).
-__device__ __forceinline__ void mask_scores(uint32_t taddr, int keys, int lim, int low, int sinks) {
+// W: -infinity over the scores that this thread's row (TMEM lane) does not see, and the maximum of the others.  Its
+// tile's keys are the blocks b0, b0 + 1, .. of vis; it sees the keys k <= lim with k >= low or k < sinks.
+__device__ __forceinline__ float mask_scores(uint32_t taddr, int keys, const VisibleUnits& vis, int b0, int lim, int low,
+                                             int sinks) {
+  float mx = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < keys; c += 32) {
-    const uint32_t sees = low_bits(lim + 1 - c) & (~low_bits(low - c) | low_bits(sinks - c));
-    if (__all_sync(0xffffffffu, sees == 0xffffffffu)) continue;
+    uint32_t sees = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k0 = vis.row_unit(b0 + c / kBS + h) * kBS;
+      const uint32_t m = low_bits(lim + 1 - k0) & (~low_bits(low - k0) | low_bits(sinks - k0));
+      sees |= (m & 0xffffu) << (16 * h);
+    }
     uint32_t s[32];
     dev::tmem_ld32(taddr + c, s);
     dev::tmem_wait_ld();
 #pragma unroll
-    for (int e = 0; e < 32; ++e) s[e] = sees >> e & 1 ? s[e] : 0xff800000u;
-    dev::tmem_st32(taddr + c, s);
+    for (int e = 0; e < 32; ++e) {
+      s[e] = sees >> e & 1 ? s[e] : 0xff800000u;
+      mx = fmaxf(mx, __uint_as_float(s[e]));
+    }
+    if (!__all_sync(0xffffffffu, sees == 0xffffffffu)) dev::tmem_st32(taddr + c, s);
   }
   dev::tmem_wait_st();
+  return mx;
 }
 
 // ---- softmax warpgroups: one S / O row per thread ---------------------------------------------------
@@ -413,7 +419,9 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
     const int npos = wg ? it.npos[1] : it.npos[0];
     const bool valid = r < T::P * G && pos < npos;
     const int first_pos = wg * T::P;
-    const int lim = valid ? it.w0 + first_pos + pos : 0;  // last key this row sees (padding rows: key 0)
+    // last key this row sees (padding rows: key 0; W: all of the item's, since a row that sees no key of a tile is
+    // masked there, and would move its reference at every tile that is not)
+    const int lim = valid ? it.w0 + first_pos + pos : W ? it.kend_all - 1 : 0;
     const int low = W && valid ? window_low(lim + 1, p.win.window) : 0;  // first key of its window
 
     // ---- Q tile: row = (position, head), 128-byte swizzle.  Consecutive lanes take consecutive chunks of a row (a
@@ -444,12 +452,14 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
       // S(j) written; its commit also covers the product of tile j - 1, so O is settled
       pf_wait(sh, &sh.s_done[wg], c & 1, p.err);
       dev::tc_fence_after();
-      const int kb = row_tile<W>(it, j) * T::KEYS;
+      const int b0 = j * (T::KEYS / kBS);  // W: the tile's first block
+      const int kb = W ? it.vis.row_unit(b0) * kBS : j * T::KEYS;
       // Whether every valid row of the warp sees the whole tile (warp-uniform): the causal mask costs a
       // compare and a select per score, so only the tiles that reach a row's diagonal take the masked code.
       // Then every key of the tile is one of the item's (the TMA wrote it), and the warp's padding rows
       // (zero q) score 0 on each.  A warp of padding rows alone keeps the mask (key 0 only).
-      const bool all = kb + T::KEYS - 1 <= lim && (!W || kb >= low || kb + T::KEYS <= p.win.sinks);
+      const bool all = kb + T::KEYS - 1 <= lim && (!W || (kb >= low && (b0 >= it.vis.head || it.vis.skip == 0)) ||
+                                                   kb + T::KEYS <= min(p.win.sinks, it.vis.head * kBS));
       const bool full = __any_sync(0xffffffffu, valid) && __all_sync(0xffffffffu, !valid || all);
       float sum4[4] = {0.f, 0.f, 0.f, 0.f};
       auto tile = [&](auto full_tag) {
@@ -493,9 +503,9 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
         // stored only once neither half moves the row max past the lazy threshold, so S is still intact
         // for the two-pass path when one does.
         if constexpr (W) {
-          // The one pass alone, its reference set ahead of the first tile and moved when a tile fails the check: the
-          // maximum comes from a loop of its own over S and the rescale runs as a loop too.  Most windowed work is a
-          // few tiles an item, where code run for the first time costs more than the second look at S.
+          // The one pass alone, its reference set ahead of the first tile and moved when a tile fails the check, by
+          // loops that stay loops: most windowed work is a few tiles an item, where code run for the first time costs
+          // more than the second look at S.
           auto one_pass = [&]() {
             constexpr int NQ = T::KEYS / 32;  // 32-column quarters: the next one is on its way while one is computed
             uint32_t s[2][32], pk[NQ][16];
@@ -537,40 +547,36 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
             }
             return ok;
           };
-          auto row_max = [&]() {
-            float mx = -INFINITY;
+          // t = 0: the mask (up to three edges a row, laid over S in tensor memory so that the softmax exists once) where
+          // a tile needs one, and the first tile's reference; t = 1, after a tile that failed the check: the reference
+          // moved, O rescaled, and then the pass succeeds.
 #pragma unroll 1
-            for (int c = 0; c < T::KEYS; c += 32) {
-              uint32_t s[32];
-              dev::tmem_ld32(tl + c, s);
-              dev::tmem_wait_ld();
+          for (int t = 0; t < 2; ++t) {
+            if (t > 0 || u == 0 || !full) {
+              const float mx = mask_scores(tl, T::KEYS, it.vis, b0, lim, low, p.win.sinks) * p.scale_log2;
+              if (t == 0) {
+                if (u == 0) m_ref = fmaxf(mx, kNoKeyMax);  // (a row's window may begin in a later tile)
+              } else {
+                const bool need = mx > m_ref + kRescaleLog2;
+                const float alpha = need ? exp2f(m_ref - mx) : 1.f;
+                if (u > 0) {
+#pragma unroll 1
+                  for (int k = 0; k < D / 32; ++k) {
+                    uint32_t o[32];
+                    dev::tmem_ld32(tl + T::SO + 32 * k, o);
+                    dev::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[e]));
-            }
-            return mx * p.scale_log2;
-          };
-          if (u == 0) m_ref = fmaxf(row_max(), kNoKeyMax);  // (the window of a row may begin in a later tile)
-#pragma unroll 1
-          for (int t = 0; t < 2; ++t) {  // with the reference moved the second passes
-            if (one_pass()) break;
-            const float mx = row_max();
-            const bool need = mx > m_ref + kRescaleLog2;
-            const float alpha = need ? exp2f(m_ref - mx) : 1.f;
-            if (u > 0) {
-#pragma unroll 1
-              for (int k = 0; k < D / 32; ++k) {
-                uint32_t o[32];
-                dev::tmem_ld32(tl + T::SO + 32 * k, o);
-                dev::tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                dev::tmem_st32(tl + T::SO + 32 * k, o);
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                    dev::tmem_st32(tl + T::SO + 32 * k, o);
+                  }
+                }
+                if (need) {
+                  l *= alpha;
+                  m_ref = mx;
+                }
               }
             }
-            if (need) {
-              l *= alpha;
-              m_ref = mx;
-            }
+            if (one_pass()) break;
           }
           return;
         }
@@ -656,18 +662,11 @@ __device__ void softmax_group(const PfParams& p, unsigned char* smem, const Bars
           }
         }
       };
-      if constexpr (W) {
-        // A windowed row's mask has up to three edges; it is laid over S in tensor memory ahead of the tile's one
-        // code path.
-        if (!full) mask_scores(tl, T::KEYS, lim - kb, low - kb, p.win.sinks - kb);
-        tile(std::true_type{});
-      } else {
-        if (full) tile(std::true_type{}); else tile(std::false_type{});
-      }
+      if (W || full) tile(std::true_type{}); else tile(std::false_type{});
       l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
       // ---- the item's last tile: V rows past its keys hold stale bytes; zero them (0 * NaN = NaN) ----
       if (wg == it.zfill_wg && j == it.n_all - 1) {
-        const int kl = it.kend_all - kb;
+        const int kl = it.tail;
         if (kl < T::KEYS) {
           const int gi = gt + u, vs = gi % kVSlots;
           pf_wait(sh, &sh.vfull[vs], (gi / kVSlots) & 1, p.err);
