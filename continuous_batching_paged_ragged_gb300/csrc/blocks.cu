@@ -395,11 +395,17 @@ __device__ void plan_moves(const CompactParams& p, const uint32_t* bits) {
 }
 
 __device__ __forceinline__ void mark(const CompactParams& p, uint32_t* bits, int64_t first, int64_t step) {
-  for (int64_t i = first; i < p.entries; i += step) {
-    const int id = __ldg(p.tables + i);
-    if (id == -1) continue;
-    if (id < 0 || id >= p.num_blocks) dev::set_error(p.err, PKV_DEVERR_BLOCK_RANGE);
-    else atomicOr(bits + (id >> 5), 1u << (id & 31));
+  constexpr int U = 4;  // loads in flight a thread
+  for (int64_t i0 = first; i0 < p.entries; i0 += U * step) {
+    int id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) id[u] = i0 + u * step < p.entries ? __ldg(p.tables + i0 + u * step) : -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (id[u] == -1) continue;
+      if (id[u] < 0 || id[u] >= p.num_blocks) dev::set_error(p.err, PKV_DEVERR_BLOCK_RANGE);
+      else atomicOr(bits + (id[u] >> 5), 1u << (id[u] & 31));
+    }
   }
 }
 
@@ -456,14 +462,6 @@ __global__ void __launch_bounds__(kWorkers * 32) compact_move_kernel(const Block
 }
 
 // ---- host -----------------------------------------------------------------------------------------
-pkv_status check_device(const pkv_pool* pool) {
-  int device = -1;
-  const cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  if (device != pool->device) return fail(PKV_ERR_INVALID_ARG, "the pool's device must be the current device");
-  return PKV_OK;
-}
-
 // Under PKV_VALIDATE=1 (and outside a capture): n int32 of `src` on the host, after the stream's earlier work.
 pkv_status fetch_for_validation(const int32_t* src, size_t n, void* stream, std::vector<int32_t>* out, bool* ran) {
   *ran = false;
@@ -632,7 +630,9 @@ extern "C" pkv_status pkv_compact(pkv_pool* pool, const int32_t* block_tables, i
   const size_t smem = ((size_t)nb + 31) / 32 * 4;
   int launches = 0;
   cudaError_t e;
-  if (smem <= 48 * 1024 && p.entries <= 64 * 1024) {
+  // One CTA marks up to 16 K entries in a few microseconds; past that (or a bitmap that shared memory does not hold) two
+  // more launches spread the marking over the GPU.
+  if (smem <= 48 * 1024 && p.entries <= 16 * 1024) {
     e = launch_pdl(compact_plan_kernel, dim3(1), dim3(kPlanThreads), smem, s, p);
     launches = 1;
   } else {

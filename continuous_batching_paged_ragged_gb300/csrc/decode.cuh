@@ -319,7 +319,7 @@ struct Streamer {
   static __device__ __forceinline__ int runs(const TaskView& v) { return v.t >= 0 ? 2 * v.nbw : 0; }
   __device__ __forceinline__ int block_pos(const TaskView& v, int j) const {
     const int b = v.bw + T::NW * j;  // of the split
-    const int gap = W && b >= (v.jump & 31) ? v.jump >> 5 : 0;
+    const int gap = W && b >= (v.jump & 31) ? (int)((uint32_t)v.jump >> 5) : 0;
     return (v.base + b + gap) * kBS;
   }
   // Run r of the warp's stream within a task: the lean blocks go in pairs, K of both then V of both; the rest
@@ -1070,7 +1070,7 @@ struct Scheduler {
         nb = min(size, vis.n - s * size);
         if constexpr (W) {  // the split's blocks ahead of the gap: none, some, or all (then it has no gap)
           const int ahead = max(0, vis.head - s * size);
-          if (ahead < nb) jump = ahead | vis.skip << 5;
+          if (ahead < nb) jump = (int)((uint32_t)ahead | (uint32_t)vis.skip << 5);
         }
         if (lane < nb) {
           int v = id[j];

@@ -84,6 +84,8 @@ pkv_status encode_f16_rows(CUtensorMap* map, void* base, uint64_t rows, int head
 // sub-tiles of 16 rows x 64 values (128-byte swizzle), sub-tile h at 2048 h bytes -- the layout of head_dim / 64
 // boxes of the 2-D map side by side, in one copy.
 pkv_status encode_f16_runs(CUtensorMap* map, void* base, uint64_t rows, int head_dim);
+// Refuses a call made while another device than the pool's is current.
+pkv_status check_device(const pkv_pool* pool);
 // The PKV_VALIDATE=1 host check of a call's device metadata (a no-op otherwise); null pointers are skipped.  Blocks
 // that no new token of their row sees behind `window` and `sinks` are not looked at; with none_ok (the slot mapping,
 // which knows no window) an entry of -1 in front of the row's new tokens passes.

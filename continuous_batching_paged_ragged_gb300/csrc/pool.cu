@@ -151,6 +151,14 @@ static size_t cache_bytes_of(const pkv_config* c) {
   return (values_bytes_of(c) + scales + 255) / 256 * 256;
 }
 
+pkv_status check_device(const pkv_pool* pool) {
+  int device = -1;
+  const cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (device != pool->device) return fail(PKV_ERR_INVALID_ARG, "the pool's device must be the current device");
+  return PKV_OK;
+}
+
 // PKV_VALIDATE=1 (read at every call): the device metadata of a call are copied to the host and checked
 // before anything is launched -- query_start_loc from 0 to num_tokens without decreasing, 1 <= q_len <=
 // ctx <= max_blocks * block_size per row, every block id a row's context reaches in [0, num_blocks), every

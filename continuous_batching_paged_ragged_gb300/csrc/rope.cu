@@ -304,6 +304,10 @@ extern "C" pkv_status pkv_positions(pkv_pool* pool, const int32_t* context_lens,
   if (num_seqs < 1) return fail(PKV_ERR_INVALID_ARG, "tokens without rows");
   if (!context_lens || !query_start_loc || !positions)
     return fail(PKV_ERR_INVALID_ARG, "metadata pointers must be non-NULL");
+  pkv_status st = check_device(pool);
+  if (st == PKV_OK) st = validate_metadata(pool, nullptr, 0x7FFFFFF, context_lens, query_start_loc, num_seqs, num_tokens, nullptr,
+                                           stream);
+  if (st != PKV_OK) return st;
   const int blocks = std::min((num_tokens + 255) / 256, pool->num_sms * 8);
   const cudaError_t e = launch_pdl(positions_kernel, dim3(blocks), dim3(256), 0, (cudaStream_t)stream, context_lens,
                                    query_start_loc, (int)num_seqs, (int)num_tokens, positions, pool->dev_error);
@@ -335,7 +339,8 @@ extern "C" pkv_status pkv_rope_append(pkv_pool* pool, int32_t layer, const pkv_r
   if ((q && (q_stride < qw || q_stride % 8 != 0)) || k_stride < kw || k_stride % 8 != 0 || v_stride < kw || v_stride % 8 != 0)
     return fail(PKV_ERR_INVALID_ARG, "strides must be multiples of 8 and hold a token's heads");
   if (q && q == q_out && q_stride != qw) return fail(PKV_ERR_INVALID_ARG, "q_out may be q only when q is packed");
-  pkv_status st = validate_metadata(pool, nullptr, 0, nullptr, nullptr, 0, num_tokens, slot_mapping, stream);
+  pkv_status st = check_device(pool);
+  if (st == PKV_OK) st = validate_metadata(pool, nullptr, 0, nullptr, nullptr, 0, num_tokens, slot_mapping, stream);
   if (st != PKV_OK) return st;
   RopeParams p;
   p.q = static_cast<const __half*>(q);

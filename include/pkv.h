@@ -257,7 +257,8 @@ pkv_status pkv_attention_append(pkv_pool* pool, int32_t layer, const void* q, co
  *   - Keys and values that a query does not see have no part in its result, whatever they hold, with one
  *     exception: in a row of 16 or more new tokens, a non-finite value (of V) that is seen by one of the row's
  *     queries, or shares a 16-token block with one that is, may reach the row's other queries.
- *   - A window at least as long as every context gives the bits of a plan without one.
+ *   - A row whose contexts the window holds whole gives the bits of a plan without one.
+ *   - pkv_attention_noalloc knows no window: it attends whole contexts.
  * window >= 1, sinks >= 0 (else PKV_ERR_INVALID_ARG, and 0 bytes). */
 size_t pkv_attention_window_workspace_bytes(const pkv_pool* pool, int32_t num_seqs, int32_t num_tokens,
                                             int32_t max_blocks_per_seq, int32_t window, int32_t sinks);
@@ -424,8 +425,8 @@ pkv_status pkv_compact(pkv_pool* pool, const int32_t* block_tables, int32_t max_
  * clears the bit and the pass is planned again. */
 pkv_status pkv_debug_expire_wait(pkv_pool* pool, int64_t limit_ns, void* stream);
 
-/* Number of kernel launches the last successful pkv_append / pkv_attention_plan / pkv_attention /
- * pkv_slot_mapping call on `pool` enqueued (for accounting; host-side counter). */
+/* Number of kernel launches the last successful call on `pool` that launches any enqueued (for accounting; host-side
+ * counter). */
 int32_t pkv_last_launch_count(const pkv_pool* pool);
 
 /* Message for the last failed call on this thread ("" if none). */

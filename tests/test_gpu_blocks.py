@@ -202,9 +202,9 @@ def test_compact(cuda, built, kv, layers, hkv, d, blocks, rows, width, used):
         assert p.check() == 0
 
 
-@pytest.mark.parametrize("blocks,rows,width", [(420000, 4, 100), (3000, 300, 300)])
+@pytest.mark.parametrize("blocks,rows,width", [(420000, 4, 100), (3000, 300, 300), (3000, 128, 128), (3000, 129, 127)])
 def test_compact_large_pools_and_tables(cuda, built, blocks, rows, width):
-    """The bitmap in the workspace: a pool past 48 KB of bits, and tables past 64 K entries."""
+    """The bitmap in the workspace: a pool past 48 KB of bits, and tables past 16 K entries (and at them)."""
     rng = np.random.default_rng(1)
     tables = rng.integers(-1, blocks, (rows, width)).astype(np.int32)
     tables[0, 0], tables[1, 1], tables[2, 2] = blocks - 1, 0, -1

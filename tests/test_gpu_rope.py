@@ -152,7 +152,7 @@ def test_in_place_keys_alone_and_far_slots(cuda, built):
     assert torch.equal(c.cache_view().view(torch.int16), want.view(torch.int16))
 
 
-def test_positions(cuda, built):
+def test_positions(cuda, built, monkeypatch):
     pool = _pool(4, 2, 64, 4, layers=1)
     ctx, q_lens = [1, 700, 33, 16], [1, 300, 33, 2]
     starts = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
@@ -165,6 +165,10 @@ def test_positions(cuda, built):
     pkv.pkv_positions(pool.handle, torch.tensor(ctx, dtype=torch.int32, device="cuda"), torch.from_numpy(starts).cuda(), 4, T, out)
     want[starts[2]:starts[3]] = 0
     assert np.array_equal(out.cpu().numpy(), want) and pool.check() == pkv.PKV_DEVERR_ROW_META
+    monkeypatch.setenv("PKV_VALIDATE", "1")
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.pkv_positions(pool.handle, torch.tensor(ctx, dtype=torch.int32, device="cuda"), torch.from_numpy(starts).cuda(), 4, T, out)
+    assert e.value.status == pkv.PKV_ERR_INVALID_ARG
 
 
 def test_refusals(cuda, built, monkeypatch):

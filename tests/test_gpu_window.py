@@ -152,9 +152,11 @@ def test_long_windows_split_items(cuda, built, kv, shape):
 
 @pytest.mark.parametrize("kv", [F16, E4M3])
 @pytest.mark.parametrize("shape", [(12, 2, 128), (8, 2, 256), (4, 4, 64)])
-def test_a_window_past_every_context_gives_the_unwindowed_bits(cuda, built, kv, shape):
-    batch = synth.custom_batch(synth.Shape(1, *shape), [0, 3000, 40, 900, 600], [1, 1, 5, 1, 50], seed=3)
-    p = Pass(batch, 100000, 7, kv)
+@pytest.mark.parametrize("window", [100000, 1024])
+def test_rows_that_the_window_holds_whole_give_the_unwindowed_bits(cuda, built, kv, shape, window):
+    batch = synth.custom_batch(synth.Shape(1, *shape), [0, 3000, 40, 900, 600, 1023, 700], [1, 1, 5, 1, 50, 1, 300], seed=3)
+    p = Pass(batch, 100000, 7, kv)  # every block stays
+    p.window = window
     p.plan()
     out = p.run()
     attn = workload.Attention(p.pool, p.ds)
@@ -162,7 +164,44 @@ def test_a_window_past_every_context_gives_the_unwindowed_bits(cuda, built, kv, 
     full = torch.empty_like(out)
     attn.run(0, p.q, full)
     torch.cuda.synchronize()
-    assert torch.equal(out.view(torch.int16), full.view(torch.int16))
+    for b in range(batch.num_seqs):
+        if batch.context_lens[b] <= window:
+            rows = slice(int(batch.query_start_loc[b]), int(batch.query_start_loc[b + 1]))
+            assert torch.equal(out[rows].view(torch.int16), full[rows].view(torch.int16)), b
+
+
+def test_non_finite_new_tokens_reach_only_those_that_see_them(cuda, built):
+    """Short chunks (decode path), fused and not: NaN and infinite keys and values of new tokens."""
+    batch = synth.custom_batch(synth.Shape(1, 12, 2, 128), [100, 3, 60], [12, 10, 15], seed=4)
+    for fused in (False, True):
+        rows = host_rows(batch, 0)
+        bad = {0: 105, 1: 6, 2: 70}  # row -> the position of its bad token
+        for b, pos in bad.items():
+            rows[b][1][pos], rows[b][2][pos] = (np.nan, np.inf)[b % 2], (np.inf, np.nan, -np.inf)[b]
+        p = Pass(batch, 3, 2, rows=rows)
+        p.plan()
+        got = p.run(fused).cpu().numpy()
+        assert p.pool.check() == 0
+        for b, (q, k, v) in enumerate(rows):
+            ql, ctx = q.shape[0], k.shape[0]
+            for i in range(ql):
+                at = ctx - ql + i
+                if bad[b] <= at < bad[b] + 3:
+                    continue  # sees it
+                ref = oracle.window_attention_row(q[i:i + 1], k[:at + 1], v[:at + 1], 3, 2)
+                assert_close(got[int(batch.query_start_loc[b]) + i][None], ref, f"row {b} query {i}")
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_passes(cuda, built, seed):
+    rng = np.random.default_rng(seed)
+    hkv, group, d = int(rng.choice([1, 2, 4])), int(rng.choice([1, 2, 4, 6, 8])), int(rng.choice([64, 128, 256]))
+    n = int(rng.integers(1, 12))
+    cached = [int(rng.choice([0, rng.integers(0, 40), rng.integers(0, 1500)])) for _ in range(n)]
+    q_lens = [int(rng.choice([1, 1, 1, rng.integers(1, 16), rng.integers(16, 150)])) for _ in range(n)]
+    window, sinks = int(2 ** rng.uniform(0, 10)), int(rng.choice([0, 1, 4, 15, 16, 33, 200]))
+    _run((hkv * group, hkv, d), cached, q_lens, window, sinks, int(rng.choice([F16, E4M3])), int(rng.choice([0, 0, 1, 5, 13])),
+         fused=bool(rng.integers(2)), sample=16, seed=seed)
 
 
 @pytest.mark.parametrize("kv", [F16, E4M3])
