@@ -461,6 +461,88 @@ __global__ void __launch_bounds__(kWorkers * 32) compact_move_kernel(const Block
   publish();
 }
 
+// Small pools and tables, in one launch: every CTA makes the whole plan for itself in shared memory (one warp orders the
+// ids) and goes on to its pieces; CTA 0 writes the plan out.  The tables are read by every CTA, so they may not be
+// rewritten in place here.
+constexpr int kSmallEntries = 1024;
+constexpr int kSmallBlocks = 2048;
+
+__global__ void __launch_bounds__(kWorkers * 32) compact_small_kernel(const BlockGeo g, const CompactParams p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint32_t bits[kSmallBlocks / 32];
+  __shared__ int32_t src[kSmallBlocks / 2], dst[kSmallBlocks / 2];
+  __shared__ int live, moves;
+  constexpr int PER = kSmallBlocks / 32 / 32;  // bitmap words a lane
+  const int lane = threadIdx.x & 31;
+  for (int w = threadIdx.x; w < kSmallBlocks / 32; w += blockDim.x) bits[w] = 0;
+  __syncthreads();
+  dev::griddep_wait();
+  mark(p, bits, threadIdx.x, blockDim.x);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    auto before = [&](int v, int& total) {  // sum over the lower lanes, and over all
+      int x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      total = __shfl_sync(0xffffffffu, x, 31);
+      return x - v;
+    };
+    uint32_t b[PER];
+    int used = 0, nm = 0, nh = 0, n, m, h;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      b[k] = bits[lane * PER + k];
+      used += __popc(b[k]);
+    }
+    before(used, n);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const uint32_t lo = below(lane * PER + k, n);
+      nm += __popc(b[k] & ~lo);
+      nh += __popc(~b[k] & lo);
+    }
+    int im = before(nm, m), ih = before(nh, h);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int w = lane * PER + k;
+      const uint32_t lo = below(w, n);
+      for (uint32_t x = b[k] & ~lo; x; x &= x - 1) src[im++] = w * 32 + __ffs(x) - 1;
+      for (uint32_t x = ~b[k] & lo; x; x &= x - 1) dst[ih++] = w * 32 + __ffs(x) - 1;
+    }
+    if (lane == 0) {
+      live = n;
+      moves = m;
+    }
+  }
+  __syncthreads();
+  // a used block's new id: its own below `live`, else that of its move (src ascends)
+  auto moved = [&](int id) {
+    if (id < live) return id;
+    int lo = 0, hi = moves - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (src[mid] <= id) lo = mid; else hi = mid - 1;
+    }
+    return dst[lo];
+  };
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < p.entries; i += (int64_t)gridDim.x * blockDim.x) {
+    const int id = __ldg(p.tables + i);
+    p.new_tables[i] = id >= 0 && id < p.num_blocks ? moved(id) : id;
+  }
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < p.num_blocks; i += gridDim.x * blockDim.x)
+    p.remap[i] = bits[i >> 5] >> (i & 31) & 1 ? moved(i) : -1;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.num_live = live;
+  bulk_copy(g, moves, smem, [&](int64_t m, bool, int& s, int& d) {
+    s = src[m];
+    d = dst[m];
+    return true;
+  });
+  publish();
+}
+
 // ---- host -----------------------------------------------------------------------------------------
 // Under PKV_VALIDATE=1 (and outside a capture): n int32 of `src` on the host, after the stream's earlier work.
 pkv_status fetch_for_validation(const int32_t* src, size_t n, void* stream, std::vector<int32_t>* out, bool* ran) {
@@ -630,6 +712,17 @@ extern "C" pkv_status pkv_compact(pkv_pool* pool, const int32_t* block_tables, i
   const size_t smem = ((size_t)nb + 31) / 32 * 4;
   int launches = 0;
   cudaError_t e;
+  const BlockGeo g = geo_of(pool);
+  const unsigned movers = (unsigned)bulk_grid(pool, g, nb);  // the number of moves is known on the device alone
+  const bool apart = p.entries == 0 || new_tables + p.entries <= block_tables || block_tables + p.entries <= new_tables;
+  if (p.entries <= kSmallEntries && nb <= kSmallBlocks && apart) {
+    static bool small_set = false;
+    e = allow_bulk_smem(compact_small_kernel, &small_set);
+    if (e == cudaSuccess) e = launch_pdl(compact_small_kernel, dim3(movers), dim3(kWorkers * 32), kBulkSmem, s, g, p);
+    if (e != cudaSuccess) return cuda_fail(e, "compact launch");
+    pool->last_launches = 1;
+    return PKV_OK;
+  }
   // One CTA marks up to 16 K entries in a few microseconds; past that (or a bitmap that shared memory does not hold) two
   // more launches spread the marking over the GPU.
   if (smem <= 48 * 1024 && p.entries <= 16 * 1024) {
@@ -644,11 +737,9 @@ extern "C" pkv_status pkv_compact(pkv_pool* pool, const int32_t* block_tables, i
     launches = 2;
   }
   if (e != cudaSuccess) return cuda_fail(e, "compact plan launch");
-  const BlockGeo g = geo_of(pool);
   static bool smem_set = false;
   e = allow_bulk_smem(compact_move_kernel, &smem_set);
-  if (e == cudaSuccess)  // the number of moves is known on the device alone
-    e = launch_pdl(compact_move_kernel, dim3((unsigned)bulk_grid(pool, g, nb)), dim3(kWorkers * 32), kBulkSmem, s, g, p);
+  if (e == cudaSuccess) e = launch_pdl(compact_move_kernel, dim3(movers), dim3(kWorkers * 32), kBulkSmem, s, g, p);
   if (e != cudaSuccess) return cuda_fail(e, "compact move launch");
   pool->last_launches = launches + 1;
   return PKV_OK;

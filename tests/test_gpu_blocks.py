@@ -182,7 +182,8 @@ def _compact(pool, tables, in_place=False):
 
 @pytest.mark.parametrize("kv", KINDS)
 @pytest.mark.parametrize("layers,hkv,d", SHAPES)
-@pytest.mark.parametrize("blocks,rows,width,used", [(1, 1, 1, 1), (33, 2, 5, 8), (64, 4, 20, 64), (500, 7, 30, 120), (700, 20, 40, 690)])
+@pytest.mark.parametrize("blocks,rows,width,used", [(1, 1, 1, 1), (33, 2, 5, 8), (64, 4, 20, 64), (500, 7, 30, 120), (700, 20, 40, 690),
+                                                    (2048, 32, 32, 700), (2049, 8, 16, 100), (600, 33, 32, 300)])
 def test_compact(cuda, built, kv, layers, hkv, d, blocks, rows, width, used):
     rng = np.random.default_rng(blocks + used)
     tables = np.full((rows, width), -1, np.int32)
