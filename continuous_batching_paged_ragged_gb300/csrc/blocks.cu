@@ -18,10 +18,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-// fork_rows: CTAs per SM.  Pieces are short and scattered (a tail of 8 rows on the 8-bit cache is 1 KB a plane and head,
-// and 32 bytes of scales), so many threads with few loads each do better than the reverse: 8 CTAs of two 16-byte
-// loads a thread 16.0 us for 288 forks over 28 layers (4.2 TB/s read and written), 4 of four 18.0, 2 of eight 17.8.
-constexpr int kForkCtas = 8;
+constexpr int kForkCtas = 6;  // fork_rows: CTAs per SM (copy_rows)
 constexpr int kBS = 16;
 
 struct BlockGeo {
@@ -53,32 +50,40 @@ BlockGeo geo_of(const pkv_pool* pool) {
 }
 
 // The first `rows` rows of every head of block src into block dst, planes [p0, p1) of the planes + scale_planes,
-// by all threads of the CTA.  The copied chunks of all planes and heads are one index range, so that every thread has
-// loads in flight however short the pieces are (a tail of one row is 64 bytes a plane and head).
+// by all threads of the CTA.  A warp takes the pieces (plane, head) in turn, kPieces at once so that its lanes have
+// loads in flight however short a piece is (one row is 64 bytes or more, all sixteen 1 to 8 KB); nothing is divided in
+// the loop.  Forks are bound by this loop's instructions and latency, not by DRAM (a parent's children share its reads
+// through L2, and the writes stay there): 288 forks over 28 layers of an 8-bit cache take 14.2 us (4.7 TB/s read and
+// written) with four pieces and six CTAs an SM, 16 with two and eight, 18 with a divided index for every chunk.
 __device__ void copy_rows(const BlockGeo& g, int src, int dst, int rows, int p0, int p1) {
-  const uint32_t run = kBS * g.row_bytes / 16;              // 16-byte chunks of a head's run
-  const uint32_t live = rows * g.row_bytes / 16;            // of which copied
-  const int64_t piece = (int64_t)g.num_kv_heads * run, plane = g.plane_bytes / 16;
-  const int v1 = min(p1, g.planes);
-  const uint4* in = reinterpret_cast<const uint4*>(g.values) + src * piece;
-  uint4* out = reinterpret_cast<uint4*>(g.values) + dst * piece;
-  const uint32_t per = live * g.num_kv_heads, n = p0 < v1 ? (v1 - p0) * per : 0;
-  constexpr int U = 2;  // chunks in flight a thread
-  for (uint32_t i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
-    uint4 v[U];
-    int64_t off[U];
+  constexpr int kPieces = 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int run = kBS * g.row_bytes / 16;    // 16-byte chunks of a head's run
+  const int live = rows * g.row_bytes / 16;  // of which copied
+  const int64_t plane = g.plane_bytes / 16;
+  const int v1 = min(p1, g.planes), n = max(0, v1 - p0) * g.num_kv_heads;
+  const uint4* in = reinterpret_cast<const uint4*>(g.values) + (int64_t)src * g.num_kv_heads * run + p0 * plane;
+  uint4* out = reinterpret_cast<uint4*>(g.values) + (int64_t)dst * g.num_kv_heads * run + p0 * plane;
+  for (int i0 = warp * kPieces; i0 < n; i0 += kThreads / 32 * kPieces) {
+    int64_t off[kPieces];
+    int p = i0 / g.num_kv_heads, h = i0 - p * g.num_kv_heads;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t i = i0 + u * kThreads;
-      off[u] = -1;
-      if (i >= n) continue;
-      const uint32_t p = i / per, r = i - p * per, h = r / live;
-      off[u] = (int64_t)(p0 + p) * plane + h * run + (r - h * live);
-      v[u] = __ldcs(in + off[u]);
+    for (int k = 0; k < kPieces; ++k) {
+      off[k] = p * plane + h * run;
+      if (++h == g.num_kv_heads) {
+        h = 0;
+        ++p;
+      }
     }
+    for (int c = lane; c < live; c += 32) {
+      uint4 v[kPieces];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (off[u] >= 0) __stcs(out + off[u], v[u]);
+      for (int k = 0; k < kPieces; ++k)
+        if (i0 + k < n) v[k] = __ldcs(in + off[k] + c);
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k)
+        if (i0 + k < n) __stcs(out + off[k] + c, v[k]);
+    }
   }
   // 8-bit: one thread a scale record (16 slots of K or V of a head), the first `rows` bytes of it
   const int s0 = max(p0, g.planes) - g.planes, s1 = p1 - g.planes;
