@@ -83,10 +83,6 @@ struct DecodeTraits {
   // much in registers for two CTAs (it spills); like its fp16 twin, which shared memory limits to one, it
   // runs one CTA per SM with the whole register file.
   static constexpr int MINB = (F8 && D == 256 && G > 6) ? 1 : (FIT < 3 ? FIT : 3);
-  // Lean blocks two at a time (one softmax step and one rescale of O per pair): measured faster for the 8-bit
-  // cache at head_dim 256 (the long-context decode, 7.3 against 8.9 ms a step), whose warps are bound by their
-  // turnaround per block; slower on the 5-slot fp16 rings and the 256-row batch, so only there.
-  static constexpr bool PAIRS = F8 && D == 256;
   static_assert(D % 64 == 0 && G >= 1 && G <= kHeadsTile, "shape");
   static_assert(RUN % 1024 == 0, "swizzled boxes need 1024-byte aligned slots");
   static_assert(KS % 2 == 0 && QB % 128 == 0, "k-steps in pairs; q buffers stay 16-byte aligned");
@@ -96,6 +92,14 @@ struct DecodeTraits {
   static_assert(OFF_SCL % 16 == 0, "scale records are bulk-copy destinations");
   static_assert(MINB >= 1, "shared memory");
 };
+
+// Lean blocks two at a time (one softmax step and one rescale of O per pair): measured faster for the 8-bit cache at
+// head_dim 256 (the long-context decode, 7.3 against 8.9 ms a step), whose warps are bound by their turnaround per
+// block, and for windowed rows at head_dim 64 (256 rows of 1024 keys, 8 / 2 heads: 45.6 against 56.7 us), whose rings
+// hold four pairs; slower on the 5-slot fp16 rings at 128 (59.5 against 51.4 us for 12 / 2 heads) and for the 256-row
+// batch, so only there.  Unwindowed rows at head_dim 64 stay single: their results keep their bits.
+template <int D, int KV, bool W>
+constexpr bool kPairs = (KV == kKvE4M3 && D == 256) || (W && D == 64);
 
 struct DecodeParams {
   CUtensorMap kv_map;  // fp16: the pool as whole runs; 8-bit: as rows of codes (64-byte aligned: first member)
@@ -314,7 +318,7 @@ struct Streamer {
     const int first = v.base + v.bw;  // visible index of the warp's block 0 (unwindowed: its block of the row)
     const int skip = W ? token_blocks<W>(p, v.ctx).skip : 0;
     const int nfull = from / kBS - skip - first;  // blocks first, first + NW, ... below from / 16
-    v.nlean = (!T::PAIRS || nfull <= 0) ? 0 : min(v.nbw, (nfull + T::NW - 1) / T::NW);
+    v.nlean = (!kPairs<D, KV, W> || nfull <= 0) ? 0 : min(v.nbw, (nfull + T::NW - 1) / T::NW);
   }
   static __device__ __forceinline__ int runs(const TaskView& v) { return v.t >= 0 ? 2 * v.nbw : 0; }
   __device__ __forceinline__ int block_pos(const TaskView& v, int j) const {
@@ -567,7 +571,7 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
       // ---- the lean blocks, two at a time: both blocks' scores, one softmax step for the pair (one max
       // reduction, one rescale of O), then both blocks' products.  Their runs sit in the ring in that order. ----
       int j = 0;
-      if constexpr (T::PAIRS) {
+      if constexpr (kPairs<D, KV, W>) {
         for (; j + 1 < d.nlean && w.ok; j += 2) {
           float x[2][4];            // scaled scores: [block][key qh head h0, key qh h0 + 1, key qh + 8 h0, .. h0 + 1]
           uint32_t evb[2][2];       // 8-bit: value scale bytes of keys qh, qh + 8

@@ -257,7 +257,8 @@ pkv_status pkv_attention_append(pkv_pool* pool, int32_t layer, const void* q, co
  *   - Keys and values that a query does not see have no part in its result, whatever they hold, with one
  *     exception: in a row of 16 or more new tokens, a non-finite value (of V) that is seen by one of the row's
  *     queries, or shares a 16-token block with one that is, may reach the row's other queries.
- *   - A row whose contexts the window holds whole gives the bits of a plan without one.
+ *   - A row whose contexts the window holds whole gives the bits of a plan without one (at head_dim 64 only with 16 or
+ *     more new tokens: shorter rows there sum their blocks in pairs).
  *   - pkv_attention_noalloc knows no window: it attends whole contexts.
  * window >= 1, sinks >= 0 (else PKV_ERR_INVALID_ARG, and 0 bytes). */
 size_t pkv_attention_window_workspace_bytes(const pkv_pool* pool, int32_t num_seqs, int32_t num_tokens,
