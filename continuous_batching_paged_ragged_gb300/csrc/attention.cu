@@ -24,7 +24,9 @@
 //    launch cost more than the merge: its CTAs cannot start until the decode's have left the SMs).
 //    Tokens with more than 32 splits are merged by merge_kernel, launched behind the decode, which
 //    spreads one token's merge over many CTAs.
-//  * Prefill rows run on the tcgen05 tile kernel (prefill.cu) ahead of the decode; on the 8-bit cache
+//  * A windowed plan (pkv_attention_window_plan) counts and walks the blocks that a window and a few first tokens leave
+//    visible; its calls launch the kernels' windowed instances (decode_window*.cu, prefill_window.cu).
+//  * Prefill rows run on the tcgen05 tile kernel (prefill.cuh) ahead of the decode; on the 8-bit cache
 //    their blocks are first dequantized into an fp16 shadow in the workspace (dequant_prefill_rows_kernel).
 #include <cuda_fp16.h>
 
