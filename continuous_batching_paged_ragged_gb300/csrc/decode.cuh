@@ -164,7 +164,7 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 // slot (chunk % 8) XOR (R % 8)).
 template <int D>
 __device__ __forceinline__ uint32_t swz8(int r, int c) {
-  if constexpr (D == 256) return swz(r, c);  // one 16-key x 128-byte box per half of the key (fp16's layout)
+  if constexpr (D == 256) return swz(r, c);  // a 16-key x 128-byte sub-tile per half of the key (fp16's layout)
   const int x = r * D + 16 * c, R = x >> 7;
   return (uint32_t)(R * 128 + ((((x >> 4) & 7) ^ (R & 7)) << 4));
 }
@@ -350,10 +350,9 @@ struct Streamer {
     if constexpr (T::F8) {
       // the codes as one box; a K run brings the block's 32-byte scale record (K and V scales) along
       dev::mbar_arrive_expect_tx(&bars[slot], T::RUN + ((r & 1) ? 0 : T::SCL));
-      if constexpr (D == 256) {  // two boxes: the keys' first and second 128 code bytes (rows are tokens)
+      if constexpr (D == 256) {  // the keys' first, then their second 128 code bytes (rows are tokens), one copy
         const int tok = ((r & 1) ? p.layer_row0_v : p.layer_row0_k) + (id * p.num_kv_heads + v.g) * kBS;
-        dev::tma_load_3d(dst, &p.kv_map, 0, 0, tok, &bars[slot], pol);
-        dev::tma_load_3d(dst + 2048, &p.kv_map, 0, 1, tok, &bars[slot], pol);
+        dev::tma_load_3d(dst, &p.kv_map, 0, tok, 0, &bars[slot], pol);
       } else {
         const int row = ((r & 1) ? p.layer_row0_v : p.layer_row0_k) + (id * p.num_kv_heads + v.g) * T::BOXROWS;
         dev::tma_load_2d(dst, &p.kv_map, 0, row, &bars[slot], pol);

@@ -55,7 +55,7 @@ struct MetaCheck {
 struct pkv_pool {
   // The cache as the TMA engine sees it, 128-byte swizzle: fp16, rows of head_dim values (one per (layer,
   // K/V, block, KV head, slot)); 8-bit, rows of 128 code bytes (a (block, KV head) run is 16*head_dim/128
-  // consecutive rows), at head_dim 256 a 3-D map (128 code bytes, the key's half, the key).
+  // consecutive rows), at head_dim 256 a 3-D map (128 code bytes, the key, the key's half).
   CUtensorMap kv_map;
   // fp16: the same cache as whole (block, KV head) runs of K or V, one box of 16 rows x head_dim values laid
   // out as head_dim / 64 swizzled 2 KB sub-tiles (the 2-D map's boxes side by side): one copy per run

@@ -58,9 +58,9 @@ typedef enum {
 } pkv_status;
 
 /* Device error word bits (pkv_pool_check). */
-#define PKV_DEVERR_SLOT_RANGE   0x1  /* pkv_append: slot outside [-1, num_blocks*block_size)        */
-#define PKV_DEVERR_BLOCK_RANGE  0x2  /* attention: block id outside [0, num_blocks)                  */
-#define PKV_DEVERR_ROW_META     0x4  /* row with q_len < 1, q_len > ctx, or ctx > max_blocks*bs       */
+#define PKV_DEVERR_SLOT_RANGE   0x1  /* an append: slot outside [-1, num_blocks*block_size)           */
+#define PKV_DEVERR_BLOCK_RANGE  0x2  /* attention or a block call: block id outside [0, num_blocks)   */
+#define PKV_DEVERR_ROW_META     0x4  /* row with q_len < 1, q_len > ctx, or ctx > max_blocks*bs; a fork's rows */
 #define PKV_DEVERR_QSL          0x8  /* query_start_loc not monotone / not ending at num_tokens       */
 #define PKV_DEVERR_WAIT_TIMEOUT 0x10 /* an on-chip barrier wait gave up (should never happen)          */
 
@@ -405,7 +405,8 @@ pkv_status pkv_fork_rows(pkv_pool* pool, int32_t* block_tables, int32_t max_bloc
  * blocks in use, the k-th lowest used block of those at n or above is copied to the k-th lowest unused block
  * below n; the others stay.  Written, all on the device:
  *     new_tables  int32 [num_seqs][max_blocks_per_seq]  block_tables with every used block's new id (other
- *                                                       entries as they were); may be block_tables itself
+ *                                                       entries as they were); may be block_tables itself, and
+ *                                                       must not overlap it otherwise
  *     remap       int32 [num_blocks]                    a used block's new id, -1 for an unused one
  *     num_live    int32 [1]                             n: blocks n .. num_blocks - 1 are free now
  * Every table of the pool's requests must be in the call: a block named in none is free, and may be overwritten.
