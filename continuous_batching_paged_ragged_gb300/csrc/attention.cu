@@ -248,9 +248,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   __syncthreads();
 
   // ---- decode tasks: tokens of rows that are not prefill items ----
-  // Largest first: every token's full splits in token order, then the short last splits by decreasing
-  // size.  The CTAs that take the last tasks of a launch then hold little work each, so the launch ends
-  // nearly together on every SM.  (The order decides which CTA computes a split, never the result.)
+  // Largest first: every token's splits but the last in token order, then the last splits by decreasing
+  // size, a full one too: by then the token's others are counted, and it merges them at its end (256 rows of three
+  // equal splits 58.5 us with all of a token's splits together, 51.3 so).  The CTAs that take the last tasks of a
+  // launch then hold little work each, so the launch ends nearly together on every SM.  (The order decides which CTA computes a split, never the result.)
   int carry = 0;
   for (int base = 0; base < p.num_tokens; base += blockDim.x) {
     const int t = base + threadIdx.x;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       nblk = visible_blocks(c, p.win.window, p.win.sinks).n;
       size = token_split(c, p.split_blocks, p.win);
     }
-    const int nfull = nblk / size, tail = nblk % size;
+    const int nfull = nblk > 0 ? (nblk - 1) / size : 0, tail = nblk - nfull * size;
     if (tail > 0) atomicAdd(&tail_at[tail], p.num_kv_heads);
     const int cnt = nfull * p.num_kv_heads;
     int total = 0;
@@ -290,7 +291,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   for (int t = threadIdx.x; t < p.num_tokens; t += blockDim.x) {
     const int c = p.tok_ctx[t];  // written by this thread above
     const int size = token_split(c, p.split_blocks, p.win);
-    const int nblk = visible_blocks(c, p.win.window, p.win.sinks).n, nfull = nblk / size, tail = nblk % size;
+    const int nblk = visible_blocks(c, p.win.window, p.win.sinks).n;
+    const int nfull = nblk > 0 ? (nblk - 1) / size : 0, tail = nblk - nfull * size;
     if (tail > 0) {
       const int at = atomicAdd(&tail_at[tail], p.num_kv_heads), row = p.tok_row[t];
       for (int g = 0; g < p.num_kv_heads; ++g) p.tasks[at + g] = make_int4(t, g | (nfull << 8), row, c);
