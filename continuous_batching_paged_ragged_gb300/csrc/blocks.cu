@@ -321,6 +321,7 @@ CompactWs compact_ws(int num_blocks) {
 }
 
 constexpr int kPlanThreads = 1024;
+constexpr size_t kPlanBitmap = 47 * 1024;  // bytes of bitmap for one planning CTA: 48 KB, less what its scans share
 
 __device__ int block_scan(int v, int* sums, int* total) {  // exclusive, over kPlanThreads threads
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -730,7 +731,7 @@ extern "C" pkv_status pkv_compact(pkv_pool* pool, const int32_t* block_tables, i
   }
   // One CTA marks up to 16 K entries in a few microseconds; past that (or a bitmap that shared memory does not hold) two
   // more launches spread the marking over the GPU.
-  if (smem <= 48 * 1024 && p.entries <= 16 * 1024) {
+  if (smem <= kPlanBitmap && p.entries <= 16 * 1024) {
     e = launch_pdl(compact_plan_kernel, dim3(1), dim3(kPlanThreads), smem, s, p);
     launches = 1;
   } else {

@@ -217,6 +217,19 @@ def test_compact_large_pools_and_tables(cuda, built, blocks, rows, width):
     Host(pool).same(want)
 
 
+@pytest.mark.parametrize("blocks", [385024, 385025, 393100, 393216, 393217])
+def test_compact_pools_whose_bitmap_about_fills_shared_memory(cuda, built, blocks):
+    rng = np.random.default_rng(blocks)
+    tables = rng.integers(-1, blocks, (40, 60)).astype(np.int32)
+    tables[0, 0], tables[1, 1] = blocks - 1, 0
+    pool = _pool(1, 1, 64, blocks, pkv.PKV_KV_E4M3)
+    want = Host(pool)
+    wt, wr, wn = _compact_host(want, tables, blocks)
+    new, remap, n = _compact(pool, tables)
+    assert n == wn and np.array_equal(new, wt) and np.array_equal(remap, wr) and pool.check() == 0
+    Host(pool).same(want)
+
+
 def test_compact_edges_and_refusals(cuda, built):
     pool = _pool(1, 2, 64, 40, pkv.PKV_KV_F16)
     want = Host(pool)
