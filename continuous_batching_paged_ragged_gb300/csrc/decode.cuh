@@ -611,8 +611,15 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
             x[u][2] = (sc[2] + sd[2]) * ks1;
             x[u][3] = (sc[3] + sd[3]) * ks1;
             if (W && w.block_pos(d, j + u) < low) {
-              if (!sees(w.block_pos(d, j + u) + qh)) x[u][0] = x[u][1] = -INFINITY;
-              if (!sees(w.block_pos(d, j + u) + qh + 8)) x[u][2] = x[u][3] = -INFINITY;
+              // a key that is not seen: weight 0, and its value's scale byte, which may decode to infinity, is dropped too
+              if (!sees(w.block_pos(d, j + u) + qh)) {
+                x[u][0] = x[u][1] = -INFINITY;
+                evb[u][0] = 0;
+              }
+              if (!sees(w.block_pos(d, j + u) + qh + 8)) {
+                x[u][2] = x[u][3] = -INFINITY;
+                evb[u][1] = 0;
+              }
             }
             w.release_run();
           }
