@@ -380,6 +380,7 @@ struct WsLayout {
   // 8-bit cache with prefill rows: the rows' first shadow block, the shadow block tables and the fp16 shadow
   size_t pf_base = 0, shadow_bt = 0, shadow = 0;
   int64_t shadow_blocks = 0;
+  bool shadow_by_id = false;  // the shadow mirrors the pool block for block (no shadow block tables)
   int max_splits;
   int64_t max_tasks;
   int prefill_min_qlen;  // 0: every row takes the decode path
@@ -439,13 +440,14 @@ static WsLayout ws_layout(const pkv_config& c, int num_seqs, int num_tokens, int
   w.part_o = off;
   off += up256(parts * 32 * (c.head_dim / 4) * sizeof(float));
   if (c.kv_dtype == PKV_KV_E4M3 && rows > 0) {
-    // the prefill rows hold at most `rows` x max_blocks blocks, and at most the pool's when no two rows
-    // share one; more than that is refused by the dequantizing kernel (reported, never written)
+    // the prefill rows' tables name at most `rows` x max_blocks blocks, a block that several rows share once for each;
+    // where the pool has fewer, the shadow is addressed by physical block instead, whoever shares it
     w.shadow_blocks = std::min<int64_t>((int64_t)c.num_blocks, rows * (int64_t)max_blocks);
+    w.shadow_by_id = rows * (int64_t)max_blocks > c.num_blocks;
     w.pf_base = off;
     off += up256((size_t)(num_seqs + 1) * 4);
     w.shadow_bt = off;
-    off += up256((size_t)num_seqs * max_blocks * 4);
+    if (!w.shadow_by_id) off += up256((size_t)num_seqs * max_blocks * 4);
     w.shadow = off;
     off += up256((size_t)2 * w.shadow_blocks * c.num_kv_heads * kBS * c.head_dim * 2);
   }
@@ -489,9 +491,13 @@ static cudaError_t launch_plan(pkv_pool* pool, char* ws, const WsLayout& w, cons
 // 8-bit cache, prefill rows: the tile kernel reads fp16 tiles, so every block of a prefill row is first
 // dequantized (exactly) into an fp16 shadow in the workspace, and the row's shadow block table is written
 // alongside.  The plan numbered the prefill rows' blocks row after row (pf_base, monotone, with the total at
-// the end); a CTA takes shadow blocks in turn, finds its row by binary search over pf_base staged in shared
+// the end); a CTA takes these in turn, finds its row by binary search over pf_base staged in shared
 // memory, and dequantizes the block's Hkv x 16 rows with all its threads.  Keys past the context in a last
 // block are written as zeros.
+// A pool with fewer blocks than the rows' tables have entries (forked prompts: rows that share their blocks) has
+// a shadow addressed by physical block, read through the pass's own block tables.  A shared block is then written
+// once for each of its rows, with the same bytes every time: all 16 keys, whatever the rows' contexts (the tile kernel
+// masks keys past a context, and zeroes its last tile's values there).
 // ---------------------------------------------------------------------------------------------------
 struct DequantParams {
   const unsigned char* codes_k;  // this layer's codes [num_blocks][Hkv][16][D]
@@ -500,7 +506,7 @@ struct DequantParams {
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* pf_base;        // [num_seqs + 1]
-  int32_t* shadow_bt;            // [num_seqs][max_blocks]
+  int32_t* shadow_bt;            // [num_seqs][max_blocks]; null: the shadow is addressed by physical block
   uint4* shadow_k;               // [shadow_blocks][Hkv][16][D] fp16
   uint4* shadow_v;
   int32_t* err;
@@ -521,10 +527,10 @@ __global__ void __launch_bounds__(256) dequant_prefill_rows_kernel(const Dequant
   for (int i = threadIdx.x; i <= p.num_seqs; i += blockDim.x) sbase[i] = p.pf_base[i];
   __syncthreads();
   const int64_t want = sbase[p.num_seqs];
-  // rows sharing blocks can hold more than the shadow: the excess is refused and reported (the tile kernel
-  // then finds an out-of-range id in their tables and reports it too)
-  if (want > p.shadow_blocks && blockIdx.x == 0 && threadIdx.x == 0) dev::set_error(p.err, PKV_DEVERR_BLOCK_RANGE);
-  const int total = (int)min(want, p.shadow_blocks);
+  const bool by_id = p.shadow_bt == nullptr;
+  // (numbered row after row, valid rows never hold more than the shadow)
+  if (!by_id && want > p.shadow_blocks && blockIdx.x == 0 && threadIdx.x == 0) dev::set_error(p.err, PKV_DEVERR_BLOCK_RANGE);
+  const int total = (int)(by_id ? want : min(want, p.shadow_blocks));
   const int per_block = p.num_kv_heads * kBS * CPR;
   for (int sb = blockIdx.x; sb < total; sb += gridDim.x) {
     int lo = 0, hi = p.num_seqs - 1;  // the row: the last b with sbase[b] <= sb (rows before it hold fewer)
@@ -539,14 +545,16 @@ __global__ void __launch_bounds__(256) dequant_prefill_rows_kernel(const Dequant
     const int id = __ldg(p.block_tables + (int64_t)b * p.max_blocks + j);
     const bool ok = id >= 0 && id < p.num_blocks;
     if (threadIdx.x == 0) {
-      p.shadow_bt[(int64_t)b * p.max_blocks + j] = sb;
+      if (!by_id) p.shadow_bt[(int64_t)b * p.max_blocks + j] = sb;
       if (!ok) dev::set_error(p.err, PKV_DEVERR_BLOCK_RANGE);
     }
+    if (by_id && !ok) continue;  // (the tile kernel skips the id as well)
+    const int64_t to = by_id ? id : sb;
     for (int i = threadIdx.x; i < per_block; i += blockDim.x) {
       const int h = i / (kBS * CPR), r = (i / CPR) % kBS, c = i % CPR;
-      const bool live = ok && j * kBS + r < ctx;
+      const bool live = ok && (by_id || j * kBS + r < ctx);
       const int64_t src = (ok ? (int64_t)id : 0) * p.num_kv_heads + h;
-      const int64_t dst = (((int64_t)sb * p.num_kv_heads + h) * kBS + r) * CPR + c;
+      const int64_t dst = ((to * p.num_kv_heads + h) * kBS + r) * CPR + c;
       const unsigned char* rec = p.scales + src * 32;
       const uint2 zero = make_uint2(0, 0);
       const uint2 ck = live ? __ldg(reinterpret_cast<const uint2*>(p.codes_k + (src * kBS + r) * D) + c) : zero;
@@ -644,7 +652,7 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
       dq.block_tables = block_tables;
       dq.context_lens = context_lens;
       dq.pf_base = reinterpret_cast<const int32_t*>(ws + w.pf_base);
-      dq.shadow_bt = reinterpret_cast<int32_t*>(ws + w.shadow_bt);
+      dq.shadow_bt = w.shadow_by_id ? nullptr : reinterpret_cast<int32_t*>(ws + w.shadow_bt);
       dq.shadow_k = reinterpret_cast<uint4*>(shadow);
       dq.shadow_v = reinterpret_cast<uint4*>(shadow + srows / 2 * c.head_dim * 2);
       dq.err = p.err;
@@ -661,7 +669,7 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
       if (e != cudaSuccess) return cuda_fail(e, "dequantize launch");
       *launches += 1;
       a.kv_map = &pool->shadow_map;
-      a.block_tables = dq.shadow_bt;
+      if (!w.shadow_by_id) a.block_tables = dq.shadow_bt;
       a.layer_row0_k = 0;
       a.layer_row0_v = (int)(srows / 2);
       a.num_blocks = (int)w.shadow_blocks;

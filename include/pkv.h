@@ -197,8 +197,8 @@ pkv_status pkv_append(pkv_pool* pool, int32_t layer, const void* k, const void* 
  * with 16 or more new tokens first have their blocks dequantized into an fp16 shadow
  * inside the workspace, read by the tensor-core tile kernel; values within 3 % of the fp16 maximum saturate
  * there.  pkv_attention_workspace_bytes then includes room for min(num_blocks, R * max_blocks_per_seq)
- * shadow blocks, R the most rows of 16+ new tokens the pass can hold; prefill rows holding more blocks in
- * total (rows sharing blocks count each time) are refused and reported (PKV_DEVERR_BLOCK_RANGE).
+ * shadow blocks, R the most rows of 16+ new tokens the pass can hold.  Rows may share blocks (forks of a prompt that is
+ * still being computed): that many hold them all.
  *
  * q                fp16 [num_tokens][num_q_heads][head_dim]   device, 16-byte aligned
  * block_tables     int32 [num_seqs][max_blocks_per_seq]       device
