@@ -48,7 +48,7 @@ namespace {
 constexpr int kKSlots = 3;             // K ring depth
 constexpr int kVSlots = 2;             // V ring depth
 constexpr int kWG = 2;                 // softmax warpgroups (Q tiles per item) at most
-constexpr int kBarItem = 1, kBarQ = 2, kBarEpi = 3, kBarOut = 4;  // named barriers (0 is __syncthreads; kBarOut per group)
+constexpr int kBarItem = 1, kBarQ = 2, kBarEpi = 3, kBarOut = 4, kBarZero = 6;  // named barriers (0 is __syncthreads; kBarOut per group)
 constexpr float kRescaleLog2 = 8.f;    // lazy rescale threshold (log2 units)
 constexpr float kNoKeyMax = -1e30f;    // W: a row's running max while it has seen none of its keys (below any score)
 
@@ -252,6 +252,27 @@ __device__ void tma_warp(const PfParams& p, unsigned char* smem, const Bars& sh,
   }
 }
 
+// W: the values between the sinks and the item's window are seen by none of its positions and may hold anything (0 * NaN is
+// NaN).  Blocks of them alone are not among the item's; those that share a block with visible ones are rows of at most
+// two tiles: of the sinks' last block, and of the window's first (where that is another).
+struct HiddenRows {
+  int a0, a1, ta;  // rows [a0, a1) of the packed blocks, in tile ta (-1: none)
+  int b0, b1, tb;
+};
+template <class T>
+__device__ __forceinline__ HiddenRows hidden_rows(const ItemGeo& it, int sinks) {
+  const int hid = min(sinks, it.low), a = hid / kBS, b = it.low / kBS;  // hidden: keys [hid, low)
+  const bool in_a = hid < it.low && hid % kBS != 0, in_b = hid < it.low && it.low % kBS != 0 && !(in_a && a == b);
+  HiddenRows h;
+  h.a0 = hid;
+  h.a1 = min(it.low, (a + 1) * kBS);
+  h.ta = in_a ? hid / T::KEYS : -1;
+  h.b0 = (b - it.vis.skip) * kBS;  // the window's first block among the packed ones
+  h.b1 = h.b0 + it.low % kBS;
+  h.tb = in_b ? h.b0 / T::KEYS : -1;
+  return h;
+}
+
 // ---- MMA warps: one per Q-tile group, each issuing its group's MMAs from one thread ------------------
 // Each group's scores and products come from its own warp (the issue rates are at the head of the file);
 // the K and V ring slots are released once both warps' MMAs that read them have completed (two arrivals).
@@ -304,6 +325,7 @@ __device__ void mma_warp(const PfParams& p, unsigned char* smem, const Bars& sh,
     const int zf = it.zfill_wg;
     // this entry holds the item's last tile and it is partial: group zf zeroes its V rows past the keys
     const bool zfe = it.te == it.n_all && it.tail < T::KEYS;
+    const HiddenRows hid = W ? hidden_rows<T>(it, p.win.sinks) : HiddenRows{0, 0, -1, 0, 0, -1};
 
     auto issue_s = [&](int j) {  // S_w(u = j) = Q_w K^T; commits every earlier MMA of this warp too
       const uint64_t dk = dk0 + (uint64_t)((((gt + j) % kKSlots) * T::KVTILE) >> 4);
@@ -342,6 +364,30 @@ __device__ void mma_warp(const PfParams& p, unsigned char* smem, const Bars& sh,
       const bool last = j == n - 1;
       pf_wait(sh, &sh.vfull[gi % kVSlots], (gi / kVSlots) & 1, p.err);
       if (!last) pf_wait(sh, &sh.kfull[(gi + 1) % kKSlots], ((gi + 1) / kKSlots) & 1, p.err);
+      if constexpr (W) {
+        // zeros over the tile's hidden V rows by the first warp, which waits for P all the same (the mixed pass of 3,155
+        // tokens takes 0.2 us more of 49; by the softmax threads, 2 us); both warps come by every tile of the entry
+        const int t = it.tb + j;
+        if (t == hid.ta || t == hid.tb) {
+          if (w == 0) {
+            const uint32_t sv = sbase + T::OFF_V + (gi % kVSlots) * T::KVTILE - t * T::KEYS * 128;
+#pragma unroll 1
+            for (int z = 0; z < 2; ++z) {
+              const int k0 = z ? hid.b0 : hid.a0, k1 = t == (z ? hid.tb : hid.ta) ? (z ? hid.b1 : hid.a1) : 0;
+#pragma unroll 1
+              for (int idx = lane; idx < (k1 - k0) * T::DH * 8; idx += 32) {
+                const int kr = k0 + idx / (T::DH * 8), rest = idx % (T::DH * 8);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sv + (rest >> 3) * (T::KEYS * 128) + kr * 128 +
+                                                                                (rest & 7) * 16),
+                             "r"(0)
+                             : "memory");
+              }
+            }
+            dev::fence_proxy_async_smem();
+          }
+          if (T::WG == 2) dev::named_bar_sync(kBarZero, 64); else __syncwarp();
+        }
+      }
       if (j < ne[w]) {
         pf_wait(sh, &sh.p_ready[w], (cw[w] + j) & 1, p.err);
         // the last tile: the other group zeroes V rows past the item's keys (its own P is ready after that).  A

@@ -256,7 +256,7 @@ pkv_status pkv_attention_append(pkv_pool* pool, int32_t layer, const void* q, co
  *     the window of the row's first new token -- are never read: they may be -1 and the blocks freed.
  *   - Keys and values that a query does not see have no part in its result, whatever they hold, with one
  *     exception: in a row of 16 or more new tokens, a non-finite value (of V) that is seen by one of the row's
- *     queries, or shares a 16-token block with one that is, may reach the row's other queries.
+ *     queries may reach the row's other queries.
  *   - A row whose contexts the window holds whole gives the bits of a plan without one (at head_dim 64 only with 16 or
  *     more new tokens: shorter rows there sum their blocks in pairs).
  *   - pkv_attention_noalloc knows no window: it attends whole contexts.

@@ -36,3 +36,29 @@ def test_hidden_scale_bytes(cuda, built, shape, window, sinks, fused):
         _spoil(p, codes)
         p.plan()
         p.check(p.run(fused))
+
+
+@pytest.mark.parametrize("kv", [F16, E4M3])
+@pytest.mark.parametrize("shape", [(4, 4, 64), (4, 2, 128), (12, 2, 128), (16, 2, 64), (6, 1, 256), (2, 2, 256)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (50, 4), (129, 130), (475, 15), (700, 1), (9, 33)])
+def test_chunks_beside_hidden_values(cuda, built, kv, shape, window, sinks):
+    """Rows of 16 or more new tokens whose hidden keys and values are NaN, those in partly visible blocks too: of the sinks' last
+    block, of the window's first, or of one block that is both."""
+    cached, q_lens = [0, 500, 37, 1000, 2000, 5, 513], [300, 40, 16, 1, 131, 2, 17]
+    batch = synth.custom_batch(synth.Shape(1, *shape), cached, q_lens, seed=12)
+    for codes in ((0x7F, 0x38) if kv == E4M3 else (None,)):
+        p = Pass(batch, window, sinks, kv)
+        _spoil(p, codes)
+        p.plan()
+        p.check(p.run(fused=True), sample=24)
+
+
+@pytest.mark.parametrize("kv", [F16, E4M3])
+@pytest.mark.parametrize("shape", [(12, 2, 128), (4, 1, 256)])
+def test_split_chunks_beside_hidden_values(cuda, built, kv, shape):
+    """A short chunk far into its row, whose work runs in two parts."""
+    for cached, new, window, sinks in ((9000, 40, 6000, 100), (7000, 16, 4500, 0), (9000, 20, 5001, 1001)):
+        p = Pass(synth.custom_batch(synth.Shape(1, *shape), [cached], [new], seed=13), window, sinks, kv)
+        _spoil(p)
+        p.plan()
+        p.check(p.run(), sample=8)
