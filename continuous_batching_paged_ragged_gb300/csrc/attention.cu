@@ -590,9 +590,11 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
                                    const int32_t* context_lens, const int32_t* qsl, int max_blocks, int num_seqs,
                                    int num_tokens, void* out, char* ws,
                                    const WsLayout& w, cudaStream_t s, int* launches,
-                                   const FusedAppend& fa = FusedAppend(), const KeyWindow& win = KeyWindow()) {
+                                   const FusedAppend& fa = FusedAppend(), const KeyWindow& win = KeyWindow(),
+                                   bool early = true) {
   const pkv_config& c = pool->cfg;
   DecodeParams p;
+  p.early = early;
   p.kv_map = c.kv_dtype == PKV_KV_E4M3 ? pool->kv_map : pool->run_map;  // fp16: one copy per run
   p.q = static_cast<const __half*>(q);
   p.block_tables = block_tables;
@@ -785,6 +787,14 @@ static KeyWindow planned_window(const pkv_pool* pool, const void* workspace) {
   return k && k->window != kNoWindow ? make_window(k->window, k->sinks, pool->cfg.split_blocks) : KeyWindow();
 }
 
+// Whether an append that plan `k` did not count on may still be running ahead of an attention call on `layer`: one launched
+// since the plan, which waited for everything before it, unless it was fused into a call under the plan itself (its rows
+// are excepted from what is streamed early).
+static bool append_since(const pkv_pool* pool, int layer, const PlanKey* k) {
+  const LayerWrite& w = pool->writes[layer];
+  return w.stamp > k->stamp && w.plan != k->stamp;
+}
+
 static void forget_plan(pkv_pool* pool, const void* workspace) {
   for (auto it = pool->plans.begin(); it != pool->plans.end(); ++it)
     if (it->workspace == workspace) {
@@ -804,7 +814,7 @@ static void remember_plan(pkv_pool* pool, const PlanKey& key) {
 // context_lens / query_start_loc contents.
 static pkv_status check_plan(const pkv_pool* pool, const void* workspace, const int32_t* context_lens,
                              const int32_t* qsl, int32_t num_seqs, int32_t num_tokens, int32_t max_blocks,
-                             const MetaCheck& mc) {
+                             const MetaCheck& mc, const PlanKey** plan) {
   const PlanKey* k = find_plan(pool, workspace);
   if (!k || k->context_lens != context_lens || k->query_start_loc != qsl || k->num_seqs != num_seqs ||
       k->num_tokens != num_tokens || k->max_blocks_per_seq != max_blocks)
@@ -812,6 +822,7 @@ static pkv_status check_plan(const pkv_pool* pool, const void* workspace, const 
   if (mc.ran && k->summed && mc.sum != k->meta_sum)
     return fail(PKV_ERR_INVALID_ARG, "PKV_VALIDATE: context_lens / query_start_loc changed since pkv_attention_plan "
                 "on this workspace; plan the pass again");
+  *plan = k;
   return PKV_OK;
 }
 
@@ -850,7 +861,7 @@ static pkv_status plan_pass(pkv_pool* pool, const int32_t* context_lens, const i
   pool->last_launches = 0;
   forget_plan(pool, workspace);
   PlanKey key{workspace, context_lens, query_start_loc, num_seqs, num_tokens, max_blocks_per_seq, mc.ran, mc.sum,
-              win.window, win.sinks};
+              win.window, win.sinks, ++pool->clock};
   if (num_tokens == 0) {
     remember_plan(pool, key);
     return PKV_OK;
@@ -907,17 +918,19 @@ extern "C" pkv_status pkv_attention(pkv_pool* pool, int32_t layer, const void* q
   if (num_tokens == 0) return PKV_OK;
   st = check_io(q, out, block_tables);
   MetaCheck mc;
+  const PlanKey* plan = nullptr;
   if (st == PKV_OK) st = validate_metadata(pool, block_tables, max_blocks_per_seq, context_lens, query_start_loc,
                                            num_seqs, num_tokens, nullptr, stream, &mc, win.window, win.sinks);
   if (st == PKV_OK) st = check_plan(pool, workspace, context_lens, query_start_loc, num_seqs, num_tokens,
-                                    max_blocks_per_seq, mc);
+                                    max_blocks_per_seq, mc, &plan);
   if (st != PKV_OK) return st;
   const WsLayout w = ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks_per_seq, win);
   st = prepare_prefill_shadow(pool, static_cast<char*>(workspace), w, num_seqs, num_tokens);
   if (st != PKV_OK) return st;
   int launches = 0;
   st = launch_attention(pool, layer, q, block_tables, context_lens, query_start_loc, max_blocks_per_seq, num_seqs, num_tokens, out,
-                        static_cast<char*>(workspace), w, (cudaStream_t)stream, &launches, FusedAppend(), win);
+                        static_cast<char*>(workspace), w, (cudaStream_t)stream, &launches, FusedAppend(), win,
+                        !append_since(pool, layer, plan));
   pool->last_launches = launches;
   return st;
 }
@@ -948,10 +961,11 @@ extern "C" pkv_status pkv_attention_append(pkv_pool* pool, int32_t layer, const 
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 16 != 0)
     return fail(PKV_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
   MetaCheck mc;
+  const PlanKey* plan = nullptr;
   st = validate_metadata(pool, block_tables, max_blocks_per_seq, context_lens, query_start_loc, num_seqs, num_tokens,
                          slot_mapping, stream, &mc, win.window, win.sinks);
   if (st == PKV_OK) st = check_plan(pool, workspace, context_lens, query_start_loc, num_seqs, num_tokens,
-                                    max_blocks_per_seq, mc);
+                                    max_blocks_per_seq, mc, &plan);
   if (st != PKV_OK) return st;
   const WsLayout w = ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks_per_seq, win);
   st = prepare_prefill_shadow(pool, static_cast<char*>(workspace), w, num_seqs, num_tokens);
@@ -965,14 +979,17 @@ extern "C" pkv_status pkv_attention_append(pkv_pool* pool, int32_t layer, const 
     if (st != PKV_OK) return st;
     launches = pool->last_launches;
     st = launch_attention(pool, layer, q, block_tables, context_lens, query_start_loc, max_blocks_per_seq, num_seqs, num_tokens,
-                          out, static_cast<char*>(workspace), w, (cudaStream_t)stream, &launches, FusedAppend(), win);
+                          out, static_cast<char*>(workspace), w, (cudaStream_t)stream, &launches, FusedAppend(), win,
+                          /*early=*/false);
   } else {
     FusedAppend fa;
     fa.k = k;
     fa.v = v;
     fa.slots = slot_mapping;
     st = launch_attention(pool, layer, q, block_tables, context_lens, query_start_loc, max_blocks_per_seq, num_seqs, num_tokens,
-                          out, static_cast<char*>(workspace), w, (cudaStream_t)stream, &launches, fa, win);
+                          out, static_cast<char*>(workspace), w, (cudaStream_t)stream, &launches, fa, win,
+                          !append_since(pool, layer, plan));
+    if (st == PKV_OK) note_append(pool, layer, plan->stamp);
   }
   pool->last_launches = launches;
   return st;

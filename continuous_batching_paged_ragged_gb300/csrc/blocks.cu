@@ -102,8 +102,8 @@ __device__ void copy_rows(const BlockGeo& g, int src, int dst, int rows, int p0,
 }
 
 // End of a kernel that writes cached rows.  The attention kernels stream their first blocks before their dependency
-// wait (only an append may run right ahead of them, and its rows are excepted there).  So the kernels below
-// release their dependents by ending, every thread's writes performed by then.
+// wait (only appends release their dependents earlier, and the attention call knows of those: append_since).  So the
+// kernels below release their dependents by ending, every thread's writes performed by then.
 __device__ __forceinline__ void publish() {
   __threadfence();
   dev::fence_proxy_async_global();

@@ -127,6 +127,9 @@ struct DecodeParams {
   // passed its own dependency wait, so the decode runs in the prefill's tail (on SMs the prefill has left)
   // and waits for it only at its end, so that whatever follows sees both complete.
   int late_wait;
+  // Whether K/V runs may be streamed ahead of the dependency wait: not while an append that this plan did not count on
+  // may be writing the rows (append_since).
+  int early;
   int layer_row0_k;    // TMA row of (layer, K, block 0, head 0, slot 0) (8-bit: rows of 128 code bytes)
   int layer_row0_v;    // TMA row of (layer, V, block 0, head 0, slot 0)
   int max_blocks;
@@ -481,13 +484,24 @@ struct Streamer {
     if (ok) issue_next();
     if (half_left > 0 && --half_left == 0 && lane == 0) dev::mbar_arrive(&sm.qmid[k % T::QD]);
   }
-  // Before the dependency wait: the first task, and its first K/V runs wherever nothing that the previous
+  // Before the dependency wait: the first task, and (p.early) its first K/V runs wherever nothing that the previous
   // kernel writes can be in them (positions the appended tokens never reach, or rows that are replaced
-  // from the appended inputs anyway).  q comes after the wait.
+  // from the appended inputs anyway).  q comes after the wait.  Behind an append of unknown tokens the runs go no further
+  // than L2: append and attention of 28 layers, 256 rows, take 0.967 ms so, 0.955 with the runs streamed ahead all the
+  // same and 1.015 with nothing ahead of the wait.
   __device__ void prologue() {
     take(0, cur);
     if (!ok) return;
     cur_q_done = cur.nbw == 0;
+    if (!p.early && !p.late_wait) {  // the same runs into L2, which an append still writes through
+      for (int r = lane; r < min((int)T::NR, runs(cur)); r += 32) {
+        int j, isv;
+        run_of(cur, r, j, isv);
+        const char* pool = reinterpret_cast<const char*>(isv ? p.cache_v : p.cache_k);
+        dev::bulk_prefetch_l2(pool + ((size_t)cur.ids[cur.bw + T::NW * j] * p.num_kv_heads + cur.g) * T::RUN, T::RUN);
+      }
+      return;
+    }
     while (issued < T::NR && issued < runs(cur)) {
       int jb, isv;
       run_of(cur, issued, jb, isv);

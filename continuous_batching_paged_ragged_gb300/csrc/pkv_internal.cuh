@@ -37,6 +37,13 @@ struct PlanKey {
   // a window longer than any context.
   int32_t window = 0x7FFFFFFF;
   int32_t sinks = 0;
+  uint64_t stamp = 0;  // when it was issued (pkv_pool::clock), which also names it
+};
+
+// The last append to a layer: when, and the plan whose own tokens a fused call appended (0: an append call).
+struct LayerWrite {
+  uint64_t stamp = 0;
+  uint64_t plan = 0;
 };
 
 // Plans remembered per pool: one per workspace, the most recently planned last.  A plan on a workspace
@@ -69,6 +76,10 @@ struct pkv_pool {
   int num_sms = 0;
   int device = 0;
   std::vector<pkv::PlanKey> plans;  // the plans issued through this pool, one per workspace (most recent last)
+  // Calls in the order they were made, and each layer's last append: what of a plan's rows may still be on its way into
+  // the cache when an attention call is launched (append_since).
+  uint64_t clock = 0;
+  std::vector<pkv::LayerWrite> writes;
   // 8-bit cache: tensor map of the fp16 shadow in the last workspace used for prefill rows (re-encoded when
   // the workspace or its size changes)
   CUtensorMap shadow_map;
@@ -84,6 +95,8 @@ pkv_status encode_f16_rows(CUtensorMap* map, void* base, uint64_t rows, int head
 // sub-tiles of 16 rows x 64 values (128-byte swizzle), sub-tile h at 2048 h bytes -- the layout of head_dim / 64
 // boxes of the 2-D map side by side, in one copy.
 pkv_status encode_f16_runs(CUtensorMap* map, void* base, uint64_t rows, int head_dim);
+// An append to `layer` has been launched: by a call of its own, or fused into an attention call under plan `plan`.
+void note_append(pkv_pool* pool, int layer, uint64_t plan = 0);
 // Refuses a call made while another device than the pool's is current.
 pkv_status check_device(const pkv_pool* pool);
 // The PKV_VALIDATE=1 host check of a call's device metadata (a no-op otherwise); null pointers are skipped.  Blocks
@@ -300,6 +313,11 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 // Brings the 128-byte line holding `addr` into L2 (a hint: no data returned, nothing to wait for).
 __device__ __forceinline__ void prefetch_l2(const void* addr) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(addr));
+}
+
+// A run of bytes into L2 (both multiples of 16): no data reaches the SM, so that it may run ahead of a wait.
+__device__ __forceinline__ void bulk_prefetch_l2(const void* addr, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(addr), "r"(bytes) : "memory");
 }
 
 // Orders this thread's generic-proxy shared-memory writes before later async-proxy (TMA) accesses.

@@ -152,6 +152,8 @@ static size_t cache_bytes_of(const pkv_config* c) {
   return (values_bytes_of(c) + scales + 255) / 256 * 256;
 }
 
+void note_append(pkv_pool* pool, int layer, uint64_t plan) { pool->writes[layer] = LayerWrite{++pool->clock, plan}; }
+
 pkv_status check_device(const pkv_pool* pool) {
   int device = -1;
   const cudaError_t e = cudaGetDevice(&device);
@@ -279,6 +281,7 @@ extern "C" pkv_status pkv_pool_init(const pkv_config* cfg, void* dev_cache, size
   p->scales_off = cfg->kv_dtype == PKV_KV_E4M3 ? values_bytes_of(cfg) : 0;
   p->dev_error = reinterpret_cast<int32_t*>(p->base + p->cache_bytes);
   p->device = attr.device;
+  p->writes.resize(cfg->num_layers);
   e = cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device);
   if (e != cudaSuccess) {
     delete p;
@@ -510,6 +513,7 @@ extern "C" pkv_status pkv_append(pkv_pool* pool, int32_t layer, const void* k, c
         break;
     }
     if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
+    note_append(pool, layer);
     pool->last_launches = 1;
     return PKV_OK;
   }
@@ -519,6 +523,7 @@ extern "C" pkv_status pkv_append(pkv_pool* pool, int32_t layer, const void* k, c
                              static_cast<uint4*>(pkv_pool_layer_ptr(pool, layer, 1)), (int)c.num_kv_heads, chunks,
                              (int64_t)c.num_blocks * c.block_size, pool->dev_error);
   if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
+  note_append(pool, layer);
   pool->last_launches = 1;
   return PKV_OK;
 }

@@ -376,6 +376,7 @@ extern "C" pkv_status pkv_rope_append(pkv_pool* pool, int32_t layer, const pkv_r
                         : c.head_dim == 128 ? launch_rope<128>(p, turns, f8, inter, s)
                                             : launch_rope<256>(p, turns, f8, inter, s);
   if (e != cudaSuccess) return cuda_fail(e, "rope_append launch");
+  note_append(pool, layer);
   pool->last_launches = 1;
   return PKV_OK;
 }

@@ -189,6 +189,8 @@ pkv_status pkv_append(pkv_pool* pool, int32_t layer, const void* k, const void* 
  * pool's other workspaces valid (double-buffered passes), up to the 32 most recently planned
  * workspaces per pool.  Plans and calls on one workspace must be ordered on one stream (or
  * synchronised by the caller).
+ * Calls on one stream see the cache as the calls before them left it, whatever an append between the plan and the
+ * attention wrote; cached rows that the caller's own kernels write are written before the plan.
  *
  * The result is independent of the batch: a row's split-K partition depends only on its own
  * context length, so a row gives bit-identical output alone or in any batch, in any row order.
