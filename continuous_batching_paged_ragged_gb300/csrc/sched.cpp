@@ -148,6 +148,14 @@ struct pkv_sched {
     return true;
   }
 
+  // The blocks registered as a request's prefix are nobody's any more (its id may come back with another prompt).
+  void forget(int64_t id) {
+    for (auto it = cached.lower_bound({id, 0}); it != cached.end() && it->first.first == id; it = cached.erase(it)) {
+      auto k = block_key.find(it->second);
+      if (k != block_key.end() && k->second == it->first) block_key.erase(k);
+    }
+  }
+
   // Blocks back to the free list's tail; keep registers a preempted request's full blocks for prefix
   // caching and returns them last block first.
   void release(Req* r, bool keep = false) {
@@ -392,6 +400,7 @@ extern "C" pkv_status pkv_sched_abort(pkv_sched* s, int64_t req_id) {
   auto wit = std::find(s->waiting.begin(), s->waiting.end(), r);
   if (wit != s->waiting.end()) s->waiting.erase(wit);
   s->release(r);
+  s->forget(req_id);
   s->live.erase(it);
   delete r;
   return PKV_OK;

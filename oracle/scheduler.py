@@ -218,6 +218,10 @@ class Scheduler:
         if req in self.waiting:
             self.waiting.remove(req)
         self._free(req)
+        for key in [k for k in self.cached if k[0] == req_id]:  # its id may come back with another prompt
+            block = self.cached.pop(key)
+            if self.block_key.get(block) == key:
+                del self.block_key[block]
         req.status = FINISHED
 
     def set_max_num_seqs(self, n: int) -> None:
