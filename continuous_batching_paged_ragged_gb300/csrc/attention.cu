@@ -696,6 +696,7 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
     if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
     *launches += 1;
     p.late_wait = 1;
+    p.early = 1;  // the prefill kernel has waited for every append
   }
   if (windowed) {
     e = f8 ? launch_decode_window_e4m3(c.head_dim, group, p, pool->num_sms, w.max_tasks, s)

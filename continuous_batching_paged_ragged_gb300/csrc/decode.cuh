@@ -486,23 +486,12 @@ struct Streamer {
   }
   // Before the dependency wait: the first task, and (p.early) its first K/V runs wherever nothing that the previous
   // kernel writes can be in them (positions the appended tokens never reach, or rows that are replaced
-  // from the appended inputs anyway).  q comes after the wait.  Behind an append of unknown tokens the runs go no further
-  // than L2: append and attention of 28 layers, 256 rows, take 0.967 ms so, 0.955 with the runs streamed ahead all the
-  // same and 1.015 with nothing ahead of the wait.
+  // from the appended inputs anyway).  q comes after the wait.
   __device__ void prologue() {
     take(0, cur);
     if (!ok) return;
     cur_q_done = cur.nbw == 0;
-    if (!p.early && !p.late_wait) {  // the same runs into L2, which an append still writes through
-      for (int r = lane; r < min((int)T::NR, runs(cur)); r += 32) {
-        int j, isv;
-        run_of(cur, r, j, isv);
-        const char* pool = reinterpret_cast<const char*>(isv ? p.cache_v : p.cache_k);
-        dev::bulk_prefetch_l2(pool + ((size_t)cur.ids[cur.bw + T::NW * j] * p.num_kv_heads + cur.g) * T::RUN, T::RUN);
-      }
-      return;
-    }
-    while (issued < T::NR && issued < runs(cur)) {
+    while (p.early && issued < T::NR && issued < runs(cur)) {
       int jb, isv;
       run_of(cur, issued, jb, isv);
       const int bpos = block_pos(cur, jb);
@@ -1150,6 +1139,19 @@ struct Scheduler {
     const int idx[kStaticTasks] = {c};
     last_idx = idx[0];
     publish(idx);
+    // Behind an append of unknown tokens the task's first runs go no further than L2, which the append writes through:
+    // append and attention of 28 layers, 256 rows, take 0.960 ms so, 0.948 with the runs streamed ahead all the same and
+    // 1.015 with nothing ahead of the wait.  (By this warp: in the streaming warps the code moved their spills, 7 % on the
+    // windowed 8-bit decode at d 256.)
+    if (!p.early) {
+      const TaskEntry* e = &sm.queue[0];
+      __syncwarp();
+      if (lane < min(e->nb, T::NW * ((T::NR + 1) / 2))) {
+        const size_t at = ((size_t)e->ids[lane] * p.num_kv_heads + (e->rec.y & 0xFF)) * T::RUN;
+        dev::bulk_prefetch_l2(reinterpret_cast<const char*>(p.cache_k) + at, T::RUN);
+        dev::bulk_prefetch_l2(reinterpret_cast<const char*>(p.cache_v) + at, T::RUN);
+      }
+    }
   }
   __device__ void run() {
     static_assert(kStaticTasks < T::QD, "queue");
