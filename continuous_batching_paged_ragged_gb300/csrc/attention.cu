@@ -566,16 +566,13 @@ __global__ void __launch_bounds__(256) dequant_prefill_rows_kernel(const Dequant
 }
 
 template <int D>
-static cudaError_t launch_dequant(const DequantParams& dq, int num_sms, cudaStream_t s) {
-  static bool attr = false;
+static cudaError_t launch_dequant(pkv_pool* pool, const DequantParams& dq, cudaStream_t s) {
   const size_t smem = (size_t)(dq.num_seqs + 1) * 4;
-  if (!attr && smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(dequant_prefill_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (kDequantMaxRows + 1) * 4);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = prepare_kernel(pool, dequant_prefill_rows_kernel<D>, (kDequantMaxRows + 1) * 4);
     if (e != cudaSuccess) return e;
-    attr = true;
   }
-  return launch_pdl(dequant_prefill_rows_kernel<D>, dim3((unsigned)(num_sms * 2)), dim3(256), smem, s, dq);
+  return launch_pdl(dequant_prefill_rows_kernel<D>, dim3((unsigned)(pool->num_sms * 2)), dim3(256), smem, s, dq);
 }
 
 // Inputs of an append fused into the decode launch (k == nullptr: not fused).
@@ -665,9 +662,9 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
       dq.num_blocks = c.num_blocks;
       dq.qsl = qsl;
       dq.win = win;
-      e = c.head_dim == 64    ? launch_dequant<64>(dq, pool->num_sms, s)
-          : c.head_dim == 128 ? launch_dequant<128>(dq, pool->num_sms, s)
-                              : launch_dequant<256>(dq, pool->num_sms, s);
+      e = c.head_dim == 64    ? launch_dequant<64>(pool, dq, s)
+          : c.head_dim == 128 ? launch_dequant<128>(pool, dq, s)
+                              : launch_dequant<256>(pool, dq, s);
       if (e != cudaSuccess) return cuda_fail(e, "dequantize launch");
       *launches += 1;
       a.kv_map = &pool->shadow_map;
@@ -689,7 +686,7 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
     a.num_q_heads = c.num_q_heads;
     a.num_kv_heads = c.num_kv_heads;
     a.head_dim = c.head_dim;
-    a.num_sms = pool->num_sms;
+    a.pool = pool;
     a.max_items = 2 * w.max_items;
     a.win = win;
     e = windowed ? launch_prefill_window(a, s) : launch_prefill(a, s);
@@ -699,15 +696,15 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
     p.early = 1;  // the prefill kernel has waited for every append
   }
   if (windowed) {
-    e = f8 ? launch_decode_window_e4m3(c.head_dim, group, p, pool->num_sms, w.max_tasks, s)
-           : launch_decode_window(c.head_dim, group, p, pool->num_sms, w.max_tasks, s);
+    e = f8 ? launch_decode_window_e4m3(c.head_dim, group, p, pool, w.max_tasks, s)
+           : launch_decode_window(c.head_dim, group, p, pool, w.max_tasks, s);
   } else if (f8) {
-    e = launch_decode_e4m3(c.head_dim, group, p, pool->num_sms, w.max_tasks, s);
+    e = launch_decode_e4m3(c.head_dim, group, p, pool, w.max_tasks, s);
   } else {
     switch (c.head_dim) {
-      case 64: e = launch_decode_g<64, kKvF16>(group, p, pool->num_sms, w.max_tasks, s); break;
-      case 128: e = launch_decode_g<128, kKvF16>(group, p, pool->num_sms, w.max_tasks, s); break;
-      case 256: e = launch_decode_g<256, kKvF16>(group, p, pool->num_sms, w.max_tasks, s); break;
+      case 64: e = launch_decode_g<64, kKvF16>(group, p, pool, w.max_tasks, s); break;
+      case 128: e = launch_decode_g<128, kKvF16>(group, p, pool, w.max_tasks, s); break;
+      case 256: e = launch_decode_g<256, kKvF16>(group, p, pool, w.max_tasks, s); break;
       default: return fail(PKV_ERR_UNSUPPORTED, "head_dim");
     }
   }
@@ -1012,35 +1009,34 @@ static __device__ __align__(256) unsigned char g_noalloc_scratch[kNoAllocScratch
 
 // The array's device address in the current context.  In host code the symbol name itself is only a
 // host-side stand-in and must never reach a kernel.  The address is looked up (cudaGetSymbolAddress, with the
-// device current) the first time a context calls, and cached per (device, context): a context created
-// after cudaDeviceReset loads the library's module again, so it gets its own lookup.
-using CtxGetCurrentFn = CUresult (*)(CUcontext*);
+// device current) the first time a context calls, and cached per context, by its id: a context created
+// after cudaDeviceReset loads the library's module again, so it gets its own lookup, and its handle may be an old one's.
+using CtxGetIdFn = CUresult (*)(CUcontext, unsigned long long*);
 
-static CtxGetCurrentFn ctx_get_current() {
-  static CtxGetCurrentFn fn = nullptr;
+static CtxGetIdFn ctx_get_id() {
+  static CtxGetIdFn fn = nullptr;
   if (!fn) {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &f, 12000, cudaEnableDefault, &q);
-    if (e == cudaSuccess && q == cudaDriverEntryPointSuccess && f) fn = reinterpret_cast<CtxGetCurrentFn>(f);
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuCtxGetId", &f, 12000, cudaEnableDefault, &q);
+    if (e == cudaSuccess && q == cudaDriverEntryPointSuccess && f) fn = reinterpret_cast<CtxGetIdFn>(f);
   }
   return fn;
 }
 
 struct ScratchAddr {
-  int device;
-  CUcontext ctx;
+  unsigned long long ctx;  // ids are never used again in a process
   void* ptr;
 };
 
-// The cached address for (device, context), or null when that context has not looked it up yet.
-static void* noalloc_scratch_cached(int device, CUcontext ctx, std::vector<ScratchAddr>& cache) {
+// The cached address for a context, or null when it has not been looked up yet.
+static void* noalloc_scratch_cached(unsigned long long ctx, std::vector<ScratchAddr>& cache) {
   for (const ScratchAddr& a : cache)
-    if (a.device == device && a.ctx == ctx) return a.ptr;
+    if (a.ctx == ctx) return a.ptr;
   return nullptr;
 }
 
-static pkv_status noalloc_scratch_ptr(int device, cudaStream_t stream, void** out) {
+static pkv_status noalloc_scratch_ptr(cudaStream_t stream, void** out) {
   static std::mutex mu;
   static std::vector<ScratchAddr> cache;
   *out = nullptr;
@@ -1049,12 +1045,12 @@ static pkv_status noalloc_scratch_ptr(int device, cudaStream_t stream, void** ou
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   cudaError_t e = cudaStreamIsCapturing(stream, &cap);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
-  CtxGetCurrentFn get = ctx_get_current();
-  if (!get) return fail(PKV_ERR_CUDA, "cuCtxGetCurrent is not available from the driver");
-  CUcontext ctx = nullptr;
-  if (get(&ctx) != CUDA_SUCCESS || !ctx) return fail(PKV_ERR_CUDA, "cuCtxGetCurrent found no current context");
+  CtxGetIdFn get = ctx_get_id();
+  if (!get) return fail(PKV_ERR_CUDA, "cuCtxGetId is not available from the driver");
+  unsigned long long ctx = 0;
+  if (get(nullptr, &ctx) != CUDA_SUCCESS) return fail(PKV_ERR_CUDA, "cuCtxGetId found no current context");
   std::lock_guard<std::mutex> lock(mu);
-  if (void* p = noalloc_scratch_cached(device, ctx, cache)) {
+  if (void* p = noalloc_scratch_cached(ctx, cache)) {
     *out = p;
     return PKV_OK;
   }
@@ -1064,7 +1060,7 @@ static pkv_status noalloc_scratch_ptr(int device, cudaStream_t stream, void** ou
   void* ptr = nullptr;
   e = cudaGetSymbolAddress(&ptr, g_noalloc_scratch);
   if (e != cudaSuccess || !ptr) return cuda_fail(e, "cudaGetSymbolAddress of the built-in scratch array");
-  cache.push_back(ScratchAddr{device, ctx, ptr});
+  cache.push_back(ScratchAddr{ctx, ptr});
   *out = ptr;
   return PKV_OK;
 }
@@ -1095,7 +1091,7 @@ extern "C" pkv_status pkv_attention_noalloc(pkv_pool* pool, int32_t layer, const
   if (device != pool->device) return fail(PKV_ERR_INVALID_ARG, "the pool's device must be the current device");
   cudaStream_t s = (cudaStream_t)stream;
   void* scratch = nullptr;
-  st = noalloc_scratch_ptr(device, s, &scratch);
+  st = noalloc_scratch_ptr(s, &scratch);
   if (st != PKV_OK) return st;
   // What must start at zero -- the task and split counters -- is cleared by the plan kernel on every call;
   // everything else is written before it is read.

@@ -114,7 +114,7 @@ struct PrefillArgs {
   int32_t* err;
   int layer_row0_k, layer_row0_v;
   int max_blocks, num_q_heads, num_kv_heads, num_blocks, head_dim;
-  int num_sms;
+  pkv_pool* pool;
   int64_t max_items;
   KeyWindow win;
 };

@@ -569,14 +569,6 @@ pkv_status fetch_for_validation(const int32_t* src, size_t n, void* stream, std:
   return PKV_OK;
 }
 
-template <typename K>
-cudaError_t allow_bulk_smem(K kernel, bool* done) {
-  if (*done) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBulkSmem);
-  *done = e == cudaSuccess;
-  return e;
-}
-
 // CTAs for up to `moves` block copies: a worker for every piece, up to what is resident at once.
 int64_t bulk_grid(const pkv_pool* pool, const BlockGeo& g, int64_t moves) {
   const int64_t pieces = moves * (g.planes + g.scale_planes);  // at least
@@ -623,8 +615,7 @@ extern "C" pkv_status pkv_copy_blocks(pkv_pool* pool, const int32_t* pairs, int3
     }
   }
   const BlockGeo g = geo_of(pool);
-  static bool smem_set = false;
-  cudaError_t e = allow_bulk_smem(copy_blocks_kernel, &smem_set);
+  cudaError_t e = prepare_kernel(pool, copy_blocks_kernel, kBulkSmem);
   if (e == cudaSuccess)
     e = launch_pdl(copy_blocks_kernel, dim3((unsigned)bulk_grid(pool, g, num_pairs)), dim3(kWorkers * 32), kBulkSmem,
                    (cudaStream_t)stream, g, pairs, (int)num_pairs);
@@ -722,8 +713,7 @@ extern "C" pkv_status pkv_compact(pkv_pool* pool, const int32_t* block_tables, i
   const unsigned movers = (unsigned)bulk_grid(pool, g, nb);  // the number of moves is known on the device alone
   const bool apart = p.entries == 0 || new_tables + p.entries <= block_tables || block_tables + p.entries <= new_tables;
   if (p.entries <= kSmallEntries && nb <= kSmallBlocks && apart) {
-    static bool small_set = false;
-    e = allow_bulk_smem(compact_small_kernel, &small_set);
+    e = prepare_kernel(pool, compact_small_kernel, kBulkSmem);
     if (e == cudaSuccess) e = launch_pdl(compact_small_kernel, dim3(movers), dim3(kWorkers * 32), kBulkSmem, s, g, p);
     if (e != cudaSuccess) return cuda_fail(e, "compact launch");
     pool->last_launches = 1;
@@ -743,8 +733,7 @@ extern "C" pkv_status pkv_compact(pkv_pool* pool, const int32_t* block_tables, i
     launches = 2;
   }
   if (e != cudaSuccess) return cuda_fail(e, "compact plan launch");
-  static bool smem_set = false;
-  e = allow_bulk_smem(compact_move_kernel, &smem_set);
+  e = prepare_kernel(pool, compact_move_kernel, kBulkSmem);
   if (e == cudaSuccess) e = launch_pdl(compact_move_kernel, dim3(movers), dim3(kWorkers * 32), kBulkSmem, s, g, p);
   if (e != cudaSuccess) return cuda_fail(e, "compact move launch");
   pool->last_launches = launches + 1;

@@ -8,6 +8,7 @@
 
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "attn_common.cuh"
@@ -1588,43 +1589,37 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
 }
 
 template <int D, int G, int KV, bool W = false>
-static cudaError_t launch_decode(const DecodeParams& p, int num_sms, int64_t max_tasks, cudaStream_t stream) {
+static cudaError_t launch_decode(const DecodeParams& p, pkv_pool* pool, int64_t max_tasks, cudaStream_t stream) {
   using T = DecodeTraits<D, G, KV>;
-  static int per_sm = 0;
-  if (per_sm == 0) {
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, G, KV, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
-    if (e != cudaSuccess) return e;
-    int n = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<D, G, KV, W>, T::NTHREADS, T::SMEM);
-    if (e != cudaSuccess) return e;
-    per_sm = n > 0 ? n : 1;
-  }
-  int64_t grid = (int64_t)num_sms * per_sm;  // persistent: one CTA per resident slot, one task at a time
+  int per_sm = 0;
+  const cudaError_t e = prepare_kernel(pool, decode_kernel<D, G, KV, W>, T::SMEM, T::NTHREADS, &per_sm);
+  if (e != cudaSuccess) return e;
+  int64_t grid = (int64_t)pool->num_sms * std::max(per_sm, 1);  // persistent: one CTA per resident slot, one task at a time
   if (grid > max_tasks) grid = max_tasks;
   if (grid < 1) grid = 1;
   return launch_pdl(decode_kernel<D, G, KV, W>, dim3((unsigned)grid), dim3(T::NTHREADS), T::SMEM, stream, p);
 }
 
 template <int D, int KV, bool W = false>
-static cudaError_t launch_decode_g(int group, const DecodeParams& p, int num_sms, int64_t max_tasks,
+static cudaError_t launch_decode_g(int group, const DecodeParams& p, pkv_pool* pool, int64_t max_tasks,
                                    cudaStream_t stream) {
   switch (group) {
-    case 1: return launch_decode<D, 1, KV, W>(p, num_sms, max_tasks, stream);
-    case 2: return launch_decode<D, 2, KV, W>(p, num_sms, max_tasks, stream);
-    case 4: return launch_decode<D, 4, KV, W>(p, num_sms, max_tasks, stream);
-    case 6: return launch_decode<D, 6, KV, W>(p, num_sms, max_tasks, stream);
-    case 8: return launch_decode<D, 8, KV, W>(p, num_sms, max_tasks, stream);
+    case 1: return launch_decode<D, 1, KV, W>(p, pool, max_tasks, stream);
+    case 2: return launch_decode<D, 2, KV, W>(p, pool, max_tasks, stream);
+    case 4: return launch_decode<D, 4, KV, W>(p, pool, max_tasks, stream);
+    case 6: return launch_decode<D, 6, KV, W>(p, pool, max_tasks, stream);
+    case 8: return launch_decode<D, 8, KV, W>(p, pool, max_tasks, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 // The 8-bit cache's instances live in their own translation unit (decode_e4m3.cu).
-cudaError_t launch_decode_e4m3(int head_dim, int group, const DecodeParams& p, int num_sms, int64_t max_tasks,
+cudaError_t launch_decode_e4m3(int head_dim, int group, const DecodeParams& p, pkv_pool* pool, int64_t max_tasks,
                                cudaStream_t stream);
 // The windowed instances of both formats in theirs (decode_window.cu, decode_window_e4m3.cu).
-cudaError_t launch_decode_window(int head_dim, int group, const DecodeParams& p, int num_sms, int64_t max_tasks,
+cudaError_t launch_decode_window(int head_dim, int group, const DecodeParams& p, pkv_pool* pool, int64_t max_tasks,
                                  cudaStream_t stream);
-cudaError_t launch_decode_window_e4m3(int head_dim, int group, const DecodeParams& p, int num_sms, int64_t max_tasks,
+cudaError_t launch_decode_window_e4m3(int head_dim, int group, const DecodeParams& p, pkv_pool* pool, int64_t max_tasks,
                                       cudaStream_t stream);
 
 }  // namespace pkv

@@ -4,12 +4,12 @@
 
 namespace pkv {
 
-cudaError_t launch_decode_window(int head_dim, int group, const DecodeParams& p, int num_sms, int64_t max_tasks,
+cudaError_t launch_decode_window(int head_dim, int group, const DecodeParams& p, pkv_pool* pool, int64_t max_tasks,
                                  cudaStream_t stream) {
   switch (head_dim) {
-    case 64: return launch_decode_g<64, kKvF16, true>(group, p, num_sms, max_tasks, stream);
-    case 128: return launch_decode_g<128, kKvF16, true>(group, p, num_sms, max_tasks, stream);
-    case 256: return launch_decode_g<256, kKvF16, true>(group, p, num_sms, max_tasks, stream);
+    case 64: return launch_decode_g<64, kKvF16, true>(group, p, pool, max_tasks, stream);
+    case 128: return launch_decode_g<128, kKvF16, true>(group, p, pool, max_tasks, stream);
+    case 256: return launch_decode_g<256, kKvF16, true>(group, p, pool, max_tasks, stream);
     default: return cudaErrorInvalidValue;
   }
 }

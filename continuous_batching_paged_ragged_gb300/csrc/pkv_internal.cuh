@@ -46,6 +46,12 @@ struct LayerWrite {
   uint64_t plan = 0;
 };
 
+// A kernel that this pool's calls have prepared in the pool's context (prepare_kernel).
+struct PreparedKernel {
+  const void* fn = nullptr;
+  int per_sm = 0;  // CTAs resident per SM, where it was asked for
+};
+
 // Plans remembered per pool: one per workspace, the most recently planned last.  A plan on a workspace
 // replaces that workspace's earlier plan and nothing else; past kMaxPlans workspaces the oldest is
 // forgotten (its next pkv_attention is refused until it is planned again).
@@ -80,6 +86,7 @@ struct pkv_pool {
   // the cache when an attention call is launched (append_since).
   uint64_t clock = 0;
   std::vector<pkv::LayerWrite> writes;
+  std::vector<pkv::PreparedKernel> kernels;
   // 8-bit cache: tensor map of the fp16 shadow in the last workspace used for prefill rows (re-encoded when
   // the workspace or its size changes)
   CUtensorMap shadow_map;
@@ -128,6 +135,27 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Allows a kernel `smem` bytes of dynamic shared memory and, with `per_sm`, asks how many of its CTAs of `threads` threads
+// are resident per SM, on its first launch for this pool.  The attribute belongs to the device's context, and so does a pool
+// (by its memory), which one host thread uses at a time: kept there, it holds for pools on other devices and for those
+// made after a device was reset.
+template <typename... KArgs>
+cudaError_t prepare_kernel(pkv_pool* pool, void (*kernel)(KArgs...), size_t smem, int threads = 0, int* per_sm = nullptr) {
+  const void* fn = reinterpret_cast<const void*>(kernel);
+  for (const PreparedKernel& k : pool->kernels)
+    if (k.fn == fn) {
+      if (per_sm) *per_sm = k.per_sm;
+      return cudaSuccess;
+    }
+  PreparedKernel k{fn, 0};
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && per_sm) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k.per_sm, kernel, threads, smem);
+  if (e != cudaSuccess) return e;
+  if (per_sm) *per_sm = k.per_sm;
+  pool->kernels.push_back(k);
+  return cudaSuccess;
 }
 
 }  // namespace pkv

@@ -945,28 +945,24 @@ __global__ void __launch_bounds__(PfTraits<D, G>::THREADS, 1) prefill_kernel(con
 }
 
 template <int D, int G, bool W>
-cudaError_t launch_t(const PfParams& p, int num_sms, int64_t max_items, cudaStream_t stream) {
+cudaError_t launch_t(const PfParams& p, pkv_pool* pool, int64_t max_items, cudaStream_t stream) {
   using T = PfTraits<D, G>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, G, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
-  int64_t grid = num_sms;  // one CTA per SM (shared memory and tensor memory bound)
+  const cudaError_t e = prepare_kernel(pool, prefill_kernel<D, G, W>, T::SMEM);
+  if (e != cudaSuccess) return e;
+  int64_t grid = pool->num_sms;  // one CTA per SM (shared memory and tensor memory bound)
   if (grid > max_items) grid = max_items;
   if (grid < 1) grid = 1;
   return launch_pdl(prefill_kernel<D, G, W>, dim3((unsigned)grid), dim3(T::THREADS), T::SMEM, stream, p);
 }
 
 template <int D, bool W>
-cudaError_t launch_d(int group, const PfParams& p, int num_sms, int64_t max_items, cudaStream_t s) {
+cudaError_t launch_d(int group, const PfParams& p, pkv_pool* pool, int64_t max_items, cudaStream_t s) {
   switch (group) {
-    case 1: return launch_t<D, 1, W>(p, num_sms, max_items, s);
-    case 2: return launch_t<D, 2, W>(p, num_sms, max_items, s);
-    case 4: return launch_t<D, 4, W>(p, num_sms, max_items, s);
-    case 6: return launch_t<D, 6, W>(p, num_sms, max_items, s);
-    case 8: return launch_t<D, 8, W>(p, num_sms, max_items, s);
+    case 1: return launch_t<D, 1, W>(p, pool, max_items, s);
+    case 2: return launch_t<D, 2, W>(p, pool, max_items, s);
+    case 4: return launch_t<D, 4, W>(p, pool, max_items, s);
+    case 6: return launch_t<D, 6, W>(p, pool, max_items, s);
+    case 8: return launch_t<D, 8, W>(p, pool, max_items, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -995,9 +991,9 @@ cudaError_t launch_prefill_items(const PrefillArgs& a, cudaStream_t stream) {
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)a.head_dim));
   const int group = a.num_q_heads / a.num_kv_heads;
   switch (a.head_dim) {
-    case 64: return launch_d<64, W>(group, p, a.num_sms, a.max_items, stream);
-    case 128: return launch_d<128, W>(group, p, a.num_sms, a.max_items, stream);
-    case 256: return launch_d<256, W>(group, p, a.num_sms, a.max_items, stream);
+    case 64: return launch_d<64, W>(group, p, a.pool, a.max_items, stream);
+    case 128: return launch_d<128, W>(group, p, a.pool, a.max_items, stream);
+    case 256: return launch_d<256, W>(group, p, a.pool, a.max_items, stream);
     default: return cudaErrorInvalidValue;
   }
 }
