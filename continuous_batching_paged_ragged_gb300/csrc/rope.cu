@@ -5,8 +5,9 @@
 // opening section and "The allocator is the other half").
 //
 // Angles: the position reaches millions and cos needs it modulo a turn, where a 32-bit product has no bits left.  So
-// f_i / (2 pi) is a 64-bit binary fraction of a turn; position times it, wrapping modulo 2^64, is the angle modulo
-// a turn to position * 2^-64, and its upper half (a signed 32-bit fraction of a turn) goes to sincospif.
+// f_i / (2 pi) is a 64-bit binary fraction of a turn; position times it, wrapping modulo 2^64, is that fraction's angle
+// modulo a turn, exactly, and its upper half (a signed 32-bit fraction of a turn) goes to sincospif.  The fraction comes
+// from a 64-bit float: 53 bits, off by less than 2^-53 of a turn for frequencies up to 1.
 // No 64-bit floating point on the device.
 //
 // Bound by memory: q, k and v read once, q_out and the slots written once.
@@ -241,7 +242,7 @@ extern "C" pkv_status pkv_rope_create(const pkv_rope_config* cfg, pkv_rope** out
   if (c.scaling < PKV_ROPE_SCALE_NONE || c.scaling > PKV_ROPE_SCALE_RAMP) return fail(PKV_ERR_INVALID_ARG, "unknown scaling");
   if (!(c.base > 1.0) || !std::isfinite(c.base)) return fail(PKV_ERR_INVALID_ARG, "base must be above 1");
   if (c.output_scale == 0.0) c.output_scale = 1.0;
-  if (!std::isfinite(c.output_scale)) return fail(PKV_ERR_INVALID_ARG, "output_scale must be finite");
+  if (!std::isfinite((float)c.output_scale)) return fail(PKV_ERR_INVALID_ARG, "output_scale must be finite in 32 bits");
   if (c.scaling != PKV_ROPE_SCALE_NONE && (!(c.factor > 0.0) || !std::isfinite(c.factor)))
     return fail(PKV_ERR_INVALID_ARG, "factor must be positive");
   if (c.scaling == PKV_ROPE_SCALE_BANDS || c.scaling == PKV_ROPE_SCALE_RAMP) {
@@ -276,6 +277,10 @@ extern "C" pkv_status pkv_rope_create(const pkv_rope_config* cfg, pkv_rope** out
       default: break;
     }
     if (w < 1.0) f = w * f + (1.0 - w) * f / c.factor;
+    if (!std::isfinite(f)) {
+      delete r;
+      return fail(PKV_ERR_INVALID_ARG, "factor is too small: a frequency is not finite");
+    }
     r->freq[i] = f;
     const double turn = f / kTwoPi;  // whole turns drop out (a factor below 1 can make it pass one)
     r->turn[i] = (uint64_t)std::ldexp(turn - std::floor(turn), 64);

@@ -316,9 +316,9 @@ pkv_status pkv_attention_noalloc(pkv_pool* pool, int32_t layer, const void* q, c
  *                            pair(t) = rot_dim ln(original_context / (2 pi t)) / (2 ln base),
  *                            lo = max(floor(pair(high_turns)), 0), hi = min(ceil(pair(low_turns)), rot_dim - 1)
  * Angles are reduced modulo a turn exactly: f_i (computed in 64-bit floating point) over 2 pi is held as a 64-bit
- * binary fraction, and its product with the position wraps.  Frequencies up to 1 are 53 bits of that fraction: below
- * 2^-24 turns off at any int32 position, 2^-34 below a million tokens.  cos, sin and the rotation are fp32; each result
- * is rounded once to fp16.
+ * binary fraction, and its product with the position wraps.  For frequencies up to 1 the fraction is off by less than
+ * 2^-53: 2^-22 turns at any int32 position, 2^-33 below a million tokens.  cos, sin and the rotation are fp32; each result
+ * is rounded once to fp16.  Frequencies and output_scale have to be finite (in 64 and 32 bits; else PKV_ERR_INVALID_ARG).
  * ---------------------------------------------------------------------------------------------- */
 #define PKV_ROPE_HALF         0
 #define PKV_ROPE_INTERLEAVED  1
