@@ -454,12 +454,12 @@ __global__ void __launch_bounds__(256) slot_mapping_kernel(const int32_t* __rest
                                                            int64_t* __restrict__ slot_mapping, int32_t* err) {
   dev::griddep_wait();
   dev::griddep_launch_dependents();
-  for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < num_tokens; t += gridDim.x * blockDim.x) {
-    const int b = dev::row_of_token(qsl, num_seqs, t);
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < num_tokens; i += (int64_t)gridDim.x * blockDim.x) {
+    const int t = (int)i, b = dev::row_of_token(qsl, num_seqs, t);
     const int q0 = __ldg(qsl + b), q1 = __ldg(qsl + b + 1);
     const int q_len = q1 - q0, ctx = __ldg(context_lens + b);
     int64_t slot = -1;
-    if (t >= q1 || q_len < 1 || ctx < q_len || ctx > max_blocks * 16) {
+    if (t < q0 || t >= q1 || q_len < 1 || ctx < q_len || ctx > (int64_t)max_blocks * 16) {
       dev::set_error(err, PKV_DEVERR_ROW_META);
     } else {
       const int p = ctx - q_len + (t - q0);
@@ -544,8 +544,7 @@ extern "C" pkv_status pkv_slot_mapping(pkv_pool* pool, const int32_t* block_tabl
                                      num_tokens, nullptr, stream, nullptr, 0x7FFFFFFF, 0, /*none_ok=*/true);
   if (vst != PKV_OK) return vst;
   const int threads = 256;
-  int blocks = (num_tokens + threads - 1) / threads;
-  if (blocks > pool->num_sms * 8) blocks = pool->num_sms * 8;
+  const int blocks = (int)std::min<int64_t>(((int64_t)num_tokens + threads - 1) / threads, pool->num_sms * 8);
   cudaError_t e = launch_pdl(slot_mapping_kernel, dim3(blocks), dim3(threads), 0, (cudaStream_t)stream, block_tables,
                              (int)max_blocks_per_seq, context_lens, query_start_loc, (int)num_seqs, (int)num_tokens,
                              (int)pool->cfg.num_blocks, slot_mapping, pool->dev_error);

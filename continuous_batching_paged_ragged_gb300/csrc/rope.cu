@@ -203,8 +203,8 @@ __global__ void __launch_bounds__(256) positions_kernel(const int32_t* __restric
                                                         int32_t* __restrict__ positions, int32_t* err) {
   dev::griddep_wait();
   dev::griddep_launch_dependents();
-  for (int t = blockIdx.x * blockDim.x + threadIdx.x; t < num_tokens; t += gridDim.x * blockDim.x) {
-    const int b = dev::row_of_token(qsl, num_seqs, t);
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < num_tokens; i += (int64_t)gridDim.x * blockDim.x) {
+    const int t = (int)i, b = dev::row_of_token(qsl, num_seqs, t);
     const int q0 = __ldg(qsl + b), q1 = __ldg(qsl + b + 1), ctx = __ldg(context_lens + b);
     const bool ok = t >= q0 && t < q1 && ctx >= q1 - q0;
     if (!ok) dev::set_error(err, PKV_DEVERR_ROW_META);
@@ -310,10 +310,10 @@ extern "C" pkv_status pkv_positions(pkv_pool* pool, const int32_t* context_lens,
   if (!context_lens || !query_start_loc || !positions)
     return fail(PKV_ERR_INVALID_ARG, "metadata pointers must be non-NULL");
   pkv_status st = check_device(pool);
-  if (st == PKV_OK) st = validate_metadata(pool, nullptr, 0x7FFFFFF, context_lens, query_start_loc, num_seqs, num_tokens, nullptr,
+  if (st == PKV_OK) st = validate_metadata(pool, nullptr, 1 << 27, context_lens, query_start_loc, num_seqs, num_tokens, nullptr,
                                            stream);
   if (st != PKV_OK) return st;
-  const int blocks = std::min((num_tokens + 255) / 256, pool->num_sms * 8);
+  const int blocks = (int)std::min<int64_t>(((int64_t)num_tokens + 255) / 256, pool->num_sms * 8);
   const cudaError_t e = launch_pdl(positions_kernel, dim3(blocks), dim3(256), 0, (cudaStream_t)stream, context_lens,
                                    query_start_loc, (int)num_seqs, (int)num_tokens, positions, pool->dev_error);
   if (e != cudaSuccess) return cuda_fail(e, "positions launch");
