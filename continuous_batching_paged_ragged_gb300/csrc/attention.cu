@@ -749,7 +749,7 @@ static pkv_status check_common(pkv_pool* pool, const int32_t* context_lens, cons
   const int64_t splits = ((int64_t)max_blocks + c.split_blocks - 1) / c.split_blocks;
   if (splits >= (1 << 23) || (int64_t)num_tokens * c.num_kv_heads * splits >= (1ll << 31))
     return fail(PKV_ERR_UNSUPPORTED, "too many splits in one pass; raise split_blocks");
-  return PKV_OK;
+  return check_device(pool);
 }
 
 static pkv_status check_workspace(pkv_pool* pool, void* workspace, size_t ws_bytes, int32_t num_seqs, int32_t num_tokens,
@@ -1085,10 +1085,6 @@ extern "C" pkv_status pkv_attention_noalloc(pkv_pool* pool, int32_t layer, const
   if (w.total > kNoAllocScratchBytes)
     return fail(PKV_ERR_OUT_OF_RANGE, "pass needs " + std::to_string(w.total) + " bytes of scratch; the built-in "
                 "array holds " + std::to_string(kNoAllocScratchBytes) + " (use pkv_attention with a workspace)");
-  int device = -1;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  if (device != pool->device) return fail(PKV_ERR_INVALID_ARG, "the pool's device must be the current device");
   cudaStream_t s = (cudaStream_t)stream;
   void* scratch = nullptr;
   st = noalloc_scratch_ptr(s, &scratch);
@@ -1098,7 +1094,7 @@ extern "C" pkv_status pkv_attention_noalloc(pkv_pool* pool, int32_t layer, const
   char* ws = static_cast<char*>(scratch);
   st = prepare_prefill_shadow(pool, ws, w, num_seqs, num_tokens);
   if (st != PKV_OK) return st;
-  e = launch_plan(pool, ws, w, context_lens, query_start_loc, num_seqs, num_tokens, max_blocks_per_seq, s);
+  cudaError_t e = launch_plan(pool, ws, w, context_lens, query_start_loc, num_seqs, num_tokens, max_blocks_per_seq, s);
   if (e != cudaSuccess) return cuda_fail(e, "plan launch");
   int launches = 1;
   st = launch_attention(pool, layer, q, block_tables, context_lens, query_start_loc, max_blocks_per_seq, num_seqs, num_tokens, out,

@@ -484,7 +484,8 @@ extern "C" pkv_status pkv_append(pkv_pool* pool, int32_t layer, const void* k, c
   if (!k || !v || !slot_mapping) return fail(PKV_ERR_INVALID_ARG, "k, v and slot_mapping must be non-NULL");
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) % 16 != 0)
     return fail(PKV_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
-  pkv_status vst = validate_metadata(pool, nullptr, 0, nullptr, nullptr, 0, num_tokens, slot_mapping, stream);
+  pkv_status vst = check_device(pool);
+  if (vst == PKV_OK) vst = validate_metadata(pool, nullptr, 0, nullptr, nullptr, 0, num_tokens, slot_mapping, stream);
   if (vst != PKV_OK) return vst;
   const pkv_config& c = pool->cfg;
   const int chunks = c.head_dim / 8;
@@ -540,8 +541,9 @@ extern "C" pkv_status pkv_slot_mapping(pkv_pool* pool, const int32_t* block_tabl
   if (max_blocks_per_seq < 1) return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq must be >= 1");
   if (!block_tables || !context_lens || !query_start_loc || !slot_mapping)
     return fail(PKV_ERR_INVALID_ARG, "metadata pointers must be non-NULL");
-  pkv_status vst = validate_metadata(pool, block_tables, max_blocks_per_seq, context_lens, query_start_loc, num_seqs,
-                                     num_tokens, nullptr, stream, nullptr, 0x7FFFFFFF, 0, /*none_ok=*/true);
+  pkv_status vst = check_device(pool);
+  if (vst == PKV_OK) vst = validate_metadata(pool, block_tables, max_blocks_per_seq, context_lens, query_start_loc, num_seqs,
+                                             num_tokens, nullptr, stream, nullptr, 0x7FFFFFFF, 0, /*none_ok=*/true);
   if (vst != PKV_OK) return vst;
   const int threads = 256;
   const int blocks = (int)std::min<int64_t>(((int64_t)num_tokens + threads - 1) / threads, pool->num_sms * 8);

@@ -14,6 +14,7 @@
  *     memory; where it needs scratch, the caller passes a workspace sized by a *_bytes query.
  *   - GPU work is enqueued asynchronously on `stream` (a cudaStream_t passed as void*; NULL = legacy
  *     default stream).  A call returns before its kernels finish.
+ *   - The pool's device is the current device in every call that launches (PKV_ERR_INVALID_ARG otherwise).
  *   - Argument and shape errors are detected on the host and returned BEFORE anything is launched;
  *     pkv_last_error() then holds a message (thread-local, valid until the next call on the thread).
  *   - Contents of device metadata (block ids, slots, lengths) cannot be checked on the host without a
