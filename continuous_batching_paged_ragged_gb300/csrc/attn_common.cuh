@@ -42,8 +42,9 @@ struct KeyWindow {
 // A windowed plan's tokens mostly see the same number of blocks, a little more than a power of two of them: full splits
 // of 32 would leave each token a last split of a few blocks, whose cost is that of a task and not of its blocks.  So a
 // token cut by its window runs in equal splits, rounded up to eight blocks (two for each streaming warp, a pair on the
-// 8-bit d 256 path): 66 blocks as 24 + 24 + 18 take 49.7 us, as 32 + 32 + 2 54.6 (256 rows, 12 / 2 heads, d 128); 34 as
-// 24 + 10 32.5 against 36.2; 261 stay at 32 (104 us on the 8-bit cache at d 256, 120 in splits of 28).  The window
+// 8-bit d 256 path): 66 blocks as 24 + 24 + 18 take 51.2 us, as 32 + 32 + 2 54.4 (256 rows, 12 / 2 heads, d 128); 34 as
+// 24 + 10 33.0 against 36.2; 261 stay at 32 (103 us on the 8-bit cache at d 256, 120 in splits of 28).  At head_dim 64,
+// whose warps go in pairs of blocks, the 66 would be faster as 32 + 32 + 2 (8 / 2 heads: 41.0 us, 45.6 so).  The window
 // alone decides, and a token whose whole context is visible keeps the unwindowed partition.
 __host__ __device__ constexpr int window_blocks_at_most(int window, int sinks) {
   return (sinks + kBS - 1) / kBS + (window > kNoWindow - kBS ? kNoWindow / kBS : (window + kBS - 2) / kBS) + 1;

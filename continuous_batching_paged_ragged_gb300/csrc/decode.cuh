@@ -657,7 +657,8 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
             o[mt][2] *= a0;
             o[mt][3] *= a1;
           }
-          // ---- O^T[d x 8 heads] += V^T P^T for both blocks ----
+          // ---- O^T[d x 8 heads] += V^T P^T for both blocks; the MMA takes weights in fp16 (at most 2^-11 of each off),
+          // the sums l0, l1 have them in fp32 ----
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             float s0 = 1.f, s1 = 1.f;

@@ -377,8 +377,8 @@ __device__ __forceinline__ void named_bar_arrive(int id, int count) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// True in one lane of the (converged) warp, the same one every time.  Code it guards is known to run in a single thread,
-// so that operands which are the same in every lane stay in uniform registers.
+// True in one lane of the (converged) warp, the same one every time (MMAs issued by a thread picked so come faster than
+// by one picked by its lane number: prefill.cuh).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));

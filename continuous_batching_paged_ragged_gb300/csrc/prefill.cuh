@@ -19,13 +19,14 @@
 //    Warpgroups 0 and 1 (softmax) each own one Q tile, one S/O row per thread (TMEM lane = thread):
 //    they load S with tcgen05.ld, apply the causal mask and an online softmax in the log2 domain, and
 //    store P as fp16 over the S they just read (tcgen05.st); the product takes P straight from tensor
-//    memory.  Per group the order is S(j), P(j)V, S(j + 1), P(j + 1)V, ...: while one group runs its
-//    softmax the tensor core works on the other group's products and scores.
+//    memory.  (P is rounded to fp16, at most 2^-11 of each weight off, because the tensor core multiplies fp16 by
+//    fp16; the running sum adds the weights in fp32, before that rounding.)  Per group the order is S(j), P(j)V,
+//    S(j + 1), P(j + 1)V, ...: while one group runs its softmax the tensor core works on the other group's products
+//    and scores.
 //  * Measured on GB300, cycles per 128 x 128 x 16 tcgen05.mma (64 at the tensor core's rate): one thread picked by its
 //    lane number issues one every 142 from shared memory (scores) and 96 with A in tensor memory (products),
-//    whatever N up to 128 -- the compiler moves every operand to the uniform registers again for each; picked by
-//    elect.sync, 107 and 70; two warps together 88 and 66 (both operands from shared memory are bound by its
-//    bandwidth).  Hence one issuing warp per Q tile, an elected thread, and 128-wide score tiles (not 64).
+//    whatever N up to 128; picked by elect.sync, 107 and 70; two warps together 88 and 66.  Hence one issuing warp per
+//    Q tile, an elected thread, and 128-wide score tiles (not 64).
 //  * The running max is lazy: O (in TMEM) and the running sum are rescaled only when a row's max grows
 //    by more than 8 (a factor 256), which keeps P <= 256 and the arithmetic exact up to rounding.
 //  * Windowed instances (W): an item's K/V tiles are packed from the blocks that some of its positions see -- the

@@ -177,8 +177,9 @@ pkv_status pkv_append(pkv_pool* pool, int32_t layer, const void* k, const void* 
  * Row b owns query tokens query_start_loc[b] .. query_start_loc[b+1]-1 (q_len_b of them) and
  * context_lens[b] keys, this pass's appended tokens included.  Query i of the row is at absolute
  * position ctx_b - q_len_b + i and attends causally to keys 0 .. ctx_b - q_len_b + i.  Query head h
- * reads KV head h / (num_q_heads / num_kv_heads).  Scores are scaled by 1/sqrt(head_dim); softmax
- * and accumulation in fp32; output rounded once to fp16 (round-to-nearest-even).
+ * reads KV head h / (num_q_heads / num_kv_heads).  Scores are scaled by 1/sqrt(head_dim); scores, the softmax's maximum
+ * and sum and the accumulation in fp32; each softmax weight (before its division by the sum) is rounded to fp16 for its
+ * product with V on the tensor cores, and the output once to fp16 (both round-to-nearest-even).
  *
  * Use: size a workspace with pkv_attention_workspace_bytes, call pkv_attention_plan once per pass
  * (after the metadata is on the device), then pkv_attention once per layer.  A plan stays valid
@@ -256,7 +257,8 @@ pkv_status pkv_attention_append(pkv_pool* pool, int32_t layer, const void* q, co
  * Everything said of pkv_attention_plan holds, and:
  *   - context_lens still count the whole row, and block tables still have an entry for every 16 tokens.  Entries
  *     of blocks that no new token of the row sees -- every key at or past the sinks, and in front of
- *     the window of the row's first new token -- are never read: they may be -1 and the blocks freed.
+ *     the window of the row's first new token -- are never read: they may be -1 and the blocks freed (by the
+ *     caller: the host scheduler below keeps the blocks of a request's whole context).
  *   - Keys and values that a query does not see have no part in its result, whatever they hold, with one
  *     exception: in a row of 16 or more new tokens, a non-finite value (of V) that is seen by one of the row's
  *     queries may reach the row's other queries.
