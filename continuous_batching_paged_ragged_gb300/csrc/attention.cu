@@ -164,7 +164,7 @@ struct PlanParams {
   const int32_t* context_lens;
   const int32_t* qsl;
   int num_seqs, num_tokens, max_ctx, split_blocks, num_kv_heads;
-  int prefill_min_qlen;  // rows with at least this many new tokens become prefill items (0: none)
+  int prefill_min_qlen;  // rows with at least this many new tokens become prefill items (0: none; plan_kernel's min_qlen)
   int prefill_pos;       // query positions per prefill item
   int prefill_keys;      // keys per prefill K/V tile
   int prefill_ctas;      // CTAs of the prefill tile kernel at most (the SM count)
@@ -190,10 +190,10 @@ __device__ __forceinline__ bool row_meta_ok(int q_len, int ctx, int max_ctx) {
 // Prefill items of row b in plan order, one per position block: `fn(n, npos, first token, w)` with n the
 // item's K/V tiles and w the keys visible to its first position minus one.
 template <typename F>
-__device__ __forceinline__ void for_row_items(const PlanParams& p, int b, F fn) {
+__device__ __forceinline__ void for_row_items(const PlanParams& p, int b, int min_qlen, F fn) {
   const int q0 = __ldg(p.qsl + b), q1 = __ldg(p.qsl + b + 1), ctx = __ldg(p.context_lens + b);
   const int q_len = q1 - q0;
-  if (p.prefill_min_qlen <= 0 || q_len < p.prefill_min_qlen || !row_meta_ok(q_len, ctx, p.max_ctx)) return;
+  if (min_qlen <= 0 || q_len < min_qlen || !row_meta_ok(q_len, ctx, p.max_ctx)) return;
   for (int qb = 0; qb * p.prefill_pos < q_len; ++qb) {
     const int npos = min(p.prefill_pos, q_len - qb * p.prefill_pos);
     const int w = ctx - q_len + qb * p.prefill_pos;
@@ -213,9 +213,9 @@ __device__ __forceinline__ VisibleUnits row_blocks(int ctx, int q_len, const Key
 __device__ __forceinline__ int split_first(int n) { return (n + 1) / 2; }
 
 // K/V tiles of all of row b's prefill items, over every KV head.
-__device__ __forceinline__ int64_t row_prefill_tiles(const PlanParams& p, int b) {
+__device__ __forceinline__ int64_t row_prefill_tiles(const PlanParams& p, int b, int min_qlen) {
   int64_t t = 0;
-  for_row_items(p, b, [&](int n, int, int, int) { t += n; });
+  for_row_items(p, b, min_qlen, [&](int n, int, int, int) { t += n; });
   return t * p.num_kv_heads;
 }
 
@@ -234,10 +234,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   __shared__ int tail_at[kMaxSplitBlocks + 1];  // per last-split size: its task count, then its next slot
   __shared__ int n_dec;
   dev::griddep_wait();
+  int bad_qsl = 0, empty_row = 0;
   for (int i = threadIdx.x; i < p.num_seqs; i += blockDim.x) {
     const int q0 = __ldg(p.qsl + i), q1 = __ldg(p.qsl + i + 1), ctx = __ldg(p.context_lens + i);
-    if (q1 < q0 || (i == 0 && q0 != 0) || (i == p.num_seqs - 1 && q1 != p.num_tokens))
+    if (q1 < q0 || (i == 0 && q0 != 0) || (i == p.num_seqs - 1 && q1 != p.num_tokens)) {
       dev::set_error(p.err, PKV_DEVERR_QSL);
+      bad_qsl = 1;
+    }
+    empty_row |= q1 == q0;
     if (!row_meta_ok(q1 - q0, ctx, p.max_ctx)) dev::set_error(p.err, PKV_DEVERR_ROW_META);
   }
   for (int i = threadIdx.x; i < p.num_tokens * p.num_kv_heads; i += blockDim.x) p.merge_cnt[i] = 0;
@@ -245,7 +249,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   for (int i = threadIdx.x; i <= kMaxSplitBlocks; i += blockDim.x) tail_at[i] = 0;
   for (int i = threadIdx.x; i < p.max_slots; i += blockDim.x) p.pf_sync[i] = make_int2(0, 0);
   if (threadIdx.x == 0) n_slots = 0;
-  __syncthreads();
+  // Reported passes stay inside the workspace and the packed rows: one whose query_start_loc is no list of rows gets no
+  // work, and beside a row without tokens (the room for prefill items counts on none) every row takes the decode path.
+  bad_qsl = __syncthreads_or(bad_qsl);
+  empty_row = __syncthreads_or(empty_row);
+  const int min_qlen = bad_qsl || empty_row ? 0 : p.prefill_min_qlen;
 
   // ---- decode tasks: tokens of rows that are not prefill items ----
   // Largest first: every token's splits but the last in token order, then the last splits by decreasing
@@ -260,8 +268,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       const int b = dev::row_of_token(p.qsl, p.num_seqs, t);
       const int q0 = __ldg(p.qsl + b), q1 = __ldg(p.qsl + b + 1), ctx = __ldg(p.context_lens + b);
       const int q_len = q1 - q0;
-      const bool prefill = p.prefill_min_qlen > 0 && q_len >= p.prefill_min_qlen;
-      if (t >= q0 && t < q1 && row_meta_ok(q_len, ctx, p.max_ctx) && !prefill) c = ctx - q_len + (t - q0) + 1;
+      const bool prefill = min_qlen > 0 && q_len >= min_qlen;
+      if (!bad_qsl && t >= q0 && t < q1 && row_meta_ok(q_len, ctx, p.max_ctx) && !prefill) c = ctx - q_len + (t - q0) + 1;
       p.tok_row[t] = b;
       p.tok_ctx[t] = c;  // 0: no decode work (prefill row or invalid metadata)
       row = b;
@@ -302,8 +310,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   // ---- prefill work entries, bucketed by K/V tile count, longest first; long items in two chunks ----
   auto bucket_of = [](int cost) { return kPrefillBuckets - 1 - min(cost, kPrefillBuckets - 1); };
   for (int b = threadIdx.x; b < p.num_seqs; b += blockDim.x) {
-    const int64_t row_tiles = row_prefill_tiles(p, b);
-    for_row_items(p, b, [&](int n, int, int, int) {
+    const int64_t row_tiles = row_prefill_tiles(p, b, min_qlen);
+    for_row_items(p, b, min_qlen, [&](int n, int, int, int) {
       if (split_item(p, n, row_tiles)) {
         atomicAdd(&hist[bucket_of(split_first(n))], p.num_kv_heads);
         atomicAdd(&hist[bucket_of(n - split_first(n))], p.num_kv_heads);
@@ -325,8 +333,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     __syncthreads();
   }
   for (int b = threadIdx.x; b < p.num_seqs; b += blockDim.x) {
-    const int64_t row_tiles = row_prefill_tiles(p, b);
-    for_row_items(p, b, [&](int n, int npos, int t0, int w) {
+    const int64_t row_tiles = row_prefill_tiles(p, b, min_qlen);
+    for_row_items(p, b, min_qlen, [&](int n, int npos, int t0, int w) {
       const bool split = split_item(p, n, row_tiles);
       const int slot = split ? atomicAdd(&n_slots, p.num_kv_heads) : -1;
       for (int chunk = 0; chunk < (split ? 2 : 1); ++chunk) {
@@ -348,7 +356,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       int nb = 0;
       if (b < p.num_seqs) {
         const int q_len = __ldg(p.qsl + b + 1) - __ldg(p.qsl + b), ctx = __ldg(p.context_lens + b);
-        if (p.prefill_min_qlen > 0 && q_len >= p.prefill_min_qlen && row_meta_ok(q_len, ctx, p.max_ctx))
+        if (min_qlen > 0 && q_len >= min_qlen && row_meta_ok(q_len, ctx, p.max_ctx))
           nb = row_blocks(ctx, q_len, p.win).n;
       }
       int total = 0;

@@ -204,6 +204,10 @@ pkv_status pkv_append(pkv_pool* pool, int32_t layer, const void* k, const void* 
  * shadow blocks, R the most rows of 16+ new tokens the pass can hold.  Rows may share blocks (forks of a prompt that is
  * still being computed): that many hold them all.
  *
+ * Rows are there to be attended: each has a new token.  A pass with rows that have none is reported
+ * (PKV_DEVERR_ROW_META) and its other rows get their results by the decode path, however long; one whose
+ * query_start_loc does not run from 0 to num_tokens (PKV_DEVERR_QSL) gets none.
+ *
  * q                fp16 [num_tokens][num_q_heads][head_dim]   device, 16-byte aligned
  * block_tables     int32 [num_seqs][max_blocks_per_seq]       device
  * context_lens     int32 [num_seqs]                           device
