@@ -550,6 +550,10 @@ __global__ void __launch_bounds__(256) dequant_prefill_rows_kernel(const Dequant
     const int ctx = __ldg(p.context_lens + b);
     const int q_len = __ldg(p.qsl + b + 1) - __ldg(p.qsl + b);
     const int j = row_blocks(ctx, q_len, p.win).row_unit(sb - sbase[b]);
+    if (j >= p.max_blocks) {  // (the row's metadata is not what was planned)
+      if (threadIdx.x == 0) dev::set_error(p.err, PKV_DEVERR_ROW_META);
+      continue;
+    }
     const int id = __ldg(p.block_tables + (int64_t)b * p.max_blocks + j);
     const bool ok = id >= 0 && id < p.num_blocks;
     if (threadIdx.x == 0) {

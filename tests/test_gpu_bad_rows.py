@@ -94,3 +94,24 @@ def test_no_list_of_rows(cuda, built, kv, window, fused, case):
     assert p.pool.check() & pkv.PKV_DEVERR_QSL and np.isnan(out).all()
     good = Pass(kv, [0, 1, 41], 41, window)
     assert np.isfinite(good.run()).all() and good.pool.check() == 0
+
+
+@pytest.mark.parametrize("window", [0, 33])
+@pytest.mark.parametrize("ctx", [5000, 2**31 - 1, 3, -7])
+def test_contexts_rewritten_after_the_plan(cuda, built, window, ctx):
+    """8-bit cache, a row of 16 and more new tokens: the pass was planned with other contexts than the call finds (which pkv.h asks
+    to plan again)."""
+    p = Pass(pkv.PKV_KV_E4M3, [0, 40, 41], 41, window)
+    planned, plan = p.ctx.clone(), pkv.pkv_attention_window_plan if window else pkv.pkv_attention_plan
+    ws, out = p.memory[GUARD:], p.out_memory[41:82]
+    plan(p.pool.handle, p.ctx, p.qsl, 2, 41, WIDTH, *((window, 2) if window else ()), ws, p.n)
+    p.ctx.fill_(ctx)
+    pkv.pkv_attention(p.pool.handle, 0, p.q, p.tables, WIDTH, p.ctx, p.qsl, 2, 41, out, ws, p.n)
+    torch.cuda.synchronize()
+    assert (p.memory[:GUARD] == 0xA5).all() and (p.memory[GUARD + p.n:] == 0xA5).all()
+    assert torch.isnan(p.out_memory[:41]).all() and torch.isnan(p.out_memory[82:]).all()
+    p.pool.check()
+    p.ctx.copy_(planned)
+    p.memory.fill_(0xA5)
+    p.out_memory.fill_(float("nan"))
+    assert np.isfinite(p.run()).all() and p.pool.check() == 0
