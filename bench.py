@@ -51,8 +51,8 @@ CONFIGS = {
 # DRAM bytes per pkv_attention call measured with ncu (dram__bytes_read.sum + dram__bytes_write.sum,
 # summed over the call's kernels) on the qwen_decode workload, keyed by the sha256 prefix of the kernel
 # source they were taken on and the cache format; reported as null once the source changes.
-TRAFFIC = {"afa604a1f3c5/fp16/qwen_decode": 142.20e6,   # profiles/decode_kernel_qwen_decode.md
-           "afa604a1f3c5/e4m3/qwen_decode": 71.44e6}    # profiles/decode_kernel_qwen_decode_e4m3.md
+TRAFFIC = {"b8c71d4a0e9f/fp16/qwen_decode": 142.12e6,   # profiles/decode_kernel_qwen_decode.md
+           "b8c71d4a0e9f/e4m3/qwen_decode": 71.45e6}    # profiles/decode_kernel_qwen_decode_e4m3.md
 
 FALLBACK_HBM_GBS = 6800.0
 
