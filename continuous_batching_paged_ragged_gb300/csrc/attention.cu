@@ -17,7 +17,8 @@
 //    blocks are dealt to the streaming warps, which stream K and V through their own TMA rings and run
 //    the G query heads' contraction on warp MMAs with an online softmax; the combiner warp folds the four
 //    warps' shares and finishes the token (fp16 output, or a split partial, or the merge of all of them).
-//    Its fp16-cache instances compile here, the 8-bit ones in decode_e4m3.cu.
+//    Its fp16-cache instances compile here, the 8-bit ones in decode_e4m3.cu, the 4-bit ones (with a block loop of
+//    their own, decode_int4.cuh) in decode_int4.cu.
 //  * Cross-split merge: a token whose context fits one split gets its fp16 output from the decode
 //    directly.  Otherwise each split leaves an unnormalised partial (m, l, o), and the CTA that finishes the
 //    token's last split merges them with log-sum-exp weights inside the same launch (a separate merge
@@ -26,7 +27,7 @@
 //    spreads one token's merge over many CTAs.
 //  * A windowed plan (pkv_attention_window_plan) counts and walks the blocks that a window and a few first tokens leave
 //    visible; its calls launch the kernels' windowed instances (decode_window*.cu, prefill_window.cu).
-//  * Prefill rows run on the tcgen05 tile kernel (prefill.cuh) ahead of the decode; on the 8-bit cache
+//  * Prefill rows run on the tcgen05 tile kernel (prefill.cuh) ahead of the decode; on the 8-bit and 4-bit caches
 //    their blocks are first dequantized into an fp16 shadow in the workspace (dequant_prefill_rows_kernel).
 #include <cuda_fp16.h>
 
@@ -39,6 +40,7 @@
 #include "attn_common.cuh"
 
 #include "decode.cuh"
+#include "int4.cuh"
 
 namespace pkv {
 
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 // ---------------------------------------------------------------------------------------------------
 struct WsLayout {
   size_t hdr, tok_row, tok_ctx, merge_cnt, tasks, items, items_slot, pf_sync, pf_ml, pf_o, part_ml, part_o, total;
-  // 8-bit cache with prefill rows: the rows' first shadow block, the shadow block tables and the fp16 shadow
+  // quantized cache with prefill rows: the rows' first shadow block, the shadow block tables and the fp16 shadow
   size_t pf_base = 0, shadow_bt = 0, shadow = 0;
   int64_t shadow_blocks = 0;
   bool shadow_by_id = false;  // the shadow mirrors the pool block for block (no shadow block tables)
@@ -408,7 +410,7 @@ static WsLayout ws_layout(const pkv_config& c, int num_seqs, int num_tokens, int
   }
   w.max_tasks = (int64_t)num_tokens * c.num_kv_heads * w.max_splits;
   const int group = c.num_q_heads / c.num_kv_heads;
-  // the tile kernel reads fp16 K/V: on an 8-bit cache it reads the prefill rows' blocks from an fp16 shadow
+  // the tile kernel reads fp16 K/V: on a quantized cache it reads the prefill rows' blocks from an fp16 shadow
   const bool prefill = prefill_supported(c.head_dim, group) && c.num_kv_heads < 256;
   w.prefill_min_qlen = prefill ? kPrefillMinQlen : 0;
   w.prefill_pos = prefill_item_positions(group, c.head_dim);
@@ -447,7 +449,7 @@ static WsLayout ws_layout(const pkv_config& c, int num_seqs, int num_tokens, int
   off += up256(parts * kHeadsTile * sizeof(float2));
   w.part_o = off;
   off += up256(parts * 32 * (c.head_dim / 4) * sizeof(float));
-  if (c.kv_dtype == PKV_KV_E4M3 && rows > 0) {
+  if (c.kv_dtype != PKV_KV_F16 && rows > 0) {
     // the prefill rows' tables name at most `rows` x max_blocks blocks, a block that several rows share once for each;
     // where the pool has fewer, the shadow is addressed by physical block instead, whoever shares it
     w.shadow_blocks = std::min<int64_t>((int64_t)c.num_blocks, rows * (int64_t)max_blocks);
@@ -496,7 +498,7 @@ static cudaError_t launch_plan(pkv_pool* pool, char* ws, const WsLayout& w, cons
 }
 
 // ---------------------------------------------------------------------------------------------------
-// 8-bit cache, prefill rows: the tile kernel reads fp16 tiles, so every block of a prefill row is first
+// 8-bit and 4-bit caches, prefill rows: the tile kernel reads fp16 tiles, so every block of a prefill row is first
 // dequantized (exactly) into an fp16 shadow in the workspace, and the row's shadow block table is written
 // alongside.  The plan numbered the prefill rows' blocks row after row (pf_base, monotone, with the total at
 // the end); a CTA takes these in turn, finds its row by binary search over pf_base staged in shared
@@ -508,9 +510,9 @@ static cudaError_t launch_plan(pkv_pool* pool, char* ws, const WsLayout& w, cons
 // masks keys past a context, and zeroes its last tile's values there).
 // ---------------------------------------------------------------------------------------------------
 struct DequantParams {
-  const unsigned char* codes_k;  // this layer's codes [num_blocks][Hkv][16][D]
+  const unsigned char* codes_k;  // this layer's codes [num_blocks][Hkv][16][D]; 4-bit: its records
   const unsigned char* codes_v;
-  const unsigned char* scales;   // this layer's scale records [num_blocks][Hkv][2][16]
+  const unsigned char* scales;   // this layer's scale records [num_blocks][Hkv][2][16] (4-bit: not used)
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* pf_base;        // [num_seqs + 1]
@@ -526,7 +528,7 @@ struct DequantParams {
 
 constexpr int kDequantMaxRows = 48 * 1024 - 1;  // pf_base staged in shared memory: (rows + 1) x 4 bytes <= 192 KB
 
-template <int D>
+template <int D, bool I4>
 __global__ void __launch_bounds__(256) dequant_prefill_rows_kernel(const DequantParams p) {
   extern __shared__ int32_t sbase[];  // [num_seqs + 1]
   dev::griddep_wait();
@@ -567,6 +569,16 @@ __global__ void __launch_bounds__(256) dequant_prefill_rows_kernel(const Dequant
       const bool live = ok && (by_id || j * kBS + r < ctx);
       const int64_t src = (ok ? (int64_t)id : 0) * p.num_kv_heads + h;
       const int64_t dst = ((to * p.num_kv_heads + h) * kBS + r) * CPR + c;
+      if constexpr (I4) {
+        using R = Int4Record<D>;
+        const unsigned char* rec = p.codes_k + src * R::BYTES;
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        p.shadow_k[dst] = live ? dev::int4x8_dequant(__ldg(reinterpret_cast<const uint32_t*>(rec + R::code_at(0, r, c))),
+                                                     __ldg(reinterpret_cast<const __half*>(rec + R::scale_at(0, r, c)))) : none;
+        p.shadow_v[dst] = live ? dev::int4x8_dequant(__ldg(reinterpret_cast<const uint32_t*>(rec + R::code_at(1, r, c))),
+                                                     __ldg(reinterpret_cast<const __half*>(rec + R::scale_at(1, r, c)))) : none;
+        continue;
+      }
       const unsigned char* rec = p.scales + src * 32;
       const uint2 zero = make_uint2(0, 0);
       const uint2 ck = live ? __ldg(reinterpret_cast<const uint2*>(p.codes_k + (src * kBS + r) * D) + c) : zero;
@@ -580,11 +592,12 @@ __global__ void __launch_bounds__(256) dequant_prefill_rows_kernel(const Dequant
 template <int D>
 static cudaError_t launch_dequant(pkv_pool* pool, const DequantParams& dq, cudaStream_t s) {
   const size_t smem = (size_t)(dq.num_seqs + 1) * 4;
+  auto* kernel = pool->cfg.kv_dtype == PKV_KV_INT4 ? dequant_prefill_rows_kernel<D, true> : dequant_prefill_rows_kernel<D, false>;
   if (smem > 48 * 1024) {
-    const cudaError_t e = prepare_kernel(pool, dequant_prefill_rows_kernel<D>, (kDequantMaxRows + 1) * 4);
+    const cudaError_t e = prepare_kernel(pool, kernel, (kDequantMaxRows + 1) * 4);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(dequant_prefill_rows_kernel<D>, dim3((unsigned)(pool->num_sms * 2)), dim3(256), smem, s, dq);
+  return launch_pdl(kernel, dim3((unsigned)(pool->num_sms * 2)), dim3(256), smem, s, dq);
 }
 
 // Inputs of an append fused into the decode launch (k == nullptr: not fused).
@@ -620,13 +633,14 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
   p.slots = fa.slots;
   p.cache_k = static_cast<__half*>(pkv_pool_layer_ptr(pool, layer, 0));
   p.cache_v = static_cast<__half*>(pkv_pool_layer_ptr(pool, layer, 1));
-  const bool f8 = c.kv_dtype == PKV_KV_E4M3;
+  const bool f8 = c.kv_dtype == PKV_KV_E4M3, i4 = c.kv_dtype == PKV_KV_INT4;
   p.scales = static_cast<unsigned char*>(pkv_pool_scales_ptr(pool, layer));
   p.num_slots = (int64_t)c.num_blocks * c.block_size;
   // TMA rows per (layer, K/V) pool: one per token (fp16) or per 128 code bytes (8-bit)
   const int64_t toks_per_pool = (int64_t)c.num_blocks * c.num_kv_heads * c.block_size;
   // (the 8-bit d 256 map addresses tokens, with the two halves of a key as its middle dimension)
-  const int rows_per_pool = (int)(f8 && c.head_dim != 256 ? toks_per_pool * c.head_dim / 128 : toks_per_pool);
+  // (4-bit: no map, its records are addressed by bytes)
+  const int rows_per_pool = (int)(i4 ? 0 : f8 && c.head_dim != 256 ? toks_per_pool * c.head_dim / 128 : toks_per_pool);
   p.layer_row0_k = (layer * 2) * rows_per_pool;
   p.layer_row0_v = (layer * 2 + 1) * rows_per_pool;
   p.max_blocks = max_blocks;
@@ -651,11 +665,11 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
     a.layer_row0_k = p.layer_row0_k;
     a.layer_row0_v = p.layer_row0_v;
     a.num_blocks = c.num_blocks;
-    if (f8) {  // the prefill rows' blocks, dequantized into the workspace's fp16 shadow (its map is prepared)
+    if (f8 || i4) {  // the prefill rows' blocks, dequantized into the workspace's fp16 shadow (its map is prepared)
       char* shadow = ws + w.shadow;
       const uint64_t srows = (uint64_t)2 * w.shadow_blocks * c.num_kv_heads * kBS;
       if (pool->shadow_base != shadow || pool->shadow_rows != srows)
-        return fail(PKV_ERR_INVALID_ARG, "8-bit cache: the shadow tensor map was not prepared for this workspace");
+        return fail(PKV_ERR_INVALID_ARG, "quantized cache: the shadow tensor map was not prepared for this workspace");
       DequantParams dq;
       dq.codes_k = static_cast<const unsigned char*>(pkv_pool_layer_ptr(pool, layer, 0));
       dq.codes_v = static_cast<const unsigned char*>(pkv_pool_layer_ptr(pool, layer, 1));
@@ -708,8 +722,11 @@ static pkv_status launch_attention(pkv_pool* pool, int layer, const void* q, con
     p.early = 1;  // the prefill kernel has waited for every append
   }
   if (windowed) {
-    e = f8 ? launch_decode_window_e4m3(c.head_dim, group, p, pool, w.max_tasks, s)
-           : launch_decode_window(c.head_dim, group, p, pool, w.max_tasks, s);
+    e = i4   ? launch_decode_window_int4(c.head_dim, group, p, pool, w.max_tasks, s)
+        : f8 ? launch_decode_window_e4m3(c.head_dim, group, p, pool, w.max_tasks, s)
+             : launch_decode_window(c.head_dim, group, p, pool, w.max_tasks, s);
+  } else if (i4) {
+    e = launch_decode_int4(c.head_dim, group, p, pool, w.max_tasks, s);
   } else if (f8) {
     e = launch_decode_e4m3(c.head_dim, group, p, pool, w.max_tasks, s);
   } else {
@@ -836,15 +853,15 @@ static pkv_status check_plan(const pkv_pool* pool, const void* workspace, const 
   return PKV_OK;
 }
 
-// Host-side refusals of the 8-bit cache's prefill path, made before anything is launched: the dequantizing
+// Host-side refusals of the quantized caches' prefill path, made before anything is launched: the dequantizing
 // kernel stages one int per row in shared memory, and the fp16 shadow's tensor map is encoded here (once per
 // workspace placement) so that a failed encode launches nothing either.
 static pkv_status prepare_prefill_shadow(pkv_pool* pool, char* ws, const WsLayout& w, int num_seqs, int num_tokens) {
   const pkv_config& c = pool->cfg;
-  if (c.kv_dtype != PKV_KV_E4M3 || w.prefill_min_qlen <= 0 || num_tokens - num_seqs < w.prefill_min_qlen - 1)
+  if (c.kv_dtype == PKV_KV_F16 || w.prefill_min_qlen <= 0 || num_tokens - num_seqs < w.prefill_min_qlen - 1)
     return PKV_OK;
   if (num_seqs > kDequantMaxRows)
-    return fail(PKV_ERR_UNSUPPORTED, "8-bit cache: prefill rows in a pass of more than 49151 rows");
+    return fail(PKV_ERR_UNSUPPORTED, "quantized cache: prefill rows in a pass of more than 49151 rows");
   char* shadow = ws + w.shadow;
   const uint64_t srows = (uint64_t)2 * w.shadow_blocks * c.num_kv_heads * kBS;
   if (pool->shadow_base != shadow || pool->shadow_rows != srows) {
@@ -981,10 +998,10 @@ extern "C" pkv_status pkv_attention_append(pkv_pool* pool, int32_t layer, const 
   st = prepare_prefill_shadow(pool, static_cast<char*>(workspace), w, num_seqs, num_tokens);
   if (st != PKV_OK) return st;
   int launches = 0;
-  // Prefill rows possible (they read the cache), or on an 8-bit cache a row with 16 or more new tokens
+  // Prefill rows possible (they read the cache), or on a quantized cache a row with 16 or more new tokens
   // (quantizing its rows once beats re-quantizing them in every tile that holds them): append first.
   const bool long_rows = num_tokens - num_seqs >= kPrefillMinQlen - 1;
-  if (w.max_items > 0 || (pool->cfg.kv_dtype == PKV_KV_E4M3 && long_rows)) {
+  if (w.max_items > 0 || (pool->cfg.kv_dtype != PKV_KV_F16 && long_rows)) {
     st = pkv_append(pool, layer, k, v, slot_mapping, num_tokens, stream);
     if (st != PKV_OK) return st;
     launches = pool->last_launches;

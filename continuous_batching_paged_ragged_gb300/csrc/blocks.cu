@@ -3,14 +3,16 @@
 // "Continuous Batching Is Not a Bigger Batch", section "The allocator is the other half": requests hold blocks and
 // a freed block becomes another request's.  What a block holds is spread over the pool: in each of the
 // 2 * num_layers planes [num_blocks][Hkv][16][d] (K and V of a layer) one contiguous piece of Hkv * 16 * d values,
-// and on an 8-bit cache in each of num_layers scale planes one piece of Hkv 32-byte records.  Nothing is
-// computed: the calls are bound by memory, every moved byte read once and written once.
+// and on an 8-bit cache in each of num_layers scale planes one piece of Hkv 32-byte records.  On a 4-bit cache it is Hkv
+// whole records in each of num_layers planes (int4.cuh).  Nothing is computed: the calls are bound by memory, every moved
+// byte read once and written once.
 #include <algorithm>
 #include <cstdlib>
 #include <cstring>
 #include <string>
 #include <vector>
 
+#include "int4.cuh"
 #include "pkv_internal.cuh"
 
 namespace pkv {
@@ -26,9 +28,9 @@ struct BlockGeo {
   unsigned char* scales;   // 8-bit: [num_layers][num_blocks][num_kv_heads][2][16] bytes, else null
   int64_t plane_bytes;     // of a value plane
   int64_t scale_bytes;     // of a scale plane
-  int planes;              // value planes: 2 * num_layers
+  int planes;              // value planes: 2 * num_layers (4-bit: num_layers, of records)
   int scale_planes;        // num_layers, or 0
-  int num_kv_heads, row_bytes, num_blocks;
+  int num_kv_heads, row_bytes, num_blocks;  // row_bytes: a sixteenth of a (block, head)'s piece
   int32_t* err;
 };
 
@@ -38,10 +40,11 @@ BlockGeo geo_of(const pkv_pool* pool) {
   BlockGeo g;
   g.values = pool->base;
   g.scales = f8 ? reinterpret_cast<unsigned char*>(pool->base + pool->scales_off) : nullptr;
-  g.row_bytes = c.head_dim * (f8 ? 1 : 2);
+  const bool i4 = c.kv_dtype == PKV_KV_INT4;
+  g.row_bytes = i4 ? int4_record_bytes(c.head_dim) / kBS : c.head_dim * (f8 ? 1 : 2);
   g.plane_bytes = (int64_t)c.num_blocks * c.num_kv_heads * kBS * g.row_bytes;
   g.scale_bytes = (int64_t)c.num_blocks * c.num_kv_heads * 32;
-  g.planes = 2 * c.num_layers;
+  g.planes = (i4 ? 1 : 2) * c.num_layers;
   g.scale_planes = f8 ? c.num_layers : 0;
   g.num_kv_heads = c.num_kv_heads;
   g.num_blocks = c.num_blocks;
@@ -98,6 +101,33 @@ __device__ void copy_rows(const BlockGeo& g, int src, int dst, int rows, int p0,
     if (rows & 4) *reinterpret_cast<uint32_t*>(to + (rows & 8)) = four;
     if (rows & 2) *reinterpret_cast<uint16_t*>(to + (rows & 12)) = (uint16_t)rest;
     if (rows & 1) to[rows & 14] = (unsigned char)(rest >> (rows & 2 ? 16 : 0));
+  }
+}
+
+// The same on a 4-bit cache: of every record the first `rows` of the 16 pieces of each group's codes, and the scales' first
+// `rows` rows (8 bytes or more each).  A warp takes a record at a time.
+__device__ void copy_rows_int4(const BlockGeo& g, int src, int dst, int rows, int p0, int p1) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int record = kBS * g.row_bytes, head_dim = record / 18;
+  const int chunks = head_dim;                    // 16-byte pieces of K's and V's codes: 2 * (head_dim / 32) * 16
+  const int words = rows * (head_dim / 64);       // 8-byte words of the scales
+  const int n = (p1 - p0) * g.num_kv_heads;
+  for (int i = warp; i < n; i += kThreads / 32) {
+    const int p = p0 + i / g.num_kv_heads, h = i % g.num_kv_heads;
+    const char* in = g.values + p * g.plane_bytes + ((int64_t)src * g.num_kv_heads + h) * record;
+    char* out = g.values + p * g.plane_bytes + ((int64_t)dst * g.num_kv_heads + h) * record;
+    constexpr int U = 4;  // loads in flight a lane
+    for (int c0 = lane; c0 < chunks; c0 += 32 * U) {
+      uint4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c0 + 32 * u < chunks && (c0 & 15) < rows) v[u] = __ldcs(reinterpret_cast<const uint4*>(in) + c0 + 32 * u);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c0 + 32 * u < chunks && (c0 & 15) < rows) __stcs(reinterpret_cast<uint4*>(out) + c0 + 32 * u, v[u]);
+    }
+    for (int c = lane; c < words; c += 32)
+      reinterpret_cast<uint2*>(out + 16 * head_dim)[c] = reinterpret_cast<const uint2*>(in + 16 * head_dim)[c];
   }
 }
 
@@ -254,6 +284,7 @@ __global__ void __launch_bounds__(kWorkers * 32) copy_blocks_kernel(const BlockG
   publish();
 }
 
+template <bool I4>
 __global__ void __launch_bounds__(kThreads, kForkCtas) fork_rows_kernel(const BlockGeo g, int32_t* tables, int max_blocks, int32_t* ctx,
                                                              int num_seqs, const int32_t* __restrict__ forks, int num_forks,
                                                              int slices) {
@@ -289,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, kForkCtas) fork_rows_kernel(const Bl
     if (tail > 0) {
       int p0, p1;
       slice_planes(g, s, slices, p0, p1);
-      copy_rows(g, last, block, tail, p0, p1);
+      if constexpr (I4) copy_rows_int4(g, last, block, tail, p0, p1); else copy_rows(g, last, block, tail, p0, p1);
     }
   }
   publish();
@@ -662,9 +693,9 @@ extern "C" pkv_status pkv_fork_rows(pkv_pool* pool, int32_t* block_tables, int32
   const int64_t ctas = (int64_t)pool->num_sms * kForkCtas;
   const int slices = slices_for(g, num_forks, ctas);
   const int64_t grid = std::min<int64_t>((int64_t)num_forks * slices, ctas);
-  const cudaError_t e = launch_pdl(fork_rows_kernel, dim3((unsigned)grid), dim3(kThreads), 0, (cudaStream_t)stream, g,
-                                   block_tables, (int)max_blocks_per_seq, context_lens, (int)num_seqs, forks, (int)num_forks,
-                                   slices);
+  const cudaError_t e = launch_pdl(pool->cfg.kv_dtype == PKV_KV_INT4 ? fork_rows_kernel<true> : fork_rows_kernel<false>,
+                                   dim3((unsigned)grid), dim3(kThreads), 0, (cudaStream_t)stream, g, block_tables,
+                                   (int)max_blocks_per_seq, context_lens, (int)num_seqs, forks, (int)num_forks, slices);
   if (e != cudaSuccess) return cuda_fail(e, "fork_rows launch");
   pool->last_launches = 1;
   return PKV_OK;

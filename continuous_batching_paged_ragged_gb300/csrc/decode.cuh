@@ -1,8 +1,8 @@
 // The persistent split-K decode kernel: per-pass tasks (one split of one (token, KV head)) taken by
 // persistent CTAs of four streaming warps, a combiner warp and a scheduler warp; the cache is streamed
 // through per-warp TMA rings and the group contraction runs on warp MMAs.  Templated on the head
-// dimension, the query heads per KV head and the cache format (fp16 values or 8-bit E4M3 codes with a
-// power-of-two scale per cached row), so each format's instances compile in their own translation unit.
+// dimension, the query heads per KV head and the cache format (fp16 values, 8-bit E4M3 codes with a
+// power-of-two scale per cached row, or 4-bit records), so each format's instances compile in their own translation unit.
 // How it fits the pass (plan, merge of long tokens, prefill, entry points) is described in attention.cu.
 #pragma once
 
@@ -12,6 +12,7 @@
 #include <cmath>
 
 #include "attn_common.cuh"
+#include "int4.cuh"
 
 namespace pkv {
 constexpr int kFusedMergeSplits = 32;  // tokens with up to this many splits are merged inside the decode
@@ -43,16 +44,20 @@ struct TaskEntry {
 // Cache formats of the decode kernel (template parameter KV).
 constexpr int kKvF16 = 0;   // fp16 values
 constexpr int kKvE4M3 = 1;  // E4M3 codes with one power-of-two scale per cached (token, KV head) row
+constexpr int kKvInt4 = 2;  // 4-bit codes with a scale for 32 values: K, V and scales of a (block, KV head) in one record
 
 template <int D, int G, int KV>
 struct DecodeTraits {
   static constexpr int NW = 4;                     // streaming warps; then the combiner and the scheduler
   static constexpr int NTHREADS = (NW + 2) * 32;
   static constexpr bool F8 = KV == kKvE4M3;
-  static constexpr int RUN = kBS * D * (F8 ? 1 : 2);  // one (block, KV head) run of K or V
+  static constexpr bool I4 = KV == kKvInt4;
+  // one (block, KV head) run of K or V; 4-bit: its whole record
+  static constexpr int RUN = I4 ? Int4Record<D>::BYTES : kBS * D * (F8 ? 1 : 2);
+  static constexpr int RPB = I4 ? 1 : 2;           // runs per block
   static constexpr int BOXROWS = kBS * D / 128;    // 8-bit: 128-byte rows of a run (its box height)
   static constexpr int SCL = F8 ? 32 : 0;          // 8-bit: scale record per slot (the K and V scales of a block)
-  static constexpr int RING = F8 ? 16 : PKV_DECODE_RING(D);  // 8-bit: as many slots as fit, up to 16
+  static constexpr int RING = F8 || I4 ? 16 : PKV_DECODE_RING(D);  // 8-bit, 4-bit: as many slots as fit, up to 16
   static constexpr int KS = D / 16;                // MMA k-steps over the head dimension (scores)
   static constexpr int MT = D / 16;                // MMA m-tiles over the head dimension (values)
   static constexpr int OV = MT * 4;                // fp32 output values per lane (8-head fragment)
@@ -85,7 +90,8 @@ struct DecodeTraits {
   // runs one CTA per SM with the whole register file.
   static constexpr int MINB = (F8 && D == 256 && G > 6) ? 1 : (FIT < 3 ? FIT : 3);
   static_assert(D % 64 == 0 && G >= 1 && G <= kHeadsTile, "shape");
-  static_assert(RUN % 1024 == 0, "swizzled boxes need 1024-byte aligned slots");
+  static_assert(I4 || RUN % 1024 == 0, "swizzled boxes need 1024-byte aligned slots");
+  static_assert(!I4 || (RUN % 128 == 0 && NR >= 2), "records are bulk-copy destinations; their blocks go in pairs");
   static_assert(KS % 2 == 0 && QB % 128 == 0, "k-steps in pairs; q buffers stay 16-byte aligned");
   static_assert(OFF_Q % 16 == 0 && OFF_BAR % 8 == 0 && OFF_STG % 16 == 0 && OFF_MML % 16 == 0, "alignment");
   static_assert(NR <= RING && SMEM <= NW * NR * SLOT + REST + 64, "shared-memory budget");
@@ -100,7 +106,7 @@ struct DecodeTraits {
 // hold four pairs; slower on the 5-slot fp16 rings at 128 (59.5 against 51.4 us for 12 / 2 heads) and for the 256-row
 // batch, so only there.  Unwindowed rows at head_dim 64 stay single: their results keep their bits.
 template <int D, int KV, bool W>
-constexpr bool kPairs = (KV == kKvE4M3 && D == 256) || (W && D == 64);
+constexpr bool kPairs = (KV == kKvE4M3 && D == 256) || (KV != kKvInt4 && W && D == 64);
 
 struct DecodeParams {
   CUtensorMap kv_map;  // fp16: the pool as whole runs; 8-bit: as rows of codes (64-byte aligned: first member)
@@ -120,7 +126,8 @@ struct DecodeParams {
   const __half* k_in;
   const __half* v_in;
   const int64_t* slots;
-  __half* cache_k;     // this layer's K pool [num_blocks][Hkv][16][D] (8-bit cache: E4M3 codes, one byte each)
+  __half* cache_k;     // this layer's K pool [num_blocks][Hkv][16][D] (8-bit cache: E4M3 codes, one byte each; 4-bit: its
+                       // records [num_blocks][Hkv])
   __half* cache_v;
   unsigned char* scales;  // 8-bit cache: this layer's scale records [num_blocks][Hkv][2 (K, V)][16]
   int64_t num_slots;
@@ -324,7 +331,7 @@ struct Streamer {
     const int nfull = from / kBS - skip - first;  // blocks first, first + NW, ... below from / 16
     v.nlean = (!kPairs<D, KV, W> || nfull <= 0) ? 0 : min(v.nbw, (nfull + T::NW - 1) / T::NW);
   }
-  static __device__ __forceinline__ int runs(const TaskView& v) { return v.t >= 0 ? 2 * v.nbw : 0; }
+  static __device__ __forceinline__ int runs(const TaskView& v) { return v.t >= 0 ? T::RPB * v.nbw : 0; }
   __device__ __forceinline__ int block_pos(const TaskView& v, int j) const {
     const int b = v.bw + T::NW * j;  // of the split
     const int gap = W && b >= (v.jump & 31) ? (int)((uint32_t)v.jump >> 5) : 0;
@@ -333,6 +340,11 @@ struct Streamer {
   // Run r of the warp's stream within a task: the lean blocks go in pairs, K of both then V of both; the rest
   // (an odd lean block, then the blocks holding the context's end or this pass's rows) one by one, K then V.
   static __device__ __forceinline__ void run_of(const TaskView& v, int r, int& j, int& isv) {
+    if constexpr (T::I4) {  // a run is a block
+      j = r;
+      isv = 0;
+      return;
+    }
     const int pr = 4 * (v.nlean >> 1);
     if (r < pr) {
       j = 2 * (r >> 2) + (r & 1);
@@ -351,7 +363,11 @@ struct Streamer {
     run_of(v, r, j, isv);
     r = isv;  // below, r & 1 tells V from K
     const int id = v.ids[v.bw + T::NW * j];
-    if constexpr (T::F8) {
+    if constexpr (T::I4) {
+      dev::mbar_arrive_expect_tx(&bars[slot], T::RUN);
+      dev::bulk_g2s(dst, reinterpret_cast<const char*>(p.cache_k) + ((size_t)id * p.num_kv_heads + v.g) * T::RUN, T::RUN,
+                    &bars[slot], pol);
+    } else if constexpr (T::F8) {
       // the codes as one box; a K run brings the block's 32-byte scale record (K and V scales) along
       dev::mbar_arrive_expect_tx(&bars[slot], T::RUN + ((r & 1) ? 0 : T::SCL));
       if constexpr (D == 256) {  // the keys' first, then their second 128 code bytes (rows are tokens), one copy
@@ -403,7 +419,22 @@ struct Streamer {
     ok = __all_sync(0xffffffffu, got) && ok;
     if (!ok) return;
     const uint32_t qs = dev::smem_addr(qbuf);
-    if constexpr (T::F8) {
+    if constexpr (T::I4) {
+      // The 4-bit K fragments: lane l's word of a 32-value group is values 8t .. 8t + 7 (t = l % 4), which unpack in
+      // pairs (i, i + 4); pairs 0 and 1 are MMA k indices 2t, 2t + 1 and 2t + 8, 2t + 9 of the group's first step, pairs 2
+      // and 3 of its second.  q takes the same order, which leaves every dot product as it is.
+#pragma unroll
+      for (int g = 0; g < D / 32; ++g) {
+        uint32_t x, y, z, u;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x), "=r"(y), "=r"(z), "=r"(u)
+                     : "r"(qs + ((lane >> 2) < G ? lane >> 2 : 0) * (D * 2) + (32 * g + 8 * (lane & 3)) * 2));
+        qb[2 * g][0] = __byte_perm(x, z, 0x5410);
+        qb[2 * g][1] = __byte_perm(x, z, 0x7632);
+        qb[2 * g + 1][0] = __byte_perm(y, u, 0x5410);
+        qb[2 * g + 1][1] = __byte_perm(y, u, 0x7632);
+      }
+    } else if constexpr (T::F8) {
       // The 8-bit K fragments hold dims 4t .. 4t + 3 of a 16-dim step as MMA k indices 2t, 2t + 1, 2t + 8,
       // 2t + 9 (the order ldmatrix delivers bytes in); q takes the same order, which leaves every dot
       // product as it is.
@@ -472,6 +503,15 @@ struct Streamer {
     ok = __all_sync(0xffffffffu, got) && ok;
     return dev::smem_addr(ring + slot * T::RUN);
   }
+  // The same for the run `ahead` places behind it, which must have been issued.
+  __device__ __forceinline__ uint32_t wait_run(int ahead) {
+    const int r = consumed + ahead;
+    const bool got = cta_wait(&bars[r % T::NR], (r / T::NR) & 1, sm.abort, p.err);
+    ok = __all_sync(0xffffffffu, got) && ok;
+    return run_addr(ahead);
+  }
+  // The slot of the run `ahead` places behind the oldest.
+  __device__ __forceinline__ uint32_t run_addr(int ahead) const { return dev::smem_addr(ring + (consumed + ahead) % T::NR * T::RUN); }
   // Half-way through the current task (half of this warp's runs consumed; at once for a warp with none): the
   // scheduler warp claims the CTA's next task once every streaming warp is there (see Scheduler).
   __device__ __forceinline__ void task_start() {
@@ -520,6 +560,11 @@ struct Streamer {
     cur_q_done = cur.nbw == 0;  // a task with no blocks for this warp needs no q
   }
 };
+
+// The 4-bit cache's loop over the same tasks (decode_int4.cuh).
+template <int D, int G, bool W>
+__device__ __forceinline__ void stream_loop_int4(const DecodeParams& p, const DecodeSmem<D, G, kKvInt4>& sm,
+                                                 Streamer<D, G, kKvInt4, W>& w);
 
 template <int D, int G, int KV, bool W>
 __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeSmem<D, G, KV>& sm, Streamer<D, G, KV, W>& w) {
@@ -1018,11 +1063,13 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
 // Output element held by register r of `lane` in the O^T fragment layout: its dim and its head.  fp16
 // cache: m-tile mt = r / 4 covers dims 16 mt .. 16 mt + 15, the lane's rows at g = lane / 4 and g + 8.
 // 8-bit cache: m-tiles 2i and 2i + 1 cover dims 32 i .. 32 i + 31, the even dims in the first and the odd
-// ones in the second; the lane's rows are dims 32 i + 2g (+ 16) and the next odd one.
+// ones in the second; the lane's rows are dims 32 i + 2g (+ 16) and the next odd one.  4-bit cache: m-tiles 2i and
+// 2i + 1 cover dims 32 i .. 32 i + 31 too, dims 4g and 4g + 1 of them in the first, 4g + 2 and 4g + 3 in the second.
 template <int KV>
 __device__ __forceinline__ void frag_coord(int lane, int r, int& dim, int& head) {
   const int mt = r >> 2, g = lane >> 2;
-  if constexpr (KV == kKvE4M3) dim = 32 * (mt >> 1) + ((r & 2) ? 16 : 0) + 2 * g + (mt & 1);
+  if constexpr (KV == kKvInt4) dim = 32 * (mt >> 1) + 4 * g + 2 * (mt & 1) + ((r >> 1) & 1);
+  else if constexpr (KV == kKvE4M3) dim = 32 * (mt >> 1) + ((r & 2) ? 16 : 0) + 2 * g + (mt & 1);
   else dim = 16 * mt + g + ((r & 2) ? 8 : 0);
   head = ((lane & 3) << 1) + (r & 1);
 }
@@ -1151,7 +1198,7 @@ struct Scheduler {
       if (lane < min(e->nb, T::NW * ((T::NR + 1) / 2))) {
         const size_t at = ((size_t)e->ids[lane] * p.num_kv_heads + (e->rec.y & 0xFF)) * T::RUN;
         dev::bulk_prefetch_l2(reinterpret_cast<const char*>(p.cache_k) + at, T::RUN);
-        dev::bulk_prefetch_l2(reinterpret_cast<const char*>(p.cache_v) + at, T::RUN);
+        if constexpr (!T::I4) dev::bulk_prefetch_l2(reinterpret_cast<const char*>(p.cache_v) + at, T::RUN);
       }
     }
   }
@@ -1568,7 +1615,9 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   __syncwarp();
   const bool poisoned = __syncthreads_or(pz);
   if (warp < T::NW) {
-    if (!poisoned) stream_loop<D, G, KV, W>(p, sm, w);
+    if (!poisoned) {
+      if constexpr (T::I4) stream_loop_int4<D, G, W>(p, sm, w); else stream_loop<D, G, KV, W>(p, sm, w);
+    }
     w.drain();
   } else if (!poisoned) {
     if (warp == T::NW) Combiner<D, G, KV, W>(p, sm, lane).run();
@@ -1621,6 +1670,11 @@ cudaError_t launch_decode_e4m3(int head_dim, int group, const DecodeParams& p, p
 cudaError_t launch_decode_window(int head_dim, int group, const DecodeParams& p, pkv_pool* pool, int64_t max_tasks,
                                  cudaStream_t stream);
 cudaError_t launch_decode_window_e4m3(int head_dim, int group, const DecodeParams& p, pkv_pool* pool, int64_t max_tasks,
+                                      cudaStream_t stream);
+// The 4-bit cache's (decode_int4.cu, decode_window_int4.cu).
+cudaError_t launch_decode_int4(int head_dim, int group, const DecodeParams& p, pkv_pool* pool, int64_t max_tasks,
+                               cudaStream_t stream);
+cudaError_t launch_decode_window_int4(int head_dim, int group, const DecodeParams& p, pkv_pool* pool, int64_t max_tasks,
                                       cudaStream_t stream);
 
 }  // namespace pkv

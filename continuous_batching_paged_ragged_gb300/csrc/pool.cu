@@ -4,7 +4,8 @@
 // the other half"): every computed token's key and value are kept, one pair per token per layer, in the
 // slot of a 16-token block that was allocated as the token was computed.  For an fp16 cache it is a pure
 // bit copy.  For the 8-bit cache (same page, "Checking it on a real system": quantize the cache when it is
-// the limit) each (token, KV head) row is stored as E4M3 codes with one power-of-two scale.
+// the limit) each (token, KV head) row is stored as E4M3 codes with one power-of-two scale; for the 4-bit cache as 4-bit
+// codes with a scale for every 32 values (int4.cuh).  pkv_gather reads rows of any cache back as fp16 values.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -13,6 +14,7 @@
 #include <string>
 #include <vector>
 
+#include "int4.cuh"
 #include "pkv_internal.cuh"
 
 namespace pkv {
@@ -44,8 +46,8 @@ static pkv_status check_config(const pkv_config* c) {
   if (!supported_group(c->num_q_heads / c->num_kv_heads))
     return fail(PKV_ERR_UNSUPPORTED, "query heads per KV head must be 1, 2, 4, 6 or 8");
   if (c->split_blocks < 0) return fail(PKV_ERR_INVALID_ARG, "split_blocks must be >= 0");
-  if (c->kv_dtype != PKV_KV_F16 && c->kv_dtype != PKV_KV_E4M3)
-    return fail(PKV_ERR_UNSUPPORTED, "kv_dtype must be PKV_KV_F16 or PKV_KV_E4M3");
+  if (c->kv_dtype != PKV_KV_F16 && c->kv_dtype != PKV_KV_E4M3 && c->kv_dtype != PKV_KV_INT4)
+    return fail(PKV_ERR_UNSUPPORTED, "kv_dtype must be PKV_KV_F16, PKV_KV_E4M3 or PKV_KV_INT4");
   return PKV_OK;
 }
 
@@ -104,6 +106,7 @@ pkv_status encode_f16_runs(CUtensorMap* map, void* base, uint64_t rows, int head
 
 static pkv_status encode_kv_map(pkv_pool* p) {
   const pkv_config& c = p->cfg;
+  if (c.kv_dtype == PKV_KV_INT4) return PKV_OK;  // its records are plain bulk copies
   const uint64_t toks = (uint64_t)c.num_layers * 2 * c.num_blocks * c.num_kv_heads * c.block_size;
   if (c.kv_dtype != PKV_KV_E4M3) {
     const pkv_status st = encode_f16_rows(&p->kv_map, p->base, toks, c.head_dim);
@@ -140,15 +143,19 @@ static pkv_status encode_kv_map(pkv_pool* p) {
   return PKV_OK;
 }
 
-// Bytes of the K/V values (fp16) or codes (8-bit) of every layer.
+// Bytes of the K/V values (fp16), codes (8-bit) or records (4-bit) of every layer.
 static size_t values_bytes_of(const pkv_config* c) {
+  if (c->kv_dtype == PKV_KV_INT4)
+    return (size_t)c->num_layers * (size_t)c->num_blocks * c->num_kv_heads * int4_record_bytes(c->head_dim);
   return (size_t)2 * c->num_layers * (size_t)c->num_blocks * c->num_kv_heads * c->block_size * c->head_dim *
          (c->kv_dtype == PKV_KV_E4M3 ? 1 : sizeof(__half));
 }
 // Everything before the status area: values, then (8-bit) one scale byte per cached row, padded to 256.
 static size_t cache_bytes_of(const pkv_config* c) {
-  if (c->kv_dtype != PKV_KV_E4M3) return values_bytes_of(c);
-  const size_t scales = (size_t)2 * c->num_layers * (size_t)c->num_blocks * c->num_kv_heads * c->block_size;
+  if (c->kv_dtype == PKV_KV_F16) return values_bytes_of(c);
+  const size_t scales = c->kv_dtype == PKV_KV_INT4
+                            ? 0  // (they are in the records)
+                            : (size_t)2 * c->num_layers * (size_t)c->num_blocks * c->num_kv_heads * c->block_size;
   return (values_bytes_of(c) + scales + 255) / 256 * 256;
 }
 
@@ -307,14 +314,18 @@ extern "C" void pkv_pool_destroy(pkv_pool* pool) { delete pool; }
 extern "C" void* pkv_pool_layer_ptr(const pkv_pool* pool, int32_t layer, int32_t kv) {
   if (!pool || layer < 0 || layer >= pool->cfg.num_layers || (kv != 0 && kv != 1)) return nullptr;
   const pkv_config& c = pool->cfg;
+  if (c.kv_dtype == PKV_KV_INT4)  // the layer's records; V's codes are 8 head_dim bytes into each
+    return pool->base + (size_t)layer * c.num_blocks * c.num_kv_heads * int4_record_bytes(c.head_dim) + (size_t)kv * 8 * c.head_dim;
   size_t per = (size_t)c.num_blocks * c.num_kv_heads * c.block_size * c.head_dim *
                (c.kv_dtype == PKV_KV_E4M3 ? 1 : sizeof(__half));
   return pool->base + ((size_t)layer * 2 + kv) * per;
 }
 
 extern "C" void* pkv_pool_scales_ptr(const pkv_pool* pool, int32_t layer) {
-  if (!pool || pool->cfg.kv_dtype != PKV_KV_E4M3 || layer < 0 || layer >= pool->cfg.num_layers) return nullptr;
+  if (!pool || pool->cfg.kv_dtype == PKV_KV_F16 || layer < 0 || layer >= pool->cfg.num_layers) return nullptr;
   const pkv_config& c = pool->cfg;
+  if (c.kv_dtype == PKV_KV_INT4)  // of the first record: the scales are 16 head_dim bytes into each
+    return static_cast<char*>(pkv_pool_layer_ptr(pool, layer, 0)) + (size_t)16 * c.head_dim;
   return pool->base + pool->scales_off + (size_t)layer * c.num_blocks * c.num_kv_heads * 2 * c.block_size;
 }
 
@@ -447,6 +458,119 @@ __global__ void __launch_bounds__(256) kv_append_e4m3_kernel(const uint4* __rest
   }
 }
 
+// 4-bit cache: the same units; a scale's 32 values are four consecutive lanes'.
+template <int D>
+__global__ void __launch_bounds__(256) kv_append_int4_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
+                                                             const int64_t* __restrict__ slot_mapping, int num_tokens,
+                                                             unsigned char* __restrict__ records, int num_kv_heads,
+                                                             int64_t num_slots, int32_t* err) {
+  using R = Int4Record<D>;
+  constexpr int CPH = D / 8;
+  dev::griddep_wait();
+  dev::griddep_launch_dependents();
+  const int64_t per_token = (int64_t)num_kv_heads * CPH;
+  const int64_t total = (int64_t)num_tokens * per_token;
+  const int lane = threadIdx.x & 31;
+  const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  for (int64_t base = ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * 32; base < total;
+       base += nwarps * 32) {
+    const int64_t i = base + lane;
+    const bool in = i < total;
+    const int64_t t = in ? i / per_token : 0;
+    const int64_t rem = i - t * per_token;
+    const int64_t h = rem / CPH;
+    const int c = (int)(rem % CPH);
+    const int64_t slot = in ? __ldg(slot_mapping + t) : -1;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint4 rk = in ? __ldg(k + i) : zero, rv = in ? __ldg(v + i) : zero;
+    const __half sk = dev::int4_scale(dev::int4_group_amax(rk)), sv = dev::int4_scale(dev::int4_group_amax(rv));
+    if (!in || slot == -1) continue;
+    if (slot < 0 || slot >= num_slots) {
+      if (c == 0 && h == 0) dev::set_error(err, PKV_DEVERR_SLOT_RANGE);
+      continue;
+    }
+    unsigned char* rec = records + ((slot >> 4) * num_kv_heads + h) * R::BYTES;
+    const int r = (int)(slot & 15);
+    *reinterpret_cast<uint32_t*>(rec + R::code_at(0, r, c)) = dev::int4_encode8(rk, sk);
+    *reinterpret_cast<uint32_t*>(rec + R::code_at(1, r, c)) = dev::int4_encode8(rv, sv);
+    if ((c & 3) == 0) {
+      *reinterpret_cast<__half*>(rec + R::scale_at(0, r, c)) = sk;
+      *reinterpret_cast<__half*>(rec + R::scale_at(1, r, c)) = sv;
+    }
+  }
+}
+
+// Rows of the cache as fp16 values: one thread per 16-byte chunk (8 values) of a slot's row of one KV head, K and V.
+// Bound by memory, every byte read and written once.
+template <int D, int KV>
+__global__ void __launch_bounds__(256) gather_kernel(const unsigned char* __restrict__ cache_k,
+                                                     const unsigned char* __restrict__ cache_v,
+                                                     const unsigned char* __restrict__ scales,
+                                                     const int64_t* __restrict__ slot_mapping, int num_tokens,
+                                                     int num_kv_heads, int64_t num_slots, uint4* __restrict__ k_out,
+                                                     uint4* __restrict__ v_out, int32_t* err) {
+  constexpr int CPH = D / 8;
+  dev::griddep_wait();
+  dev::griddep_launch_dependents();
+  const int64_t per_token = (int64_t)num_kv_heads * CPH;
+  const int64_t total = (int64_t)num_tokens * per_token;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t t = i / per_token, rem = i - t * per_token, h = rem / CPH;
+    const int c = (int)(rem % CPH);
+    const int64_t slot = __ldg(slot_mapping + t);
+    if (slot == -1) continue;
+    if (slot < 0 || slot >= num_slots) {
+      if (c == 0 && h == 0) dev::set_error(err, PKV_DEVERR_SLOT_RANGE);
+      continue;
+    }
+    const int64_t head = (slot >> 4) * num_kv_heads + h;  // of the pool's (block, KV head) pairs
+    const int r = (int)(slot & 15);
+    if constexpr (KV == PKV_KV_INT4) {
+      using R = Int4Record<D>;
+      const unsigned char* rec = cache_k + head * R::BYTES;
+      const uint32_t ck = __ldg(reinterpret_cast<const uint32_t*>(rec + R::code_at(0, r, c)));
+      const uint32_t cv = __ldg(reinterpret_cast<const uint32_t*>(rec + R::code_at(1, r, c)));
+      const __half sk = __ldg(reinterpret_cast<const __half*>(rec + R::scale_at(0, r, c)));
+      const __half sv = __ldg(reinterpret_cast<const __half*>(rec + R::scale_at(1, r, c)));
+      k_out[i] = dev::int4x8_dequant(ck, sk);
+      v_out[i] = dev::int4x8_dequant(cv, sv);
+    } else if constexpr (KV == PKV_KV_E4M3) {
+      const int64_t at = (head * 16 + r) * CPH + c;
+      const uint2 ck = __ldg(reinterpret_cast<const uint2*>(cache_k) + at), cv = __ldg(reinterpret_cast<const uint2*>(cache_v) + at);
+      const uint32_t sk = __ldg(scales + head * 32 + r), sv = __ldg(scales + head * 32 + 16 + r);
+      k_out[i] = dev::e4m3x8_dequant(ck, sk);
+      v_out[i] = dev::e4m3x8_dequant(cv, sv);
+    } else {
+      const int64_t at = (head * 16 + r) * CPH + c;
+      const uint4 xk = __ldg(reinterpret_cast<const uint4*>(cache_k) + at), xv = __ldg(reinterpret_cast<const uint4*>(cache_v) + at);
+      k_out[i] = xk;
+      v_out[i] = xv;
+    }
+  }
+}
+
+template <int D>
+static cudaError_t launch_gather(const pkv_pool* pool, int layer, const int64_t* slots, int num_tokens, uint4* k_out, uint4* v_out,
+                                 unsigned blocks, cudaStream_t s) {
+  const pkv_config& c = pool->cfg;
+  auto* kernel = c.kv_dtype == PKV_KV_INT4   ? gather_kernel<D, PKV_KV_INT4>
+                 : c.kv_dtype == PKV_KV_E4M3 ? gather_kernel<D, PKV_KV_E4M3>
+                                             : gather_kernel<D, PKV_KV_F16>;
+  return launch_pdl(kernel, dim3(blocks), dim3(256), 0, s, static_cast<const unsigned char*>(pkv_pool_layer_ptr(pool, layer, 0)),
+                    static_cast<const unsigned char*>(pkv_pool_layer_ptr(pool, layer, 1)),
+                    static_cast<const unsigned char*>(pkv_pool_scales_ptr(pool, layer)), slots, num_tokens, (int)c.num_kv_heads,
+                    (int64_t)c.num_blocks * c.block_size, k_out, v_out, pool->dev_error);
+}
+
+template <int D>
+static cudaError_t launch_append_int4(const pkv_pool* pool, int layer, const void* k, const void* v, const int64_t* slots,
+                                      int num_tokens, unsigned blocks, cudaStream_t s) {
+  const pkv_config& c = pool->cfg;
+  return launch_pdl(kv_append_int4_kernel<D>, dim3(blocks), dim3(256), 0, s, static_cast<const uint4*>(k), static_cast<const uint4*>(v),
+                    slots, num_tokens, static_cast<unsigned char*>(pkv_pool_layer_ptr(pool, layer, 0)), (int)c.num_kv_heads,
+                    (int64_t)c.num_blocks * c.block_size, pool->dev_error);
+}
+
 __global__ void __launch_bounds__(256) slot_mapping_kernel(const int32_t* __restrict__ block_tables, int max_blocks,
                                                            const int32_t* __restrict__ context_lens,
                                                            const int32_t* __restrict__ qsl, int num_seqs,
@@ -494,6 +618,16 @@ extern "C" pkv_status pkv_append(pkv_pool* pool, int32_t layer, const void* k, c
   int64_t blocks = (total + threads - 1) / threads;
   const int64_t cap = (int64_t)pool->num_sms * 8;
   if (blocks > cap) blocks = cap;
+  if (c.kv_dtype == PKV_KV_INT4) {
+    const cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e = c.head_dim == 64    ? launch_append_int4<64>(pool, layer, k, v, slot_mapping, num_tokens, (unsigned)blocks, s)
+                          : c.head_dim == 128 ? launch_append_int4<128>(pool, layer, k, v, slot_mapping, num_tokens, (unsigned)blocks, s)
+                                              : launch_append_int4<256>(pool, layer, k, v, slot_mapping, num_tokens, (unsigned)blocks, s);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
+    note_append(pool, layer);
+    pool->last_launches = 1;
+    return PKV_OK;
+  }
   if (c.kv_dtype == PKV_KV_E4M3) {
     const uint4* k4 = static_cast<const uint4*>(k);
     const uint4* v4 = static_cast<const uint4*>(v);
@@ -525,6 +659,35 @@ extern "C" pkv_status pkv_append(pkv_pool* pool, int32_t layer, const void* k, c
                              (int64_t)c.num_blocks * c.block_size, pool->dev_error);
   if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
   note_append(pool, layer);
+  pool->last_launches = 1;
+  return PKV_OK;
+}
+
+extern "C" pkv_status pkv_gather(pkv_pool* pool, int32_t layer, const int64_t* slot_mapping, int32_t num_tokens, void* k_out,
+                                 void* v_out, void* stream) {
+  clear_error();
+  if (!pool) return fail(PKV_ERR_INVALID_ARG, "pool is NULL");
+  pool->last_launches = 0;
+  if (layer < 0 || layer >= pool->cfg.num_layers) return fail(PKV_ERR_OUT_OF_RANGE, "layer out of range");
+  if (num_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "num_tokens must be >= 0");
+  if (num_tokens == 0) return PKV_OK;
+  if (!slot_mapping || !k_out || !v_out) return fail(PKV_ERR_INVALID_ARG, "slot_mapping, k_out and v_out must be non-NULL");
+  if ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) % 16 != 0)
+    return fail(PKV_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+  if (k_out == v_out) return fail(PKV_ERR_INVALID_ARG, "k_out and v_out must be apart");
+  pkv_status st = check_device(pool);
+  if (st == PKV_OK) st = validate_metadata(pool, nullptr, 0, nullptr, nullptr, 0, num_tokens, slot_mapping, stream);
+  if (st != PKV_OK) return st;
+  const pkv_config& c = pool->cfg;
+  const int64_t total = (int64_t)num_tokens * c.num_kv_heads * (c.head_dim / 8);
+  const unsigned blocks = (unsigned)std::min<int64_t>((total + 255) / 256, (int64_t)pool->num_sms * 8);
+  uint4* ko = static_cast<uint4*>(k_out);
+  uint4* vo = static_cast<uint4*>(v_out);
+  const cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = c.head_dim == 64    ? launch_gather<64>(pool, layer, slot_mapping, num_tokens, ko, vo, blocks, s)
+                        : c.head_dim == 128 ? launch_gather<128>(pool, layer, slot_mapping, num_tokens, ko, vo, blocks, s)
+                                            : launch_gather<256>(pool, layer, slot_mapping, num_tokens, ko, vo, blocks, s);
+  if (e != cudaSuccess) return cuda_fail(e, "gather launch");
   pool->last_launches = 1;
   return PKV_OK;
 }

@@ -1,4 +1,4 @@
-// Rotary positions, fused with the append.
+// Rotary positions, fused with the append; the same with a norm of every query and key head in front.
 //
 // Pair i of a head turns by position * f_i: a' = a cos - b sin, b' = b cos + a sin.  The pages have no
 // counterpart; the keys land in their slots as kv_append stores them ("Continuous Batching Is Not a Bigger Batch",
@@ -10,6 +10,9 @@
 // from a 64-bit float: 53 bits, off by less than 2^-53 of a turn for frequencies up to 1.
 // No 64-bit floating point on the device.
 //
+// Norms: y = x / sqrt(mean(x^2) + eps) * (offset + w) over a head's head_dim values, all in fp32: the mean square, the
+// product and the rotation behind it, with one rounding to fp16 at the end.
+//
 // Bound by memory: q, k and v read once, q_out and the slots written once.
 #include <cuda_fp16.h>
 
@@ -18,6 +21,7 @@
 #include <new>
 #include <string>
 
+#include "int4.cuh"
 #include "pkv_internal.cuh"
 
 constexpr int kMaxPairs = 128;
@@ -53,12 +57,35 @@ struct RopeParams {
   int rot_dim;
   float out_scale;
   int32_t* err;
+  // Norms: a head's weights, [head_dim]; null: its heads are not normalised.
+  const __half* q_weight;
+  const __half* k_weight;
+  float eps, weight_offset;
 };
 
 constexpr int kThreads = 128;
 constexpr int kMaxTokens = 4;  // per CTA
 
 __device__ __forceinline__ uint4 ld16(const __half* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+
+__device__ __forceinline__ void to_floats(const uint4& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+    x[2 * j] = f.x;
+    x[2 * j + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint4 to_halves(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 // One rotated pair of fp16 vectors of 8 values: pair j is (a_j, b_j).
 __device__ __forceinline__ void rotate8(uint4& a, uint4& b, const float (&c)[8], const float (&s)[8]) {
@@ -90,10 +117,15 @@ __device__ __forceinline__ void rotate8_interleaved(uint4& a, uint4& b, const fl
 // for every few heads, 8192 tokens took 15 to 21 us).  The unit of the rest is an item: 16 values of a q or KV head (two
 // 16-byte chunks that hold 8 whole pairs, or 16 values past the rotated part; of a KV head the key's and the value's).
 // A thread loads its first items before it computes its angles, so that neither waits for the other.
-template <int D, bool F8, bool INTER>
+// With norms (NORM) a head's mean square is a sum over its items' lanes, and a thread, whose items are all the same piece
+// of some head, holds its piece of both weights from the start.  On a 4-bit cache a scale's 32 values are four 8-value
+// chunks of up to four items: the chunks' largest magnitudes meet in shared memory.
+template <int D, int KV, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams p, const __grid_constant__ RopeTurns turns) {
   constexpr int PC = D / 16;  // items per head: a power of two within a warp
   constexpr int U = 2;        // items in flight a thread
+  static_assert(kThreads % PC == 0 && 32 % PC == 0, "a thread's items are one piece of different heads");
+  __shared__ uint4 chunk_amax[KV == PKV_KV_INT4 ? kThreads / 2 : 1];  // [thread's head][chunk] largest magnitude
   // (cos, sin) of pairs 2j and 2j + 1 of a token's rotated 16-value piece pc at [token][j][pc]: consecutive lanes read
   // consecutive 16 bytes
   __shared__ float4 angle[kMaxTokens][4][PC];
@@ -104,6 +136,20 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
   const uint32_t per = heads * PC, items = n * per;
   dev::griddep_wait();
   dev::griddep_launch_dependents();
+  uint4 wqa, wqb, wka, wkb;
+  if constexpr (NORM) {
+    const int pc = threadIdx.x % PC;
+    const int c0 = !INTER && pc < pieces ? pc : 2 * pc, c1 = !INTER && pc < pieces ? pc + half / 8 : 2 * pc + 1;
+    wqa = wqb = wka = wkb = make_uint4(0, 0, 0, 0);
+    if (p.q_weight) {
+      wqa = ld16(p.q_weight + 8 * c0);
+      wqb = ld16(p.q_weight + 8 * c1);
+    }
+    if (p.k_weight) {
+      wka = ld16(p.k_weight + 8 * c0);
+      wkb = ld16(p.k_weight + 8 * c1);
+    }
+  }
   for (uint32_t i0 = 0; i0 < items; i0 += U * kThreads) {  // the same number of rounds in every thread
     uint4 a[U], b[U], va[U], vb[U];
     int64_t slot[U];
@@ -150,8 +196,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
       const int c0 = !INTER && rot ? pc : 2 * pc, c1 = !INTER && rot ? pc + half / 8 : 2 * pc + 1;
       const bool kv = in && g >= 0 && slot[u] >= 0 && slot[u] < p.num_slots;
       if (in && g == 0 && pc == 0 && slot[u] != -1 && !kv) dev::set_error(p.err, PKV_DEVERR_SLOT_RANGE);
+      float cs[8], sn[8];
       if (in && rot) {
-        float cs[8], sn[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float4 x = angle[tb][j][pc];
@@ -160,6 +206,40 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
           cs[2 * j + 1] = x.z;
           sn[2 * j + 1] = x.w;
         }
+      }
+      if constexpr (NORM) {
+        float xa[8], xb[8], sum = 0.f;
+        to_floats(a[u], xa);
+        to_floats(b[u], xb);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], sum));
+#pragma unroll
+        for (int o = 1; o < PC; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);  // every lane of the warp is here
+        if (g < 0 ? p.q_weight != nullptr : p.k_weight != nullptr) {
+          const float r = 1.f / sqrtf(sum * (1.f / D) + p.eps);
+          float wa[8], wb[8];
+          to_floats(g < 0 ? wqa : wka, wa);
+          to_floats(g < 0 ? wqb : wkb, wb);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            xa[j] *= r * (p.weight_offset + wa[j]);
+            xb[j] *= r * (p.weight_offset + wb[j]);
+          }
+        }
+        if (rot) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            // pair j: (a_j, b_j), or side by side
+            float& x = INTER ? (j < 4 ? xa[2 * j] : xb[2 * j - 8]) : xa[j];
+            float& y = INTER ? (j < 4 ? xa[2 * j + 1] : xb[2 * j - 7]) : xb[j];
+            const float x0 = x, y0 = y;
+            x = x0 * cs[j] - y0 * sn[j];
+            y = y0 * cs[j] + x0 * sn[j];
+          }
+        }
+        a[u] = to_halves(xa);
+        b[u] = to_halves(xb);
+      } else if (in && rot) {
         if constexpr (INTER) rotate8_interleaved(a[u], b[u], cs, sn); else rotate8(a[u], b[u], cs, sn);
       }
       if (in && g < 0) {
@@ -168,7 +248,30 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
         dst[c1] = b[u];
       }
       const int64_t row = kv ? ((slot[u] >> 4) * p.num_kv_heads + g) * 16 + (slot[u] & 15) : 0;
-      if constexpr (F8) {
+      if constexpr (KV == PKV_KV_INT4) {
+        uint32_t* amax = reinterpret_cast<uint32_t*>(chunk_amax) + 2 * (threadIdx.x - pc);  // this head's chunks
+        amax[c0] = dev::f16x8_amax_bits(a[u]);
+        amax[c1] = dev::f16x8_amax_bits(b[u]);
+        const uint32_t av = dev::row_amax_bits<2>(max(dev::f16x8_amax_bits(va[u]), dev::f16x8_amax_bits(vb[u])));
+        __syncwarp();
+        const uint4 m0 = reinterpret_cast<const uint4*>(amax)[c0 >> 2], m1 = reinterpret_cast<const uint4*>(amax)[c1 >> 2];
+        __syncwarp();  // read before the next item's go over them
+        if (kv) {
+          using R = Int4Record<D>;
+          const __half s0 = dev::int4_scale(max(max(m0.x, m0.y), max(m0.z, m0.w)));
+          const __half s1 = dev::int4_scale(max(max(m1.x, m1.y), max(m1.z, m1.w)));
+          const __half sv = dev::int4_scale(av);
+          unsigned char* rec = p.cache_k + ((slot[u] >> 4) * p.num_kv_heads + g) * R::BYTES;
+          const int r = (int)(slot[u] & 15);
+          *reinterpret_cast<uint32_t*>(rec + R::code_at(0, r, c0)) = dev::int4_encode8(a[u], s0);
+          *reinterpret_cast<uint32_t*>(rec + R::code_at(0, r, c1)) = dev::int4_encode8(b[u], s1);
+          *reinterpret_cast<uint2*>(rec + R::code_at(1, r, 2 * pc)) =
+              make_uint2(dev::int4_encode8(va[u], sv), dev::int4_encode8(vb[u], sv));
+          if ((c0 & 3) == 0) *reinterpret_cast<__half*>(rec + R::scale_at(0, r, c0)) = s0;
+          if ((c1 & 3) == 0) *reinterpret_cast<__half*>(rec + R::scale_at(0, r, c1)) = s1;
+          if ((pc & 1) == 0) *reinterpret_cast<__half*>(rec + R::scale_at(1, r, 2 * pc)) = sv;
+        }
+      } else if constexpr (KV == PKV_KV_E4M3) {
         // a row's PC lanes are consecutive and lane-aligned; every lane of the warp takes part
         const uint32_t ak = dev::row_amax_bits<PC>(max(dev::f16x8_amax_bits(a[u]), dev::f16x8_amax_bits(b[u])));
         const uint32_t av = dev::row_amax_bits<PC>(max(dev::f16x8_amax_bits(va[u]), dev::f16x8_amax_bits(vb[u])));
@@ -212,13 +315,15 @@ __global__ void __launch_bounds__(256) positions_kernel(const int32_t* __restric
   }
 }
 
-template <int D>
-cudaError_t launch_rope(const RopeParams& p, const RopeTurns& turns, bool f8, bool inter, cudaStream_t s) {
+template <int D, bool NORM>
+cudaError_t launch_rope(const RopeParams& p, const RopeTurns& turns, int kv_dtype, bool inter, cudaStream_t s) {
   const dim3 grid((unsigned)((p.num_tokens + p.tokens - 1) / p.tokens)), block(kThreads);
-  if (f8) return inter ? launch_pdl(rope_append_kernel<D, true, true>, grid, block, 0, s, p, turns)
-                       : launch_pdl(rope_append_kernel<D, true, false>, grid, block, 0, s, p, turns);
-  return inter ? launch_pdl(rope_append_kernel<D, false, true>, grid, block, 0, s, p, turns)
-               : launch_pdl(rope_append_kernel<D, false, false>, grid, block, 0, s, p, turns);
+  auto* kernel = kv_dtype == PKV_KV_INT4
+                     ? (inter ? rope_append_kernel<D, PKV_KV_INT4, true, NORM> : rope_append_kernel<D, PKV_KV_INT4, false, NORM>)
+                 : kv_dtype == PKV_KV_E4M3
+                     ? (inter ? rope_append_kernel<D, PKV_KV_E4M3, true, NORM> : rope_append_kernel<D, PKV_KV_E4M3, false, NORM>)
+                     : (inter ? rope_append_kernel<D, PKV_KV_F16, true, NORM> : rope_append_kernel<D, PKV_KV_F16, false, NORM>);
+  return launch_pdl(kernel, grid, block, 0, s, p, turns);
 }
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
@@ -321,20 +426,23 @@ extern "C" pkv_status pkv_positions(pkv_pool* pool, const int32_t* context_lens,
   return PKV_OK;
 }
 
-extern "C" pkv_status pkv_rope_append(pkv_pool* pool, int32_t layer, const pkv_rope* rope, const void* q, int64_t q_stride,
-                                      const void* k, int64_t k_stride, const void* v, int64_t v_stride,
-                                      const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens,
-                                      void* q_out, void* stream) {
-  clear_error();
-  if (!pool) return fail(PKV_ERR_INVALID_ARG, "pool is NULL");
-  pool->last_launches = 0;
-  if (layer < 0 || layer >= pool->cfg.num_layers) return fail(PKV_ERR_OUT_OF_RANGE, "layer out of range");
-  if (!rope) return fail(PKV_ERR_INVALID_ARG, "rope is NULL");
+// The norms of a call: null weights leave the heads as they are.
+struct HeadNorms {
+  const void* q_weight = nullptr;
+  const void* k_weight = nullptr;
+  float eps = 0.f, offset = 0.f;
+};
+
+// Rotation (none with a null rope) and append, with norms in front where `norms` is given.
+static pkv_status rope_append(pkv_pool* pool, int32_t layer, const pkv_rope* rope, const HeadNorms* norms, const void* q,
+                              int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens, void* q_out,
+                              void* stream) {
   const pkv_config& c = pool->cfg;
-  if (rope->cfg.head_dim != c.head_dim) return fail(PKV_ERR_INVALID_ARG, "rope and pool differ in head_dim");
+  if (rope && rope->cfg.head_dim != c.head_dim) return fail(PKV_ERR_INVALID_ARG, "rope and pool differ in head_dim");
   if (num_tokens < 0) return fail(PKV_ERR_INVALID_ARG, "num_tokens must be >= 0");
   if (num_tokens == 0) return PKV_OK;
-  if (!k || !v || !positions || !slot_mapping)
+  if (!k || !v || (rope && !positions) || !slot_mapping)
     return fail(PKV_ERR_INVALID_ARG, "k, v, positions and slot_mapping must be non-NULL");
   if ((q == nullptr) != (q_out == nullptr)) return fail(PKV_ERR_INVALID_ARG, "q and q_out go together");
   const uintptr_t all = reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
@@ -364,24 +472,67 @@ extern "C" pkv_status pkv_rope_append(pkv_pool* pool, int32_t layer, const pkv_r
   p.num_tokens = num_tokens;
   p.num_q_heads = q ? c.num_q_heads : 0;
   p.num_kv_heads = c.num_kv_heads;
-  p.rot_dim = rope->cfg.rot_dim;
-  p.out_scale = (float)rope->cfg.output_scale;
+  p.rot_dim = rope ? rope->cfg.rot_dim : 0;
+  p.out_scale = rope ? (float)rope->cfg.output_scale : 1.f;
   p.err = pool->dev_error;
+  const HeadNorms none;
+  const HeadNorms& hn = norms ? *norms : none;
+  p.q_weight = q ? static_cast<const __half*>(hn.q_weight) : nullptr;
+  p.k_weight = static_cast<const __half*>(hn.k_weight);
+  p.eps = hn.eps;
+  p.weight_offset = hn.offset;
   // Two items a thread, in up to four tokens a CTA (larger CTAs start and end in coarser steps: 256 threads and twice
   // the items took 13.3 us where these take 12.4, 8192 tokens of 12 / 2 heads at d 128); fewer while that would leave
   // SMs without two CTAs.
   const int64_t per = (int64_t)(p.num_q_heads + p.num_kv_heads) * (c.head_dim / 16);
   const int64_t fill = std::max<int64_t>(1, 2 * 128 / per), spread = std::max<int64_t>(1, num_tokens / (2 * (int64_t)pool->num_sms));
   p.tokens = (int)std::min<int64_t>(4, std::min(fill, spread));
-  RopeTurns turns;
-  std::copy(rope->turn, rope->turn + kMaxPairs, turns.turn);
-  const bool f8 = c.kv_dtype == PKV_KV_E4M3, inter = rope->cfg.layout == PKV_ROPE_INTERLEAVED;
+  RopeTurns turns = {};
+  if (rope) std::copy(rope->turn, rope->turn + kMaxPairs, turns.turn);
+  const bool inter = rope && rope->cfg.layout == PKV_ROPE_INTERLEAVED;
+  const int kv = c.kv_dtype;
   const cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = c.head_dim == 64    ? launch_rope<64>(p, turns, f8, inter, s)
-                        : c.head_dim == 128 ? launch_rope<128>(p, turns, f8, inter, s)
-                                            : launch_rope<256>(p, turns, f8, inter, s);
+  const cudaError_t e =
+      norms ? (c.head_dim == 64    ? launch_rope<64, true>(p, turns, kv, inter, s)
+               : c.head_dim == 128 ? launch_rope<128, true>(p, turns, kv, inter, s)
+                                   : launch_rope<256, true>(p, turns, kv, inter, s))
+            : (c.head_dim == 64    ? launch_rope<64, false>(p, turns, kv, inter, s)
+               : c.head_dim == 128 ? launch_rope<128, false>(p, turns, kv, inter, s)
+                                   : launch_rope<256, false>(p, turns, kv, inter, s));
   if (e != cudaSuccess) return cuda_fail(e, "rope_append launch");
   note_append(pool, layer);
   pool->last_launches = 1;
   return PKV_OK;
+}
+
+extern "C" pkv_status pkv_rope_append(pkv_pool* pool, int32_t layer, const pkv_rope* rope, const void* q, int64_t q_stride,
+                                      const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                      const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens,
+                                      void* q_out, void* stream) {
+  clear_error();
+  if (!pool) return fail(PKV_ERR_INVALID_ARG, "pool is NULL");
+  pool->last_launches = 0;
+  if (layer < 0 || layer >= pool->cfg.num_layers) return fail(PKV_ERR_OUT_OF_RANGE, "layer out of range");
+  if (!rope) return fail(PKV_ERR_INVALID_ARG, "rope is NULL");
+  return rope_append(pool, layer, rope, nullptr, q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping, num_tokens,
+                     q_out, stream);
+}
+
+extern "C" pkv_status pkv_norm_rope_append(pkv_pool* pool, int32_t layer, const pkv_rope* rope, const void* q_weight,
+                                           const void* k_weight, float eps, float weight_offset, const void* q, int64_t q_stride,
+                                           const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                           const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens,
+                                           void* q_out, void* stream) {
+  clear_error();
+  if (!pool) return fail(PKV_ERR_INVALID_ARG, "pool is NULL");
+  pool->last_launches = 0;
+  if (layer < 0 || layer >= pool->cfg.num_layers) return fail(PKV_ERR_OUT_OF_RANGE, "layer out of range");
+  if (!q_weight && !k_weight) return fail(PKV_ERR_INVALID_ARG, "no weights: pkv_rope_append is the call without norms");
+  if ((reinterpret_cast<uintptr_t>(q_weight) | reinterpret_cast<uintptr_t>(k_weight)) % 16 != 0)
+    return fail(PKV_ERR_INVALID_ARG, "weights must be 16-byte aligned");
+  if (!(eps >= 1e-30f) || !std::isfinite(eps)) return fail(PKV_ERR_INVALID_ARG, "eps must be finite and at least 1e-30");
+  if (!std::isfinite(weight_offset)) return fail(PKV_ERR_INVALID_ARG, "weight_offset must be finite");
+  const HeadNorms norms{q_weight, k_weight, eps, weight_offset};
+  return rope_append(pool, layer, rope, &norms, q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping, num_tokens, q_out,
+                     stream);
 }

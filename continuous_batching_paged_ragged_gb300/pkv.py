@@ -42,12 +42,14 @@ PKV_ROPE_SCALE_RAMP = 3
 
 PKV_KV_F16 = 0
 PKV_KV_E4M3 = 1
+PKV_KV_INT4 = 4
 
 DEFAULT_SPLIT_BLOCKS = 32  # pkv_config.split_blocks = 0 selects this many blocks per split-K partition
 
 _p = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
+_f32 = ctypes.c_float
 _f64 = ctypes.c_double
 _sz = ctypes.c_size_t
 
@@ -94,6 +96,7 @@ SIGNATURES = {
     "pkv_pool_check": (ctypes.c_int, [_p, ctypes.POINTER(_i32), _i32]),
     "pkv_slot_mapping": (ctypes.c_int, [_p, _p, _i32, _p, _p, _i32, _i32, _p, _p]),
     "pkv_append": (ctypes.c_int, [_p, _i32, _p, _p, _p, _i32, _p]),
+    "pkv_gather": (ctypes.c_int, [_p, _i32, _p, _i32, _p, _p, _p]),
     "pkv_attention_workspace_bytes": (_sz, [_p, _i32, _i32, _i32]),
     "pkv_attention_plan": (ctypes.c_int, [_p, _p, _p, _i32, _i32, _i32, _p, _sz, _p]),
     "pkv_attention_window_workspace_bytes": (_sz, [_p, _i32, _i32, _i32, _i32, _i32]),
@@ -107,6 +110,8 @@ SIGNATURES = {
     "pkv_rope_frequencies": (_i32, [_p, ctypes.POINTER(_f64), _i32]),
     "pkv_positions": (ctypes.c_int, [_p, _p, _p, _i32, _i32, _p, _p]),
     "pkv_rope_append": (ctypes.c_int, [_p, _i32, _p, _p, _i64, _p, _i64, _p, _i64, _p, _p, _i32, _p, _p]),
+    "pkv_norm_rope_append": (ctypes.c_int, [_p, _i32, _p, _p, _p, _f32, _f32, _p, _i64, _p, _i64, _p, _i64, _p, _p, _i32, _p,
+                                            _p]),
     "pkv_copy_blocks": (ctypes.c_int, [_p, _p, _i32, _p]),
     "pkv_fork_rows": (ctypes.c_int, [_p, _p, _i32, _p, _i32, _p, _i32, _p]),
     "pkv_compact_workspace_bytes": (_sz, [_p]),
@@ -227,6 +232,11 @@ def pkv_append(pool: int, layer: int, k, v, slot_mapping, num_tokens: int, strea
            "pkv_append")
 
 
+def pkv_gather(pool: int, layer: int, slot_mapping, num_tokens: int, k_out, v_out, stream=None) -> None:
+    _check(load().pkv_gather(pool, layer, _ptr(slot_mapping), num_tokens, _ptr(k_out), _ptr(v_out), _stream(stream)),
+           "pkv_gather")
+
+
 def pkv_attention_workspace_bytes(pool: int, num_seqs: int, num_tokens: int, max_blocks_per_seq: int) -> int:
     return load().pkv_attention_workspace_bytes(pool, num_seqs, num_tokens, max_blocks_per_seq)
 
@@ -296,6 +306,14 @@ def pkv_rope_append(pool: int, layer: int, rope: int, q, q_stride: int, k, k_str
            "pkv_rope_append")
 
 
+def pkv_norm_rope_append(pool: int, layer: int, rope: Optional[int], q_weight, k_weight, eps: float, weight_offset: float, q,
+                         q_stride: int, k, k_stride: int, v, v_stride: int, positions, slot_mapping, num_tokens: int, q_out,
+                         stream=None) -> None:
+    _check(load().pkv_norm_rope_append(pool, layer, rope, _ptr(q_weight), _ptr(k_weight), eps, weight_offset, _ptr(q), q_stride,
+                                       _ptr(k), k_stride, _ptr(v), v_stride, _ptr(positions), _ptr(slot_mapping), num_tokens,
+                                       _ptr(q_out), _stream(stream)), "pkv_norm_rope_append")
+
+
 def pkv_copy_blocks(pool: int, pairs, num_pairs: int, stream=None) -> None:
     _check(load().pkv_copy_blocks(pool, _ptr(pairs), num_pairs, _stream(stream)), "pkv_copy_blocks")
 
@@ -359,15 +377,26 @@ class Pool:
     def is_8bit(self) -> bool:
         return self.cfg.kv_dtype == PKV_KV_E4M3
 
+    @property
+    def is_4bit(self) -> bool:
+        return self.cfg.kv_dtype == PKV_KV_INT4
+
     def layer(self, layer: int, kv: int):
         """torch view [num_blocks, Hkv, bs, d] of one layer's K (kv=0) or V (kv=1) pool: fp16 values, or uint8
-        E4M3 codes for an 8-bit cache."""
+        E4M3 codes for an 8-bit cache; of a 4-bit cache the uint8 codes [num_blocks, Hkv, d / 32, bs, 16]."""
+        if self.is_4bit:
+            d = self.cfg.head_dim
+            return self.cache_view()[layer, ..., 8 * d * kv:8 * d * (kv + 1)].unflatten(-1, (d // 32, self.cfg.block_size, 16))
         return self.cache_view()[layer, kv]
 
     def cache_view(self):
-        """torch view [L, 2, num_blocks, Hkv, bs, d] of the whole cache (fp16, or uint8 codes)."""
+        """torch view [L, 2, num_blocks, Hkv, bs, d] of the whole cache (fp16, or uint8 codes); of a 4-bit cache its
+        records, uint8 [L, num_blocks, Hkv, 18 d]."""
         import torch
         c = self.cfg
+        if self.is_4bit:
+            shape = (c.num_layers, c.num_blocks, c.num_kv_heads, 18 * c.head_dim)
+            return self.buffer[:shape[0] * shape[1] * shape[2] * shape[3]].view(shape)
         n = 2 * c.num_layers * c.num_blocks * c.num_kv_heads * c.block_size * c.head_dim
         if self.is_8bit:
             v = self.buffer[:n]
@@ -376,8 +405,13 @@ class Pool:
         return v.view(c.num_layers, 2, c.num_blocks, c.num_kv_heads, c.block_size, c.head_dim)
 
     def scales_view(self):
-        """8-bit cache: torch uint8 view [L, num_blocks, Hkv, 2 (K, V), bs] of the scale bytes."""
+        """8-bit cache: torch uint8 view [L, num_blocks, Hkv, 2 (K, V), bs] of the scale bytes.  4-bit cache: fp16
+        view [L, num_blocks, Hkv, bs, 2 (K, V), d / 32] of the scales."""
         c = self.cfg
+        if self.is_4bit:
+            import torch
+            d = c.head_dim
+            return self.cache_view()[..., 16 * d:].view(torch.float16).unflatten(-1, (c.block_size, 2, d // 32))
         assert self.is_8bit, "an fp16 cache has no scales"
         off = 2 * c.num_layers * c.num_blocks * c.num_kv_heads * c.block_size * c.head_dim
         n = 2 * c.num_layers * c.num_blocks * c.num_kv_heads * c.block_size

@@ -34,7 +34,7 @@
  *   - A pool handle is used by one host thread at a time: it remembers the plan issued on each of its 32
  *     most recently planned workspaces and, on an 8-bit cache, the tensor map of the last workspace's fp16
  *     shadow.  Different pools are independent; pkv_last_error is per thread.
- *   - Supported shapes: fp16 Q and K/V inputs; an fp16 or 8-bit (E4M3) cache; head_dim 64, 128 or 256;
+ *   - Supported shapes: fp16 Q and K/V inputs; an fp16, 8-bit (E4M3) or 4-bit cache; head_dim 64, 128 or 256;
  *     block_size 16; num_q_heads a multiple of num_kv_heads with a group of 1, 2, 4, 6 or 8 query heads
  *     per KV head.  Others: PKV_ERR_UNSUPPORTED.
  */
@@ -59,7 +59,7 @@ typedef enum {
 } pkv_status;
 
 /* Device error word bits (pkv_pool_check). */
-#define PKV_DEVERR_SLOT_RANGE   0x1  /* an append: slot outside [-1, num_blocks*block_size)           */
+#define PKV_DEVERR_SLOT_RANGE   0x1  /* an append or gather: slot outside [-1, num_blocks*block_size) */
 #define PKV_DEVERR_BLOCK_RANGE  0x2  /* attention or a block call: block id outside [0, num_blocks)   */
 #define PKV_DEVERR_ROW_META     0x4  /* row with q_len < 1, q_len > ctx, or ctx > max_blocks*bs; a fork's rows */
 #define PKV_DEVERR_QSL          0x8  /* query_start_loc not monotone / not ending at num_tokens       */
@@ -91,9 +91,24 @@ typedef enum {
  * then the status area (at the next 256-byte boundary).  A (block, kv head) run of codes is
  * block_size*head_dim bytes; its K and V scales are one 32-byte record.  Bytes per token of context =
  * 2 * num_layers * num_kv_heads * (head_dim + 1).  K and V inputs must be finite.
+ *
+ * kv_dtype = PKV_KV_INT4, the 4-bit cache.  [ABL], same section, sizes a window's cache at 4 bits next to 8.  32
+ * consecutive values of a cached row (one token's head_dim values of one KV head, K and V separately) share a scale s: the
+ * smallest number of at most 8 significant bits, and a multiple of 2^-24, that is no less than a seventh of their largest
+ * magnitude, kept in fp16 (0 for 32 zeros).  Each value is held as the integer nearest to x / s, ties to even,
+ * which is in -7 .. 7; nothing is clipped.  It stands for code * s, which is an fp16 number (unless within 3 % of the
+ * fp16 maximum): attention, in every path, and pkv_gather read exactly that.  A (block, KV head) is one record of
+ * 18 * head_dim bytes, codes stored plus 8 and two to a byte, the lower half first:
+ *     records[num_layers][num_blocks][num_kv_heads]:
+ *         K codes [head_dim / 32][block_size][16]  uint8
+ *         V codes [head_dim / 32][block_size][16]  uint8
+ *         scales  [block_size][2 (K, V)][head_dim / 32]  fp16
+ * then the status area.  Bytes per token of context = 2 * num_layers * num_kv_heads * (head_dim / 2 + head_dim / 16):
+ * 0.56 of the 8-bit cache's, 0.28 of fp16's.  K and V inputs must be finite.
  * ---------------------------------------------------------------------------------------------- */
 #define PKV_KV_F16  0
 #define PKV_KV_E4M3 1
+#define PKV_KV_INT4 4
 
 typedef struct {
   int32_t num_layers;
@@ -103,7 +118,7 @@ typedef struct {
   int32_t block_size;    /* tokens per block; must be 16 */
   int32_t num_blocks;    /* physical blocks per layer    */
   int32_t split_blocks;  /* blocks per split-K partition of a decode row; 0 = library default (32) */
-  int32_t kv_dtype;      /* PKV_KV_F16 (0) or PKV_KV_E4M3 */
+  int32_t kv_dtype;      /* PKV_KV_F16 (0), PKV_KV_E4M3 or PKV_KV_INT4 */
 } pkv_config;
 
 typedef struct pkv_pool pkv_pool;
@@ -121,11 +136,12 @@ pkv_status pkv_pool_init(const pkv_config* cfg, void* dev_cache, size_t bytes, p
 void pkv_pool_destroy(pkv_pool* pool);
 
 /* Device address of layer `layer`'s K (kv = 0) or V (kv = 1) pool [num_blocks][Hkv][bs][d] (fp16 values,
- * or E4M3 codes for an 8-bit cache); NULL on a bad argument. */
+ * or E4M3 codes for an 8-bit cache; for a 4-bit cache the K or V codes of the layer's first record, of records
+ * 18 * d bytes apart); NULL on a bad argument. */
 void* pkv_pool_layer_ptr(const pkv_pool* pool, int32_t layer, int32_t kv);
 
-/* Device address of layer `layer`'s scale bytes [num_blocks][Hkv][2 (K, V)][bs] of an 8-bit cache; NULL
- * for an fp16 cache or a bad argument. */
+/* Device address of layer `layer`'s scale bytes [num_blocks][Hkv][2 (K, V)][bs] of an 8-bit cache, or of the scales
+ * of the layer's first record of a 4-bit cache; NULL for an fp16 cache or a bad argument. */
 void* pkv_pool_scales_ptr(const pkv_pool* pool, int32_t layer);
 
 /* Synchronously read the device error word (PKV_DEVERR_* bits) into *bits, then clear it if `clear`.
@@ -161,13 +177,25 @@ pkv_status pkv_slot_mapping(pkv_pool* pool, const int32_t* block_tables, int32_t
  * slot_mapping[t] for t < num_tokens; a slot of -1 is skipped (padding); any other out-of-range slot
  * is skipped and sets PKV_DEVERR_SLOT_RANGE.  fp16 cache: a bit copy, no arithmetic.  8-bit cache: each
  * (token, KV head) row of K and of V is quantized as the pool section describes (codes and scale byte,
- * bit-exact).  Duplicate slots in one call race (last writer unspecified).
+ * bit-exact); the 4-bit cache likewise (codes and scales, bit-exact).  Duplicate slots in one call race (last writer unspecified).
  *
  * k, v          fp16 [num_tokens][num_kv_heads][head_dim]   device, 16-byte aligned
  * slot_mapping  int64 [num_tokens]                          device
  * ---------------------------------------------------------------------------------------------- */
 pkv_status pkv_append(pkv_pool* pool, int32_t layer, const void* k, const void* v,
                       const int64_t* slot_mapping, int32_t num_tokens, void* stream);
+
+/* Reads cached rows back as values, whatever the cache holds them in: k_out[t], v_out[t] ([num_kv_heads][head_dim] fp16
+ * each) become what slot slot_mapping[t] of `layer` stands for, for t < num_tokens -- the bits of an fp16 cache, code
+ * times scale of an 8-bit or 4-bit one (exact where that is an fp16 number, as the 4-bit cache's always are, else rounded
+ * to one; within 3 % of the fp16 maximum it saturates to +-65504).  The way out of a pool into another one, of another
+ * format or another engine's, by an append.  Where the slot is -1 the outputs are left as they were; any other
+ * out-of-range slot likewise, and sets PKV_DEVERR_SLOT_RANGE.  A slot may be named more than once.
+ *
+ * slot_mapping  int64 [num_tokens]                          device
+ * k_out, v_out  fp16 [num_tokens][num_kv_heads][head_dim]   device, 16-byte aligned, apart from one another */
+pkv_status pkv_gather(pkv_pool* pool, int32_t layer, const int64_t* slot_mapping, int32_t num_tokens, void* k_out,
+                      void* v_out, void* stream);
 
 /* ------------------------------------------------------------------------------------------------
  * Ragged paged attention
@@ -204,6 +232,10 @@ pkv_status pkv_append(pkv_pool* pool, int32_t layer, const void* k, const void* 
  * shadow blocks, R the most rows of 16+ new tokens the pass can hold.  Rows may share blocks (forks of a prompt that is
  * still being computed): that many hold them all.
  *
+ * 4-bit cache: attention reads the values code * s exactly; scores are scaled by group in fp32, and each softmax
+ * weight is rounded to fp16 together with the value scale that it is multiplied by.  Rows with 16 or more new tokens take
+ * the same fp16 shadow, with the same workspace.
+ *
  * Rows are there to be attended: each has a new token.  A pass with rows that have none is reported
  * (PKV_DEVERR_ROW_META) and its other rows get their results by the decode path, however long; one whose
  * query_start_loc does not run from 0 to num_tokens (PKV_DEVERR_QSL) gets none.
@@ -231,10 +263,10 @@ pkv_status pkv_attention(pkv_pool* pool, int32_t layer, const void* q, const int
  * as pkv_append(pool, layer, k, v, slot_mapping, num_tokens) followed by pkv_attention(...) with the
  * other arguments, under the same plan.  When no row of the pass can take the prefill path (every row
  * has fewer than 16 new tokens; the host checks num_tokens - num_seqs < 15), the append runs inside
- * the decode launch: tiles take this pass's keys and values from k / v directly (on an 8-bit cache,
- * quantized exactly as the append would store them), and each token is written to the cache by the warp
+ * the decode launch: tiles take this pass's keys and values from k / v directly (on an 8-bit
+ * or 4-bit cache, quantized exactly as the append would store them), and each token is written to the cache by the warp
  * whose block holds its position, so no separate append precedes the attention.  Otherwise (and on an
- * 8-bit cache whenever a row may have 16 or more new tokens) this is the append launch followed by the
+ * 8-bit or 4-bit cache whenever a row may have 16 or more new tokens) this is the append launch followed by the
  * attention launches.  Tokens of rows
  * whose metadata is rejected (PKV_DEVERR_ROW_META) are not appended on the fused path.
  *
@@ -365,7 +397,8 @@ pkv_status pkv_positions(pkv_pool* pool, const int32_t* context_lens, const int3
  * slot_mapping[t] of `layer`, as pkv_append would store them (8-bit cache: quantized from the rotated key
  * rounded to fp16, bit for bit what a rotation followed by pkv_append stores).  A slot of -1 is skipped (its
  * query is rotated all the same); any other out-of-range slot is skipped and sets PKV_DEVERR_SLOT_RANGE.
- * Duplicate slots in one call race (last writer unspecified).
+ * Duplicate slots in one call race (last writer unspecified).  (A 4-bit cache quantizes the rounded rotated key, as an 8-bit
+ * one does.)
  *
  * q, k, v       fp16, token t's heads at t * {q,k,v}_stride values from the pointer, [heads][head_dim] within a
  *               token: separate tensors, or slices of one packed projection.  16-byte aligned; strides multiples of 8 and
@@ -379,11 +412,28 @@ pkv_status pkv_rope_append(pkv_pool* pool, int32_t layer, const pkv_rope* rope, 
                            const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens, void* q_out,
                            void* stream);
 
+/* pkv_rope_append with a norm of every head in front of its rotation: with x a query or key head of head_dim values,
+ *     y = x / sqrt(mean(x^2) + eps) * (weight_offset + w)
+ * takes the place of x, w being q_weight for query heads and k_weight for key heads.  All in fp32 -- the mean square, the
+ * product and the rotation of its first rot_dim values -- and rounded once to fp16; an 8-bit or 4-bit cache quantizes that.
+ * Values (v) are appended as they are.  Everything else as pkv_rope_append, and:
+ *
+ * rope                NULL: no rotation (positions are then not read, and may be NULL)
+ * q_weight, k_weight  fp16 [head_dim], device, 16-byte aligned; NULL: the query (key) heads are not normalised.  Not both
+ *                     NULL
+ * eps                 finite, at least 1e-30
+ * weight_offset       finite; 0 for weights as they are, 1 for weights kept as their distance from one */
+pkv_status pkv_norm_rope_append(pkv_pool* pool, int32_t layer, const pkv_rope* rope, const void* q_weight,
+                                const void* k_weight, float eps, float weight_offset, const void* q, int64_t q_stride,
+                                const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                const int32_t* positions, const int64_t* slot_mapping, int32_t num_tokens, void* q_out,
+                                void* stream);
+
 /* ------------------------------------------------------------------------------------------------
  * Copying, forking and compacting blocks (device, every layer)
  *
  * [CB] "The allocator is the other half": requests hold blocks, and a freed block is another's.  These calls
- * move what blocks hold: K and V of every layer and, on an 8-bit cache, the scale bytes, bit for bit.
+ * move what blocks hold: K and V of every layer and, on an 8-bit or 4-bit cache, the scales, bit for bit.
  * ---------------------------------------------------------------------------------------------- */
 
 /* pairs int32 [num_pairs][2] (source, destination), device: block `destination` becomes a copy of block

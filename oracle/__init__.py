@@ -23,6 +23,8 @@ Pages it follows (cited by title and section in each function):
   Not a Bigger Batch", section "Checking it on a real system"); 8-bit KV halves the raw bytes, scales on
   top ("An advertised batch limit proves nothing until sampled", section "Context math sets the ceiling
   the fields ignore").  The E4M3 format is the OCP 8-bit floating point specification's.
+* The 4-bit cache (``oracle.int4``): the same remedy at half the bits (the latter page sizes a window's cache at 4 bits
+  next to 8).
 
 Every function here is pinned by a ``-m "not gpu"`` test against something other than itself (a library
 routine, a closed form, values the pages print, or brute force); see ``tests/test_oracle_*.py``.
@@ -31,12 +33,12 @@ from .attention import attention_row, attention_batch, round_fp16
 from .paging import (kv_bytes_per_token, kv_bytes_for_window, pool_blocks_for_bytes, blocks_for_tokens,
                      max_resident_sequences, cache_bytes, slot_of, slot_mapping_for_batch, append_reference)
 from .window import visible_keys, window_attention_row
-from . import fp8
+from . import fp8, int4
 from .scheduler import ON_DEMAND, PASS, REQUEST, RESERVE, Request, Scheduler, StepRows
 
 __all__ = [
     "attention_row", "attention_batch", "round_fp16",
     "kv_bytes_per_token", "kv_bytes_for_window", "pool_blocks_for_bytes", "blocks_for_tokens",
     "max_resident_sequences", "cache_bytes", "slot_of", "slot_mapping_for_batch", "append_reference",
-    "visible_keys", "window_attention_row", "fp8", "Request", "Scheduler", "StepRows", "ON_DEMAND", "RESERVE", "PASS", "REQUEST",
+    "visible_keys", "window_attention_row", "fp8", "int4", "Request", "Scheduler", "StepRows", "ON_DEMAND", "RESERVE", "PASS", "REQUEST",
 ]
