@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   __shared__ int warp_sums[32];
   __shared__ int hist[kPrefillBuckets];
   __shared__ int n_slots;
-  __shared__ int tail_at[kMaxSplitBlocks + 1];  // per last-split size: its task count, then its next slot
+  __shared__ int tail_at[kMaxSplitBlocksInt4 + 1];  // per last-split size: its task count, then its next slot
   __shared__ int n_dec;
   dev::griddep_wait();
   int bad_qsl = 0, empty_row = 0;
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   }
   for (int i = threadIdx.x; i < p.num_tokens * p.num_kv_heads; i += blockDim.x) p.merge_cnt[i] = 0;
   for (int i = threadIdx.x; i < kPrefillBuckets; i += blockDim.x) hist[i] = 0;
-  for (int i = threadIdx.x; i <= kMaxSplitBlocks; i += blockDim.x) tail_at[i] = 0;
+  for (int i = threadIdx.x; i <= kMaxSplitBlocksInt4; i += blockDim.x) tail_at[i] = 0;
   for (int i = threadIdx.x; i < p.max_slots; i += blockDim.x) p.pf_sync[i] = make_int2(0, 0);
   if (threadIdx.x == 0) n_slots = 0;
   // Reported passes stay inside the workspace and the packed rows: one whose query_start_loc is no list of rows gets no
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   }
   if (threadIdx.x == 0) {  // each last-split size's first slot, largest size first
     int at = carry;
-    for (int sz = kMaxSplitBlocks; sz >= 1; --sz) {
+    for (int sz = kMaxSplitBlocksInt4; sz >= 1; --sz) {
       const int n = tail_at[sz];
       tail_at[sz] = at;
       at += n;
@@ -773,8 +773,8 @@ static pkv_status check_common(pkv_pool* pool, const int32_t* context_lens, cons
   if (max_blocks < 1) return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq must be >= 1");
   if (num_tokens > 0 && (!context_lens || !qsl)) return fail(PKV_ERR_INVALID_ARG, "metadata pointers must be non-NULL");
   const pkv_config& c = pool->cfg;
-  if (c.split_blocks > kMaxSplitBlocks)
-    return fail(PKV_ERR_UNSUPPORTED, "split_blocks above " + std::to_string(kMaxSplitBlocks));
+  const int most = c.kv_dtype == PKV_KV_INT4 ? kMaxSplitBlocksInt4 : kMaxSplitBlocks;
+  if (c.split_blocks > most) return fail(PKV_ERR_UNSUPPORTED, "split_blocks above " + std::to_string(most));
   const int64_t splits = ((int64_t)max_blocks + c.split_blocks - 1) / c.split_blocks;
   if (splits >= (1 << 23) || (int64_t)num_tokens * c.num_kv_heads * splits >= (1ll << 31))
     return fail(PKV_ERR_UNSUPPORTED, "too many splits in one pass; raise split_blocks");
@@ -801,6 +801,10 @@ static pkv_status check_io(const void* q, const void* out, const int32_t* block_
   return PKV_OK;
 }
 
+static KeyWindow pool_window(const pkv_config& c, int window, int sinks) {
+  return make_window(window, sinks, c.split_blocks, c.kv_dtype == PKV_KV_INT4 ? 24 : 8);
+}
+
 // The plan remembered for `workspace`, or null.
 static const PlanKey* find_plan(const pkv_pool* pool, const void* workspace) {
   for (auto it = pool->plans.rbegin(); it != pool->plans.rend(); ++it)
@@ -811,7 +815,7 @@ static const PlanKey* find_plan(const pkv_pool* pool, const void* workspace) {
 // The window of the plan on `workspace` (none without a plan: the call is refused later).
 static KeyWindow planned_window(const pkv_pool* pool, const void* workspace) {
   const PlanKey* k = pool ? find_plan(pool, workspace) : nullptr;
-  return k && k->window != kNoWindow ? make_window(k->window, k->sinks, pool->cfg.split_blocks) : KeyWindow();
+  return k && k->window != kNoWindow ? pool_window(pool->cfg, k->window, k->sinks) : KeyWindow();
 }
 
 // Whether an append that plan `k` did not count on may still be running ahead of an attention call on `layer`: one launched
@@ -915,8 +919,7 @@ extern "C" pkv_status pkv_attention_plan(pkv_pool* pool, const int32_t* context_
 extern "C" size_t pkv_attention_window_workspace_bytes(const pkv_pool* pool, int32_t num_seqs, int32_t num_tokens,
                                                        int32_t max_blocks_per_seq, int32_t window, int32_t sinks) {
   if (!pool || num_seqs < 0 || num_tokens < 0 || max_blocks_per_seq < 1 || window < 1 || sinks < 0) return 0;
-  return ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks_per_seq,
-                   make_window(window, sinks, pool->cfg.split_blocks)).total;
+  return ws_layout(pool->cfg, num_seqs, num_tokens, max_blocks_per_seq, pool_window(pool->cfg, window, sinks)).total;
 }
 
 extern "C" pkv_status pkv_attention_window_plan(pkv_pool* pool, const int32_t* context_lens,
@@ -928,7 +931,7 @@ extern "C" pkv_status pkv_attention_window_plan(pkv_pool* pool, const int32_t* c
   if (sinks < 0) return fail(PKV_ERR_INVALID_ARG, "sinks must be >= 0");
   if (!pool) return fail(PKV_ERR_INVALID_ARG, "pool is NULL");
   return plan_pass(pool, context_lens, query_start_loc, num_seqs, num_tokens, max_blocks_per_seq,
-                   make_window(window, sinks, pool->cfg.split_blocks), workspace, workspace_bytes, stream);
+                   pool_window(pool->cfg, window, sinks), workspace, workspace_bytes, stream);
 }
 
 extern "C" pkv_status pkv_attention(pkv_pool* pool, int32_t layer, const void* q, const int32_t* block_tables,

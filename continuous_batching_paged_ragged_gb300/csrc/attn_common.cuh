@@ -11,6 +11,7 @@ namespace pkv {
 
 constexpr int kBS = 16;          // tokens per cache block
 constexpr int kHeadsTile = 8;    // query heads per KV head handled by one decode MMA tile (G <= 8)
+constexpr int kMaxSplitBlocksInt4 = 128;  // upper bound on split_blocks, and its default, on a 4-bit cache
 
 // Rows with at least this many new tokens (a prefill chunk) go to the tensor-core tile kernel; shorter
 // rows (decode, short chunks) to the split-K decode kernel.  The choice depends on the row alone, so a
@@ -45,13 +46,14 @@ struct KeyWindow {
 // 8-bit d 256 path): 66 blocks as 24 + 24 + 18 take 51.2 us, as 32 + 32 + 2 54.4 (256 rows, 12 / 2 heads, d 128); 34 as
 // 24 + 10 33.0 against 36.2; 261 stay at 32 (103 us on the 8-bit cache at d 256, 120 in splits of 28).  At head_dim 64,
 // whose warps go in pairs of blocks, the 66 would be faster as 32 + 32 + 2 (8 / 2 heads: 41.0 us, 45.6 so).  The window
-// alone decides, and a token whose whole context is visible keeps the unwindowed partition.
+// alone decides, and a token whose whole context is visible keeps the unwindowed partition.  (On a 4-bit cache, of
+// longer splits for more warps, rounded up to `unit` = 24 blocks, a pair for each of twelve.)
 __host__ __device__ constexpr int window_blocks_at_most(int window, int sinks) {
   return (sinks + kBS - 1) / kBS + (window > kNoWindow - kBS ? kNoWindow / kBS : (window + kBS - 2) / kBS) + 1;
 }
-__host__ constexpr KeyWindow make_window(int window, int sinks, int split_blocks) {
+__host__ constexpr KeyWindow make_window(int window, int sinks, int split_blocks, int unit = 8) {
   const int seen = window_blocks_at_most(window, sinks < kNoWindow - kBS ? sinks : kNoWindow - kBS);
-  const int n = (seen + split_blocks - 1) / split_blocks, even = ((seen + n - 1) / n + 7) / 8 * 8;
+  const int n = (seen + split_blocks - 1) / split_blocks, even = ((seen + n - 1) / n + unit - 1) / unit * unit;
   return KeyWindow{window, sinks, even < split_blocks ? even : split_blocks};
 }
 // Blocks per split of a token that sees ctx keys without the window.

@@ -1,5 +1,5 @@
 // The persistent split-K decode kernel: per-pass tasks (one split of one (token, KV head)) taken by
-// persistent CTAs of four streaming warps, a combiner warp and a scheduler warp; the cache is streamed
+// persistent CTAs of four streaming warps (more on the 4-bit cache), a combiner warp and a scheduler warp; the cache is streamed
 // through per-warp TMA rings and the group contraction runs on warp MMAs.  Templated on the head
 // dimension, the query heads per KV head and the cache format (fp16 values, 8-bit E4M3 codes with a
 // power-of-two scale per cached row, or 4-bit records), so each format's instances compile in their own translation unit.
@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "int4.cuh"
@@ -29,16 +30,16 @@ constexpr int kMaxSplitBlocks = 32;   // upper bound on split_blocks (a split's 
 constexpr int kSmemPerSM = 228 * 1024;  // shared memory of one SM
 constexpr int kSmemReservedPerCTA = 1024;
 constexpr int kStaticTasks = 1;         // each CTA's first task comes without a counter (see Scheduler)
-constexpr int kEagerClaimBlocks = 8;    // past tasks this small, the scheduler claims as early as slots allow
 
 // One task as the scheduler warp hands it to the streaming warps and the combiner warp (shared memory).
+template <int MAXB, typename Jump>
 struct TaskEntry {
   int4 rec;  // {token (-1: no more tasks), kv head | split << 8, row, causal context}
   int nst;   // the row's first position appended this pass
   int nb;    // blocks in the split
-  int rot;   // block i of the split goes to streaming warp (i + rot) % 4 (a function of the row alone)
-  int jump;  // windowed: split blocks ahead of the gap behind the sinks (5 bits) | row blocks in the gap << 5
-  int ids[kMaxSplitBlocks];  // the split's physical block ids
+  int rot;   // block i of the split (4-bit: pair of blocks i) goes to streaming warp (i + rot) % NW (a function of the row alone)
+  Jump jump;  // windowed: split blocks ahead of the gap behind the sinks (JB bits) | row blocks in the gap << JB
+  int ids[MAXB];  // the split's physical block ids
 };
 
 // Cache formats of the decode kernel (template parameter KV).
@@ -48,39 +49,55 @@ constexpr int kKvInt4 = 2;  // 4-bit codes with a scale for 32 values: K, V and 
 
 template <int D, int G, int KV>
 struct DecodeTraits {
-  static constexpr int NW = 4;                     // streaming warps; then the combiner and the scheduler
-  static constexpr int NTHREADS = (NW + 2) * 32;
   static constexpr bool F8 = KV == kKvE4M3;
   static constexpr bool I4 = KV == kKvInt4;
-  // one (block, KV head) run of K or V; 4-bit: its whole record
-  static constexpr int RUN = I4 ? Int4Record<D>::BYTES : kBS * D * (F8 ? 1 : 2);
-  static constexpr int RPB = I4 ? 1 : 2;           // runs per block
+  // Streaming warps; then the combiner and the scheduler (4-bit: and the producers, decode_int4.cuh).  fp16, 8-bit: four
+  // streaming warps, in two or three CTAs per SM.  4-bit: one CTA with as many warps as the registers allow (sixteen in all
+  // with 128 each; twelve with 168 at head_dim 256, two fewer with eight query heads, whose shares leave less room for the
+  // rings).  Its blocks are a quarter of the bytes, so its tasks are more blocks (up to 128, MAXB), and what a task costs
+  // beside its blocks is paid once an SM.
+  static constexpr int NW = !I4 ? 4 : D != 256 ? 12 : G > 6 ? 6 : 8;
+  static constexpr int NP = I4 ? 2 : 0;
+  static constexpr int MAXB = I4 ? kMaxSplitBlocksInt4 : kMaxSplitBlocks;  // blocks of a task at most
+  static constexpr int JB = I4 ? 16 : 5;
+  using Jump = std::conditional_t<I4, uint64_t, uint32_t>;
+  using Task = TaskEntry<MAXB, Jump>;
+  static constexpr int EAGER = 2 * NW;             // past tasks this small, the scheduler claims as early as slots allow
+  static constexpr int NTHREADS = (NW + 2 + NP) * 32;
+  // one (block, KV head) run of K or V; 4-bit: the records of two blocks, a stage of the ring
+  static constexpr int RUN = I4 ? 2 * Int4Record<D>::BYTES : kBS * D * (F8 ? 1 : 2);
   static constexpr int BOXROWS = kBS * D / 128;    // 8-bit: 128-byte rows of a run (its box height)
   static constexpr int SCL = F8 ? 32 : 0;          // 8-bit: scale record per slot (the K and V scales of a block)
-  static constexpr int RING = F8 || I4 ? 16 : PKV_DECODE_RING(D);  // 8-bit, 4-bit: as many slots as fit, up to 16
+  static constexpr int RING = I4 ? 4 * NW : F8 ? 16 : PKV_DECODE_RING(D);  // 8-bit, 4-bit: as many slots as fit
   static constexpr int KS = D / 16;                // MMA k-steps over the head dimension (scores)
   static constexpr int MT = D / 16;                // MMA m-tiles over the head dimension (values)
   static constexpr int OV = MT * 4;                // fp32 output values per lane (8-head fragment)
   static constexpr int LG = (G + 1) / 2;           // lanes l with (l & 3) < LG hold real heads
   static constexpr int SHL = 8 * LG;               // such lanes
   static constexpr int QD = 3;                     // task queue depth
-  static constexpr int QB = G * D * 2;             // a streaming warp's q buffer (the G heads' rows)
+  static constexpr int QB = G * D * 2;             // a q buffer (the G heads' rows)
+  static constexpr int NQ = I4 ? QD : NW;          // q buffers: one a streaming warp; 4-bit: one a queue entry
+  static constexpr int RW = I4 ? 1 : NW;           // rings that NR is the slots of: every streaming warp's; 4-bit: all in one
   // everything but the rings: q buffers, shares, staging, queue, the other barriers, flag, alignment slack
-  static constexpr int REST = NW * QB + NW * OV * SHL * 4 + NW * kHeadsTile * 8 + G * D * 4 + 64 +
-                              QD * (int)sizeof(TaskEntry) + (3 * NW + 3 * QD + 1) * 8 + 8 + 16 + 1024;
-  static constexpr int SLOT = RUN + SCL + 8;       // a ring slot with its scale record and its barrier
-  static constexpr int NR_FIT = (kSmemPerSM / 2 - kSmemReservedPerCTA - REST) / (NW * SLOT);
-  static constexpr int NR = RING < NR_FIT ? RING : (NR_FIT < 2 ? 2 : NR_FIT);
-  static constexpr int OFF_QB = NW * NR * RUN;                       // [NW] q buffers
-  static constexpr int OFF_SHARE = OFF_QB + NW * QB;                 // [NW][OV][SHL] fp32 o shares
+  static constexpr int REST = NQ * QB + NW * OV * SHL * 4 + NW * kHeadsTile * 8 + G * D * 4 + 64 +
+                              QD * (int)sizeof(Task) + (2 * NW + NQ + 3 * QD + 1) * 8 + 8 + 16 + 1024;
+  static constexpr int SLOT = RUN + SCL + (I4 ? 16 : 8);  // a ring slot with its scale record and its barrier (4-bit: two)
+  static constexpr int WANT = I4 ? 1 : 2;          // CTAs per SM that the rings leave room for
+  static constexpr int NR_FIT = (kSmemPerSM / WANT - kSmemReservedPerCTA - REST) / (RW * SLOT);
+  static constexpr int NR_ANY = RING < NR_FIT ? RING : (NR_FIT < 2 ? 2 : NR_FIT);
+  static constexpr int NRW = NR_ANY / (I4 ? NW : 1);  // slots of a streaming warp
+  static constexpr int NR = I4 ? NRW * NW : NR_ANY;
+  static constexpr int RB = I4 ? 2 * NR : NW * NR;  // ring barriers
+  static constexpr int OFF_QB = RW * NR * RUN;                       // [NQ] q buffers
+  static constexpr int OFF_SHARE = OFF_QB + NQ * QB;                 // [NW][OV][SHL] fp32 o shares
   static constexpr int OFF_SML = OFF_SHARE + NW * OV * SHL * 4;      // [NW][8] float2 (m, l) shares
   static constexpr int OFF_STG = OFF_SML + NW * kHeadsTile * 8;      // combiner staging [G][D] fp32
   static constexpr int OFF_MML = OFF_STG + G * D * 4;                // staged split's (m, l): [8] float2
-  static constexpr int OFF_Q = OFF_MML + 64;                         // [QD] TaskEntry
-  static constexpr int OFF_BAR = OFF_Q + QD * (int)sizeof(TaskEntry);
-  // barriers: ring [NW][NR], share_full [NW], share_empty [NW], queue full [QD], queue empty [QD], q [NW],
-  // queue half-done [QD], the combiner's partial copy
-  static constexpr int NBARS = NW * NR + 3 * NW + 3 * QD + 1;
+  static constexpr int OFF_Q = OFF_MML + 64;                         // [QD] Task
+  static constexpr int OFF_BAR = OFF_Q + QD * (int)sizeof(Task);
+  // barriers: ring [NW][NR] (4-bit: full [NR], empty [NR]), share_full [NW], share_empty [NW], queue full [QD], queue empty
+  // [QD], q [NQ], queue half-done [QD], the combiner's partial copy
+  static constexpr int NBARS = RB + 2 * NW + NQ + 3 * QD + 1;
   static constexpr int OFF_FLAG = OFF_BAR + (NBARS * 8 + 15) / 16 * 16;  // the CTA's abort flag
   static constexpr int OFF_SCL = OFF_FLAG + 16;                      // 8-bit: [NW][NR] scale records
   static constexpr int SMEM = OFF_SCL + NW * NR * SCL + 1024;        // + slack to align the rings to 1024 bytes
@@ -88,13 +105,13 @@ struct DecodeTraits {
   // CTAs per SM (shared memory bound).  The 8-bit d = 256 kernel with 8 query heads per KV head holds too
   // much in registers for two CTAs (it spills); like its fp16 twin, which shared memory limits to one, it
   // runs one CTA per SM with the whole register file.
-  static constexpr int MINB = (F8 && D == 256 && G > 6) ? 1 : (FIT < 3 ? FIT : 3);
+  static constexpr int MINB = I4 || (F8 && D == 256 && G > 6) ? 1 : (FIT < 3 ? FIT : 3);
   static_assert(D % 64 == 0 && G >= 1 && G <= kHeadsTile, "shape");
   static_assert(I4 || RUN % 1024 == 0, "swizzled boxes need 1024-byte aligned slots");
-  static_assert(!I4 || (RUN % 128 == 0 && NR >= 2), "records are bulk-copy destinations; their blocks go in pairs");
+  static_assert(!I4 || (RUN % 256 == 0 && NRW >= 2 && NW % NP == 0), "records are bulk-copy destinations; stages ahead");
   static_assert(KS % 2 == 0 && QB % 128 == 0, "k-steps in pairs; q buffers stay 16-byte aligned");
   static_assert(OFF_Q % 16 == 0 && OFF_BAR % 8 == 0 && OFF_STG % 16 == 0 && OFF_MML % 16 == 0, "alignment");
-  static_assert(NR <= RING && SMEM <= NW * NR * SLOT + REST + 64, "shared-memory budget");
+  static_assert(NR <= RING && SMEM <= RW * NR * SLOT + REST + 64, "shared-memory budget");
   static_assert(!F8 || (RUN % 1024 == 0 && BOXROWS <= 256), "8-bit runs are whole swizzle atoms, one box each");
   static_assert(OFF_SCL % 16 == 0, "scale records are bulk-copy destinations");
   static_assert(MINB >= 1, "shared memory");
@@ -209,13 +226,13 @@ struct DecodeSmem {
   float2* sh_ml;        // [NW][8]
   float* stg;           // [G][D] fp32 (or [G][D] fp16 for a final output)
   float2* mml;          // [8] (m, l) of the staged split
-  TaskEntry* queue;     // [QD]
+  typename T::Task* queue;  // [QD]
   uint64_t* ring_bar;   // [NW][NR]
   uint64_t* share_full;
   uint64_t* share_empty;
   uint64_t* qfull;
   uint64_t* qempty;
-  uint64_t* qbar;       // [NW] the q buffers' barriers
+  uint64_t* qbar;       // [NQ] the q buffers' barriers
   uint64_t* qmid;       // [QD] every streaming warp has consumed half of its runs of the entry's task
   uint64_t* pbar;       // the combiner's copy of another split's partial into stg / mml
   volatile int* abort;
@@ -227,14 +244,14 @@ struct DecodeSmem {
     sh_ml = reinterpret_cast<float2*>(s + T::OFF_SML);
     stg = reinterpret_cast<float*>(s + T::OFF_STG);
     mml = reinterpret_cast<float2*>(s + T::OFF_MML);
-    queue = reinterpret_cast<TaskEntry*>(s + T::OFF_Q);
+    queue = reinterpret_cast<typename T::Task*>(s + T::OFF_Q);
     ring_bar = reinterpret_cast<uint64_t*>(s + T::OFF_BAR);
-    share_full = ring_bar + T::NW * T::NR;
+    share_full = ring_bar + T::RB;
     share_empty = share_full + T::NW;
     qfull = share_empty + T::NW;
     qempty = qfull + T::QD;
     qbar = qempty + T::QD;
-    qmid = qbar + T::NW;
+    qmid = qbar + T::NQ;
     pbar = qmid + T::QD;
     abort = reinterpret_cast<volatile int*>(s + T::OFF_FLAG);
     scl = s + T::OFF_SCL;
@@ -245,14 +262,18 @@ struct DecodeSmem {
 struct TaskView {
   int t, g, row, ctx, nst;
   int base;         // the split's first block among the token's (visible) blocks
-  int nbw;          // blocks of the split dealt to this warp: task-local blocks bw, bw + 4, ...
+  int nbw;          // blocks of the split dealt to this warp: task-local blocks bw, bw + NW, ...
   int bw;
   int nlean;        // the warp's leading blocks that are full and hold no row of this pass (see Streamer)
-  int jump;         // W: TaskEntry::jump
+  uint32_t jump;    // W: TaskEntry::jump
   const int* ids;   // shared memory: the split's block ids
 };
 
-__device__ __forceinline__ int warp_blocks(int nb, int bw) { return nb > bw ? (nb - bw + 3) / 4 : 0; }
+template <int NW>
+__device__ __forceinline__ int warp_blocks(int nb, int bw) { return nb > bw ? (nb - bw + NW - 1) / NW : 0; }
+// The place of warp w in a dealing rotated by rot (both below NW).
+template <int NW>
+__device__ __forceinline__ int dealt(int w, int rot) { return NW == 4 ? (w - rot) & 3 : w >= rot ? w - rot : w - rot + NW; }
 
 // ---------------------------------------------------------------------------------------------------
 // Streaming warp: takes the CTA's tasks in queue order, streams the K and V runs of its share of each
@@ -309,7 +330,7 @@ struct Streamer {
       v.nbw = 0;
       return;
     }
-    const TaskEntry* e = &sm.queue[kk % T::QD];
+    const typename T::Task* e = &sm.queue[kk % T::QD];
     const int4 rec = e->rec;
     v.t = rec.x;
     v.g = rec.y & 0xFF;
@@ -318,8 +339,8 @@ struct Streamer {
     v.base = (rec.y >> 8) * split_size<W>(p, v.ctx);
     v.nst = e->nst;
     if constexpr (W) v.jump = e->jump;
-    v.bw = (warp - e->rot) & 3;
-    v.nbw = v.t >= 0 ? warp_blocks(e->nb, v.bw) : 0;
+    v.bw = dealt<T::NW>(warp, e->rot);
+    v.nbw = v.t >= 0 ? warp_blocks<T::NW>(e->nb, v.bw) : 0;
     v.ids = e->ids;
     // A block is on the lean path when all its 16 keys are inside the context and none is this pass's (with
     // the append fused, the pass's rows come from the inputs): blocks below position `from`.  The same rule
@@ -331,20 +352,15 @@ struct Streamer {
     const int nfull = from / kBS - skip - first;  // blocks first, first + NW, ... below from / 16
     v.nlean = (!kPairs<D, KV, W> || nfull <= 0) ? 0 : min(v.nbw, (nfull + T::NW - 1) / T::NW);
   }
-  static __device__ __forceinline__ int runs(const TaskView& v) { return v.t >= 0 ? T::RPB * v.nbw : 0; }
+  static __device__ __forceinline__ int runs(const TaskView& v) { return v.t >= 0 ? 2 * v.nbw : 0; }
   __device__ __forceinline__ int block_pos(const TaskView& v, int j) const {
     const int b = v.bw + T::NW * j;  // of the split
-    const int gap = W && b >= (v.jump & 31) ? (int)((uint32_t)v.jump >> 5) : 0;
+    const int gap = W && b >= (int)(v.jump & ((1u << T::JB) - 1)) ? (int)(v.jump >> T::JB) : 0;
     return (v.base + b + gap) * kBS;
   }
   // Run r of the warp's stream within a task: the lean blocks go in pairs, K of both then V of both; the rest
   // (an odd lean block, then the blocks holding the context's end or this pass's rows) one by one, K then V.
   static __device__ __forceinline__ void run_of(const TaskView& v, int r, int& j, int& isv) {
-    if constexpr (T::I4) {  // a run is a block
-      j = r;
-      isv = 0;
-      return;
-    }
     const int pr = 4 * (v.nlean >> 1);
     if (r < pr) {
       j = 2 * (r >> 2) + (r & 1);
@@ -363,11 +379,7 @@ struct Streamer {
     run_of(v, r, j, isv);
     r = isv;  // below, r & 1 tells V from K
     const int id = v.ids[v.bw + T::NW * j];
-    if constexpr (T::I4) {
-      dev::mbar_arrive_expect_tx(&bars[slot], T::RUN);
-      dev::bulk_g2s(dst, reinterpret_cast<const char*>(p.cache_k) + ((size_t)id * p.num_kv_heads + v.g) * T::RUN, T::RUN,
-                    &bars[slot], pol);
-    } else if constexpr (T::F8) {
+    if constexpr (T::F8) {
       // the codes as one box; a K run brings the block's 32-byte scale record (K and V scales) along
       dev::mbar_arrive_expect_tx(&bars[slot], T::RUN + ((r & 1) ? 0 : T::SCL));
       if constexpr (D == 256) {  // the keys' first, then their second 128 code bytes (rows are tokens), one copy
@@ -419,22 +431,7 @@ struct Streamer {
     ok = __all_sync(0xffffffffu, got) && ok;
     if (!ok) return;
     const uint32_t qs = dev::smem_addr(qbuf);
-    if constexpr (T::I4) {
-      // The 4-bit K fragments: lane l's word of a 32-value group is values 8t .. 8t + 7 (t = l % 4), which unpack in
-      // pairs (i, i + 4); pairs 0 and 1 are MMA k indices 2t, 2t + 1 and 2t + 8, 2t + 9 of the group's first step, pairs 2
-      // and 3 of its second.  q takes the same order, which leaves every dot product as it is.
-#pragma unroll
-      for (int g = 0; g < D / 32; ++g) {
-        uint32_t x, y, z, u;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x), "=r"(y), "=r"(z), "=r"(u)
-                     : "r"(qs + ((lane >> 2) < G ? lane >> 2 : 0) * (D * 2) + (32 * g + 8 * (lane & 3)) * 2));
-        qb[2 * g][0] = __byte_perm(x, z, 0x5410);
-        qb[2 * g][1] = __byte_perm(x, z, 0x7632);
-        qb[2 * g + 1][0] = __byte_perm(y, u, 0x5410);
-        qb[2 * g + 1][1] = __byte_perm(y, u, 0x7632);
-      }
-    } else if constexpr (T::F8) {
+    if constexpr (T::F8) {
       // The 8-bit K fragments hold dims 4t .. 4t + 3 of a 16-dim step as MMA k indices 2t, 2t + 1, 2t + 8,
       // 2t + 9 (the order ldmatrix delivers bytes in); q takes the same order, which leaves every dot
       // product as it is.
@@ -503,15 +500,6 @@ struct Streamer {
     ok = __all_sync(0xffffffffu, got) && ok;
     return dev::smem_addr(ring + slot * T::RUN);
   }
-  // The same for the run `ahead` places behind it, which must have been issued.
-  __device__ __forceinline__ uint32_t wait_run(int ahead) {
-    const int r = consumed + ahead;
-    const bool got = cta_wait(&bars[r % T::NR], (r / T::NR) & 1, sm.abort, p.err);
-    ok = __all_sync(0xffffffffu, got) && ok;
-    return run_addr(ahead);
-  }
-  // The slot of the run `ahead` places behind the oldest.
-  __device__ __forceinline__ uint32_t run_addr(int ahead) const { return dev::smem_addr(ring + (consumed + ahead) % T::NR * T::RUN); }
   // Half-way through the current task (half of this warp's runs consumed; at once for a warp with none): the
   // scheduler warp claims the CTA's next task once every streaming warp is there (see Scheduler).
   __device__ __forceinline__ void task_start() {
@@ -560,11 +548,6 @@ struct Streamer {
     cur_q_done = cur.nbw == 0;  // a task with no blocks for this warp needs no q
   }
 };
-
-// The 4-bit cache's loop over the same tasks (decode_int4.cuh).
-template <int D, int G, bool W>
-__device__ __forceinline__ void stream_loop_int4(const DecodeParams& p, const DecodeSmem<D, G, kKvInt4>& sm,
-                                                 Streamer<D, G, kKvInt4, W>& w);
 
 template <int D, int G, int KV, bool W>
 __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeSmem<D, G, KV>& sm, Streamer<D, G, KV, W>& w) {
@@ -1104,18 +1087,23 @@ struct Scheduler {
 #pragma unroll
     for (int j = 0; j < N; ++j)  // past the list: the end of the work, with nothing to load
       rec[j] = idx[j] < n_tasks && idx[j] < p.max_tasks ? __ldcg(p.tasks + idx[j]) : make_int4(-1, 0, 0, 0);
-    int id[N], q0[N];
+    constexpr int IL = T::MAXB / 32;  // block ids a lane
+    int id[N][IL], q0[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      id[j] = 0;
+#pragma unroll
+      for (int i = 0; i < IL; ++i) id[j][i] = 0;
       q0[j] = 0;
       if (rec[j].x >= 0) {
         const int s = rec[j].y >> 8;
         const VisibleUnits vis = token_blocks<W>(p, rec[j].w);
         const int size = split_size<W>(p, rec[j].w);
-        const int b = s * size + lane;  // the split's block `lane` among the visible ones
-        if (lane < min(size, vis.n - s * size))
-          id[j] = __ldcg(p.block_tables + (int64_t)rec[j].z * p.max_blocks + (W ? vis.row_unit(b) : b));
+#pragma unroll
+        for (int i = 0; i < IL; ++i) {
+          const int b = s * size + lane + 32 * i;  // the split's block `lane + 32 i` among the visible ones
+          if (lane + 32 * i < min(size, vis.n - s * size))
+            id[j][i] = __ldcg(p.block_tables + (int64_t)rec[j].z * p.max_blocks + (W ? vis.row_unit(b) : b));
+        }
         q0[j] = __ldcg(p.qsl + rec[j].z);
       }
     }
@@ -1123,8 +1111,9 @@ struct Scheduler {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       if (ended) break;
-      TaskEntry* e = &sm.queue[filled % T::QD];
-      int nb = 0, nst = 0, rot = 0, jump = 0;
+      typename T::Task* e = &sm.queue[filled % T::QD];
+      int nb = 0, nst = 0, rot = 0;
+      typename T::Jump jump = 0;
       if (rec[j].x >= 0) {
         const int g = rec[j].y & 0xFF, s = rec[j].y >> 8, ctx = rec[j].w;
         const VisibleUnits vis = token_blocks<W>(p, ctx);
@@ -1132,19 +1121,21 @@ struct Scheduler {
         nb = min(size, vis.n - s * size);
         if constexpr (W) {  // the split's blocks ahead of the gap: none, some, or all (then it has no gap)
           const int ahead = max(0, vis.head - s * size);
-          if (ahead < nb) jump = (int)((uint32_t)ahead | (uint32_t)vis.skip << 5);
+          if (ahead < nb) jump = (typename T::Jump)ahead | (typename T::Jump)vis.skip << T::JB;
         }
-        if (lane < nb) {
-          int v = id[j];
-          if (v < 0 || v >= p.num_blocks) {
-            dev::set_error(p.err, PKV_DEVERR_BLOCK_RANGE);
-            v = 0;  // keep the copy in bounds; this token's output is flagged as invalid
+#pragma unroll
+        for (int i = 0; i < IL; ++i)
+          if (lane + 32 * i < nb) {
+            int v = id[j][i];
+            if (v < 0 || v >= p.num_blocks) {
+              dev::set_error(p.err, PKV_DEVERR_BLOCK_RANGE);
+              v = 0;  // keep the copy in bounds; this token's output is flagged as invalid
+            }
+            e->ids[lane + 32 * i] = v;
           }
-          e->ids[lane] = v;
-        }
         const int qi = rec[j].x - q0[j];  // the token's index among its row's new tokens
         nst = ctx - 1 - qi;
-        rot = (qi + g + s) & 3;  // row-local, so the dealing (and the result) does not depend on the batch
+        rot = (uint32_t)(qi + g + s) % T::NW;  // row-local, so the dealing (and the result) does not depend on the batch
       }
       if (lane == 0) {
         e->rec = rec[j];
@@ -1193,12 +1184,16 @@ struct Scheduler {
     // 1.015 with nothing ahead of the wait.  (By this warp: in the streaming warps the code moved their spills, 7 % on the
     // windowed 8-bit decode at d 256.)
     if (!p.early) {
-      const TaskEntry* e = &sm.queue[0];
+      const typename T::Task* e = &sm.queue[0];
       __syncwarp();
-      if (lane < min(e->nb, T::NW * ((T::NR + 1) / 2))) {
+      if constexpr (T::I4) {
+        constexpr int REC = T::RUN / 2;
+        if (lane < e->nb)
+          dev::bulk_prefetch_l2(reinterpret_cast<const char*>(p.cache_k) + ((size_t)e->ids[lane] * p.num_kv_heads + (e->rec.y & 0xFF)) * REC, REC);
+      } else if (lane < min(e->nb, T::NW * ((T::NR + 1) / 2))) {
         const size_t at = ((size_t)e->ids[lane] * p.num_kv_heads + (e->rec.y & 0xFF)) * T::RUN;
         dev::bulk_prefetch_l2(reinterpret_cast<const char*>(p.cache_k) + at, T::RUN);
-        if constexpr (!T::I4) dev::bulk_prefetch_l2(reinterpret_cast<const char*>(p.cache_v) + at, T::RUN);
+        dev::bulk_prefetch_l2(reinterpret_cast<const char*>(p.cache_v) + at, T::RUN);
       }
     }
   }
@@ -1215,7 +1210,7 @@ struct Scheduler {
       const int m = filled;
       // A long list (many tasks per CTA) balances itself; there the next task is claimed as soon as the
       // previous one has been handed on, for the deepest look-ahead.
-      const bool small = last_nb <= kEagerClaimBlocks || n_tasks > 4 * (int)gridDim.x;
+      const bool small = last_nb <= T::EAGER || n_tasks > 4 * (int)gridDim.x;
       // Near the end of the list (this CTA's last claim was within two grids of it), the counter is read
       // before waiting: once every task has been claimed (the counter may lag, never run ahead) the end of
       // the work is published at once, and the warps finish without waiting for a claim that can only come
@@ -1423,7 +1418,7 @@ struct Combiner {
     for (int k = 0;; ++k) {
       // ---- the task's description; then its queue slot may be refilled ----
       if (!cta_wait(&sm.qfull[k % T::QD], (k / T::QD) & 1, sm.abort, p.err)) return;
-      const TaskEntry* e = &sm.queue[k % T::QD];
+      const typename T::Task* e = &sm.queue[k % T::QD];
       const int4 rec = e->rec;
       const int nb = e->nb, rot = e->rot;
       __syncwarp();
@@ -1466,8 +1461,48 @@ struct Combiner {
 #pragma unroll
       for (int r = 0; r < T::OV; ++r) acc[r] = 0.f;
       float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
+      if constexpr (T::I4) {
+        // The 4-bit cache's shares are more and come sooner one after another: all of them first, then one reference for all
+        // and a single pass (one by one, twelve shares took 9 us, longer than their task).
+        uint32_t there = 0;
+        for (int w = 0; w < T::NW; ++w) {
+          if (dealt<T::NW>(w, rot) >= (nb + 1) / 2) continue;  // (dealt in pairs)
+          if (!cta_wait(&sm.share_full[w], (taken >> w) & 1, sm.abort, p.err)) {
+            bail();
+            return;
+          }
+          there |= 1u << w;
+        }
+        taken ^= there;
+        if (real) {
+          for (int w = 0; w < T::NW; ++w)
+            if (there >> w & 1) {
+              const float4 ml = *reinterpret_cast<const float4*>(sm.sh_ml + w * kHeadsTile + 2 * hg);
+              M0 = fmaxf(M0, ml.x);
+              M1 = fmaxf(M1, ml.z);
+            }
+          for (int w = 0; w < T::NW; ++w)
+            if (there >> w & 1) {
+              const float4 ml = *reinterpret_cast<const float4*>(sm.sh_ml + w * kHeadsTile + 2 * hg);
+              const float f0 = dev::ex2_approx(ml.x - M0), f1 = dev::ex2_approx(ml.z - M1);
+              L0 = fmaf(ml.y, f0, L0);
+              L1 = fmaf(ml.w, f1, L1);
+              const float4* so = reinterpret_cast<const float4*>(sm.sh_o + w * T::OV * T::SHL) + ci;
+#pragma unroll
+              for (int mt = 0; mt < T::MT; ++mt) {
+                const float4 v = so[mt * T::SHL];
+                acc[4 * mt] = fmaf(v.x, f0, acc[4 * mt]);
+                acc[4 * mt + 1] = fmaf(v.y, f1, acc[4 * mt + 1]);
+                acc[4 * mt + 2] = fmaf(v.z, f0, acc[4 * mt + 2]);
+                acc[4 * mt + 3] = fmaf(v.w, f1, acc[4 * mt + 3]);
+              }
+            }
+        }
+        __syncwarp();
+        if (there >> lane & 1) dev::mbar_arrive(&sm.share_empty[lane]);
+      } else
       for (int w = 0; w < T::NW; ++w) {
-        if (warp_blocks(nb, (w - rot) & 3) == 0) continue;
+        if (warp_blocks<T::NW>(nb, dealt<T::NW>(w, rot)) == 0) continue;
         if (!cta_wait(&sm.share_full[w], (taken >> w) & 1, sm.abort, p.err)) {
           bail();
           return;
@@ -1580,7 +1615,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // set-up that reads nothing written by earlier kernels runs before the dependency wait
   if (threadIdx.x == 0) {
-    for (int i = 0; i < T::NW * T::NR; ++i) dev::mbar_init(&sm.ring_bar[i], 1);
+    for (int i = 0; i < T::RB; ++i) dev::mbar_init(&sm.ring_bar[i], 1);
     for (int i = 0; i < T::NW; ++i) {
       dev::mbar_init(&sm.share_full[i], 1);
       dev::mbar_init(&sm.share_empty[i], 1);
@@ -1615,9 +1650,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   __syncwarp();
   const bool poisoned = __syncthreads_or(pz);
   if (warp < T::NW) {
-    if (!poisoned) {
-      if constexpr (T::I4) stream_loop_int4<D, G, W>(p, sm, w); else stream_loop<D, G, KV, W>(p, sm, w);
-    }
+    if (!poisoned) stream_loop<D, G, KV, W>(p, sm, w);
     w.drain();
   } else if (!poisoned) {
     if (warp == T::NW) Combiner<D, G, KV, W>(p, sm, lane).run();

@@ -6,12 +6,7 @@ namespace pkv {
 
 cudaError_t launch_decode_int4(int head_dim, int group, const DecodeParams& p, pkv_pool* pool, int64_t max_tasks,
                                cudaStream_t stream) {
-  switch (head_dim) {
-    case 64: return launch_decode_g<64, kKvInt4>(group, p, pool, max_tasks, stream);
-    case 128: return launch_decode_g<128, kKvInt4>(group, p, pool, max_tasks, stream);
-    case 256: return launch_decode_g<256, kKvInt4>(group, p, pool, max_tasks, stream);
-    default: return cudaErrorInvalidValue;
-  }
+  return launch_int4_shape<false>(head_dim, group, p, pool, max_tasks, stream);
 }
 
 }  // namespace pkv

@@ -1,27 +1,22 @@
 // The streaming warps' loop over a 4-bit cache.
 //
-// A block is one record (int4.cuh): K's codes, V's codes and the scales of 16 keys arrive in one bulk copy.  Blocks go in
-// pairs: both blocks' scores, one softmax step, both blocks' products.
+// A block is one record (int4.cuh): K's codes, V's codes and the scales of 16 keys arrive together.  Blocks go in
+// pairs: both blocks' scores, one softmax step, both blocks' products, in one straight line of code whose chains overlap.
 //
-//   scores   S[key][head] = sum over groups g of s_K[key][g] * (sum_{d in g} c[key][d] q[d] - 8 sum_{d in g} q[d])
-//   values   O[d][head]  += sum over keys of (c[key][d] - 8) * (w[key][head] * s_V[key][g(d)])
+//   scores   S[key][head] = sum over groups g of s_K[key][g] * sum_{d in g} code[key][d] q[d]
+//   values   O[d][head]  += sum over keys of (code[key][d] s_V[key][g(d)]) * w[key][head]
 //
-// with c the codes as they are stored, 1 .. 15 (8 more than what they stand for), which the tensor cores multiply in fp16.
 // What bounds such a loop is instructions per block, not bytes (a record is 2.3 KB at head_dim 128 and an SM's share of
-// DRAM brings one every 100 cycles), so:
-//  * Unpacking: a code masked out of its word IS an fp16 number, the subnormal c * 2^-24, and its products with q or
-//    with a weight are exact in the MMA's fp32 sums.  A pair of values costs a mask and a share of a shift: no conversion, no
-//    exponent to set, nothing to subtract.  The factor 2^24 goes into the score's scale and into the final output.
-//  * The 8: of the scores, it is the MMA's C operand, -8 sum q, summed once per task; of the values, a second MMA on
-//    the same weights with a constant A (-8 * 2^-24), so that O's sums are those of the signed codes.
-//  * Scores are scaled by group in fp32 (exact products of codes and q until then); a value's scale rides on its key's
-//    weight, one weight fragment a group.
-//  * In V's fragments every second code stays where it is in its word, 16 times as large; its output rows take that
-//    back at the end.
-// The weights of a block times its scales are rounded to fp16 (at most 2^-11 of each off).  So that this holds for scales
-// of any size, the softmax's reference is not the running maximum but 28 - e below it (in log2 units), e the exponent field
-// of the largest value scale the warp has met: weights times scales stay below 2^14 and keep 2^-24 as their smallest
-// step.  l, o and the reference m belong together, whatever m is: the combiner and the merges need nothing else.
+// DRAM brings one every 100 cycles), so the work on a code is what it can be in packed fp16: a mask under an exponent makes
+// 1024 + c or 1024 + 16 c of it (c = code + 8, as it is stored), one fused multiply-add the code itself.  Scores are
+// scaled by group in fp32, on the exact sums of 32 products.  Values are multiplied by their scales in fp16, which is exact
+// (a code times its scale is an fp16 number); halved, so that the largest does not overflow, and the output doubled at the end:
+// under scales below 2^-14 that may round a value by half of fp16's smallest number.
+// The softmax's reference moves only when a weight would pass 2^15, and then to 2^-4 of the largest: most pairs need neither
+// a reduction over the warp nor a rescaling of O.  (Weights are rounded to fp16 for the product, at most 2^-11 of each off;
+// l, o and the reference m belong together, whatever m is: the combiner and the merges need nothing else.)
+// Tried: codes as fp16 subnormals c * 2^-24, straight out of the mask, and the 8 taken away by MMAs of its own: a fifth fewer
+// instructions, but the tensor core lines such products up by their exponents and cuts off what is 2^-14 of a key's scale.
 #pragma once
 
 #include "decode.cuh"
@@ -29,14 +24,13 @@
 namespace pkv {
 
 namespace dev {
-// D = A * B + C with C apart from D.
-__device__ __forceinline__ void mma_16816_c(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1,
-                                            float c2, float c3) {
+// D = A * B.
+__device__ __forceinline__ void mma_16816_0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %11, %12, %13};"
+      "{%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
@@ -47,6 +41,8 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
 }
 __device__ __forceinline__ float2 halves(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+__device__ __forceinline__ uint32_t as_word(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 }  // namespace dev
 
 // This pass's rows of a block, `nov` of them from row r0 on, quantized from the inputs exactly as the append stores them,
@@ -100,234 +96,429 @@ __device__ __forceinline__ void write_row(const DecodeParams& p, uint32_t base, 
   }
 }
 
-template <int D, int G, bool W>
-__device__ __forceinline__ void stream_loop_int4(const DecodeParams& p, const DecodeSmem<D, G, kKvInt4>& sm,
-                                                 Streamer<D, G, kKvInt4, W>& w) {
-  using T = DecodeTraits<D, G, kKvInt4>;
+// The pair of codes in bits 0 .. 3 (lo) or 4 .. 7 (hi) of a word's halves, or half of them.
+namespace dev {
+// (x & mask) | bits, in one instruction (from the expression the compiler made two, which took 467 in place of 310 cycles a
+// block and scheduler at head_dim 128).
+__device__ __forceinline__ uint32_t masked_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
+  return r;
+}
+__device__ __forceinline__ __half2 codes_lo(uint32_t x, bool halve) {
+  const __half2 v = as_half2(masked_or(x, 0x000F000Fu, 0x64006400u));
+  return halve ? __hfma2(v, as_half2(0x38003800u), as_half2(0xE008E008u))  // (1024 + c) / 2 - 516
+               : __hadd2(v, as_half2(0xE408E408u));                        // 1024 + c - 1032
+}
+__device__ __forceinline__ __half2 codes_hi(uint32_t x, bool halve) {
+  const __half2 v = as_half2(masked_or(x, 0x00F000F0u, 0x64006400u));
+  return halve ? __hfma2(v, as_half2(0x28002800u), as_half2(0xD080D080u))   // (1024 + 16 c) / 32 - 36
+               : __hfma2(v, as_half2(0x2C002C00u), as_half2(0xD480D480u));  // (1024 + 16 c) / 16 - 72
+}
+}  // namespace dev
+
+// One step over a pair of blocks, whose records are at base[0] and base[1] in shared memory: scores, the softmax's step, values.
+// hide: bit 2u, this lane's key qh of block u is not seen, bit 2u + 1: key qh + 8.  References m, sums l, outputs o.
+template <int D>
+__device__ __forceinline__ void attend_pair(const uint32_t (&base)[2], uint32_t hide, const uint32_t (&qb)[D / 16][2], float scale,
+                                            int lane, float& m0, float& m1, float& l0, float& l1, float (&o)[D / 16][4]) {
   using R = Int4Record<D>;
   static_assert(R::VALUES == R::GROUPS * 256, "V's codes follow K's groups");
   constexpr int NG = R::GROUPS, SW = NG / 2;  // groups of a row; 32-bit words of its K or V scales
-  constexpr uint32_t kLo = 0x000F000Fu, kHi = 0x00F000F0u;
-  // -8 as the codes are scaled: 2^-24 in rows 0 .. 7 of an m-tile, 2^-20 in rows 8 .. 15
-  const uint32_t minus8[4] = {0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u};
-  const int lane = w.lane, warp = w.warp;
+  constexpr int LW = SW < 2 ? SW : 2;         // of which so many are loaded at once (more cost registers)
+  constexpr float kCap = 15.f, kTop = 4.f;    // log2 of the largest weight allowed, and of the largest after a move
   const int qh = lane >> 2;        // this lane's score rows are keys qh and qh + 8; its q column is head qh
-  const int h0 = (lane & 3) << 1;  // heads of this lane's score / output columns: h0, h0 + 1
-  int shares = 0;                  // shares this warp has handed to the combiner warp
-  float* my_o = sm.sh_o + warp * T::OV * T::SHL;
-  float2* my_ml = sm.sh_ml + warp * kHeadsTile;
-  const float scale = p.scale_log2 * 0x1p24f;
-  while (w.ok && w.cur.t >= 0) {
-    const TaskView d = w.cur;
-    w.task_start();
-    w.fill();
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // references and sums (see above)
-    uint32_t top = 0;                                          // exponent field of the largest value scale met
-    float shift = 28.f;                                        // 28 - top
-    float o[T::MT][4];
+  const int h0 = (lane & 3) << 1;  // heads of this lane's score / output columns: h0, h0 + 1; its value columns are keys h0, h0 + 1
+  // ---- scores of both blocks: S^T[16 keys x 8 heads] = K Q^T ----
+  float s[2][4];  // [block][key qh head h0, key qh h0 + 1, key qh + 8 h0, .. h0 + 1]
+  {
+    uint32_t k0[2][LW], k1[2][LW];
 #pragma unroll
-    for (int mt = 0; mt < T::MT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
-    const int low = W ? window_low(d.ctx, p.win.window) : 0;  // the window's first key
-
-    if (d.nbw > 0 && w.ok) {
-      uint32_t qb[T::KS][2];
-      w.load_q(qb);
-      // -8 sum q over each group for heads h0, h0 + 1, as the MMAs' C operand
-      float c8[NG][2];
+    for (int u = 0; u < 2; ++u) s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        float s = 0.f;
+    for (int gp = 0; gp < SW; ++gp) {
+      if (gp % LW == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = dev::halves(qb[2 * g + (i >> 1)][i & 1]);
-          s += f.x + f.y;
+        for (int u = 0; u < 2; ++u) {
+          dev::lds_words<LW>(base[u] + R::SCALES + qh * R::SCALE_ROW + gp * 4, k0[u]);
+          dev::lds_words<LW>(base[u] + R::SCALES + (qh + 8) * R::SCALE_ROW + gp * 4, k1[u]);
         }
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        c8[g][0] = __shfl_sync(0xffffffffu, s, h0 * 4) * -0x1p-21f;
-        c8[g][1] = __shfl_sync(0xffffffffu, s, h0 * 4 + 4) * -0x1p-21f;
       }
-
-      for (int j = 0; j < d.nbw && w.ok; j += 2) {
-        const int n = min(2, d.nbw - j);
-        uint32_t hide = 0;   // bit 2u: key qh of block u is not seen, bit 2u + 1: key qh + 8
-        bool wrote = false;  // rows of this pass have gone over a record
-#pragma unroll 1
-        for (int u = 0; u < n; ++u) {
-          const int bpos = w.block_pos(d, j + u);  // the block's first position
-          const int ntok = min(kBS, d.ctx - bpos);
-          // fused append: positions ov0 .. bpos + ntok - 1 of the block are this pass's tokens, whose rows come from the
-          // inputs; the block holding the token's own position writes it into the cache
-          const int ov0 = max(bpos, d.nst), nov = p.k_in != nullptr ? bpos + ntok - ov0 : 0;
-          const int64_t token0 = d.t - (d.ctx - 1 - ov0);  // the packed token of position ov0
-          const bool own = nov > 0 && d.ctx - 1 < bpos + kBS;
-          uint4 first = make_uint4(0, 0, 0, 0);
-          if (nov > 0 && lane < nov * NewRows<D>::CPT) first = NewRows<D>::load(p, lane, token0, d.g);
-          const int64_t slot = own ? __ldcg(p.slots + d.t) : -1;
-          const uint32_t base = w.wait_run(u);
-          if (!w.ok) break;
-          if (nov > 0) {
-            NewRows<D>::store(p, base, ov0 - bpos, nov, token0, d.g, lane, first);
-            if (own && slot != -1) write_row<D>(p, base, d.ctx - 1 - bpos, slot, d.g, lane);
-            wrote = true;
-          }
-          if (ntok < kBS || (W && bpos < low)) {
-            auto sees = [&](int key) { return key < ntok && (!W || bpos + key >= low || bpos + key < p.win.sinks); };
-            hide |= (sees(qh) ? 0u : 1u) << (2 * u) | (sees(qh + 8) ? 0u : 2u) << (2 * u);
-          }
+      uint32_t r[2][4];  // key qh and key qh + 8 of group 2 gp, then of group 2 gp + 1
+      float c[2][2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) dev::ldsm_x4(base[u] + gp * 512 + lane * 16, r[u]);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t ra = r[u][2 * h], rb = r[u][2 * h + 1];
+          const uint32_t a[4] = {dev::as_word(dev::codes_lo(ra, false)), dev::as_word(dev::codes_lo(rb, false)),
+                                 dev::as_word(dev::codes_hi(ra, false)), dev::as_word(dev::codes_hi(rb, false))};
+          dev::mma_16816_0(c[u][h], a, qb[4 * gp + 2 * h][0], qb[4 * gp + 2 * h][1]);
         }
-        if (!w.ok) break;
-        const uint32_t base[2] = {w.run_addr(0), w.run_addr(1)};
-
-        // ---- scores of both blocks: S^T[16 keys x 8 heads] = K Q^T ----
-        float x[2][4];  // [block][key qh head h0, key qh h0 + 1, key qh + 8 h0, .. h0 + 1]
-        __half2 vtop = __half2half2(__ushort_as_half(0));
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          x[u][0] = x[u][1] = x[u][2] = x[u][3] = -INFINITY;
-          if (u >= n) continue;
-          const uint32_t row = base[u] + R::SCALES + qh * R::SCALE_ROW;
-          uint32_t k0[SW], k1[SW], v0[SW], v1[SW];
-          dev::lds_words<SW>(row, k0);
-          dev::lds_words<SW>(row + SW * 4, v0);
-          dev::lds_words<SW>(row + 8 * R::SCALE_ROW, k1);
-          dev::lds_words<SW>(row + 8 * R::SCALE_ROW + SW * 4, v1);
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int gp = 0; gp < SW; ++gp) {
-            uint32_t r[4];  // key qh and key qh + 8 of group 2 gp, then of group 2 gp + 1
-            dev::ldsm_x4(base[u] + gp * 512 + lane * 16, r);
-            const float2 f0 = dev::halves(k0[gp]), f1 = dev::halves(k1[gp]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int g = 2 * gp + h;
-              const uint32_t ra = r[2 * h], rb = r[2 * h + 1];
-              float c[4];
-              const uint32_t a0[4] = {ra & kLo, rb & kLo, (ra >> 4) & kLo, (rb >> 4) & kLo};
-              const uint32_t a1[4] = {(ra >> 8) & kLo, (rb >> 8) & kLo, (ra >> 12) & kLo, (rb >> 12) & kLo};
-              dev::mma_16816_c(c, a0, qb[2 * g][0], qb[2 * g][1], c8[g][0], c8[g][1], c8[g][0], c8[g][1]);
-              dev::mma_16816(c, a1, qb[2 * g + 1][0], qb[2 * g + 1][1]);
-              const float fa = h ? f0.y : f0.x, fb = h ? f1.y : f1.x;
-              s[0] = fmaf(c[0], fa, s[0]);
-              s[1] = fmaf(c[1], fa, s[1]);
-              s[2] = fmaf(c[2], fb, s[2]);
-              s[3] = fmaf(c[3], fb, s[3]);
-            }
-          }
-          const bool hid0 = hide & (1u << (2 * u)), hid1 = hide & (2u << (2 * u));
-          x[u][0] = hid0 ? -INFINITY : s[0] * scale;
-          x[u][1] = hid0 ? -INFINITY : s[1] * scale;
-          x[u][2] = hid1 ? -INFINITY : s[2] * scale;
-          x[u][3] = hid1 ? -INFINITY : s[3] * scale;
-#pragma unroll
-          for (int i = 0; i < SW; ++i) {  // (what lies in unseen rows may be anything)
-            const uint32_t a = hid0 ? 0u : v0[i], b = hid1 ? 0u : v1[i];
-            vtop = __hmax2(vtop, __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b)));
-          }
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t ra = r[u][2 * h] >> 8, rb = r[u][2 * h + 1] >> 8;
+          const uint32_t a[4] = {dev::as_word(dev::codes_lo(ra, false)), dev::as_word(dev::codes_lo(rb, false)),
+                                 dev::as_word(dev::codes_hi(ra, false)), dev::as_word(dev::codes_hi(rb, false))};
+          dev::mma_16816(c[u][h], a, qb[4 * gp + 2 * h + 1][0], qb[4 * gp + 2 * h + 1][1]);
         }
-        // ---- one online-softmax step for the pair (log2 domain) ----
-        float b0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-        float b1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
 #pragma unroll
-        for (int m = 4; m < 32; m <<= 1) {
-          b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, m));
-          b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, m));
+      for (int u = 0; u < 2; ++u) {
+        const float2 f0 = dev::halves(k0[u][gp % LW]), f1 = dev::halves(k1[u][gp % LW]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float fa = h ? f0.y : f0.x, fb = h ? f1.y : f1.x;
+          s[u][0] = fmaf(c[u][h][0], fa, s[u][0]);
+          s[u][1] = fmaf(c[u][h][1], fa, s[u][1]);
+          s[u][2] = fmaf(c[u][h][2], fb, s[u][2]);
+          s[u][3] = fmaf(c[u][h][3], fb, s[u][3]);
         }
-        float r0 = m0, r1 = m1;  // the references so far, as the new shift has them
-        {
-          const uint32_t v = *reinterpret_cast<const uint32_t*>(&vtop);
-          const uint32_t e = __reduce_max_sync(0xffffffffu, max(v & 0xFFFFu, v >> 16)) >> 10;
-          if (e > top) {
-            r0 += (float)(e - top);
-            r1 += (float)(e - top);
-            shift -= (float)(e - top);
-            top = e;
-          }
-        }
-        const float n0 = fmaxf(r0, b0 - shift), n1 = fmaxf(r1, b1 - shift);
-        const float a0 = dev::ex2_approx(m0 - n0), a1 = dev::ex2_approx(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          x[u][0] = dev::ex2_approx(x[u][0] - n0);
-          x[u][1] = dev::ex2_approx(x[u][1] - n1);
-          x[u][2] = dev::ex2_approx(x[u][2] - n0);
-          x[u][3] = dev::ex2_approx(x[u][3] - n1);
-        }
-        l0 = l0 * a0 + ((x[0][0] + x[0][2]) + (x[1][0] + x[1][2]));
-        l1 = l1 * a1 + ((x[0][1] + x[0][3]) + (x[1][1] + x[1][3]));
-        if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {
-#pragma unroll
-          for (int mt = 0; mt < T::MT; ++mt) {
-            o[mt][0] *= a0;
-            o[mt][1] *= a1;
-            o[mt][2] *= a0;
-            o[mt][3] *= a1;
-          }
-        }
-        // ---- O^T[d x 8 heads] += V^T P^T for both blocks ----
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (u >= n) continue;
-          const uint32_t row = base[u] + R::SCALES + qh * R::SCALE_ROW + SW * 4;
-          uint32_t v0[SW], v1[SW];
-          dev::lds_words<SW>(row, v0);
-          dev::lds_words<SW>(row + 8 * R::SCALE_ROW, v1);
-          const bool hid0 = hide & (1u << (2 * u)), hid1 = hide & (2u << (2 * u));
-#pragma unroll
-          for (int gp = 0; gp < SW; ++gp) {
-            uint32_t r[4];  // keys 2t, 2t + 1 and keys 2t + 8, 2t + 9 at dims 4 qh .. 4 qh + 3 of group 2 gp, then of 2 gp + 1
-            dev::ldsm_x4_t(base[u] + R::VALUES + gp * 512 + lane * 16, r);
-            const float2 f0 = dev::halves(hid0 ? 0u : v0[gp]), f1 = dev::halves(hid1 ? 0u : v1[gp]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int g = 2 * gp + h;
-              const float fa = h ? f0.y : f0.x, fb = h ? f1.y : f1.x;
-              const __half2 pk0 = __floats2half2_rn(x[u][0] * fa, x[u][1] * fa);
-              const __half2 pk1 = __floats2half2_rn(x[u][2] * fb, x[u][3] * fb);
-              const uint32_t pb0 = dev::movmatrix_t(*reinterpret_cast<const uint32_t*>(&pk0));
-              const uint32_t pb1 = dev::movmatrix_t(*reinterpret_cast<const uint32_t*>(&pk1));
-              const uint32_t ra = r[2 * h], rb = r[2 * h + 1];
-              const uint32_t va[4] = {ra & kLo, ra & kHi, rb & kLo, rb & kHi};
-              const uint32_t vb[4] = {(ra >> 8) & kLo, (ra >> 8) & kHi, (rb >> 8) & kLo, (rb >> 8) & kHi};
-              dev::mma_16816(o[2 * g], va, pb0, pb1);
-              dev::mma_16816(o[2 * g + 1], vb, pb0, pb1);
-              dev::mma_16816(o[2 * g], minus8, pb0, pb1);
-              dev::mma_16816(o[2 * g + 1], minus8, pb0, pb1);
-            }
-          }
-        }
-        if (wrote) dev::fence_proxy_async_smem();  // generic writes precede the slots' next bulk copies
-        w.release_run();
-        if (n > 1) w.release_run();
-        w.prefetch_q();  // the next task's q, once the scheduler has published it
       }
     }
-    if (!w.ok) break;
+  }
+  if (hide != 0) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (hide & (1u << (2 * u))) s[u][0] = s[u][1] = -INFINITY;
+      if (hide & (2u << (2 * u))) s[u][2] = s[u][3] = -INFINITY;
+    }
+  }
+  // ---- one online-softmax step for the pair (log2 domain): the references move if some weight would pass its cap ----
+  float b0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2])) * scale;
+  float b1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3])) * scale;
+  if (__any_sync(0xffffffffu, b0 - m0 > kCap || b1 - m1 > kCap)) {
+#pragma unroll
+    for (int m = 4; m < 32; m <<= 1) {
+      b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, m));
+      b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, m));
+    }
+    const float n0 = b0 - m0 > kCap ? b0 - kTop : m0, n1 = b1 - m1 > kCap ? b1 - kTop : m1;
+    const float a0 = dev::ex2_approx(m0 - n0), a1 = dev::ex2_approx(m1 - n1);
+    m0 = n0;
+    m1 = n1;
+    l0 *= a0;
+    l1 *= a1;
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt) {
+      o[mt][0] *= a0;
+      o[mt][1] *= a1;
+      o[mt][2] *= a0;
+      o[mt][3] *= a1;
+    }
+  }
+  uint32_t pb[2][2];  // P^T as the MMAs' B operand: k = keys, n = heads
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const float p0 = dev::ex2_approx(fmaf(s[u][0], scale, -m0)), p1 = dev::ex2_approx(fmaf(s[u][1], scale, -m1));
+    const float p2 = dev::ex2_approx(fmaf(s[u][2], scale, -m0)), p3 = dev::ex2_approx(fmaf(s[u][3], scale, -m1));
+    l0 += p0 + p2;
+    l1 += p1 + p3;
+    pb[u][0] = dev::movmatrix_t(dev::as_word(__floats2half2_rn(p0, p1)));
+    pb[u][1] = dev::movmatrix_t(dev::as_word(__floats2half2_rn(p2, p3)));
+  }
+  // ---- O^T[d x 8 heads] += V^T P^T for both blocks ----
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    uint32_t v0[2][LW], v1[2][LW];  // value scales: [keys h0, h0 + 1][groups], the same for keys h0 + 8, h0 + 9
+#pragma unroll
+    for (int gp = 0; gp < SW; ++gp) {
+      if (gp % LW == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          dev::lds_words<LW>(base[u] + R::SCALES + (h0 + i) * R::SCALE_ROW + (SW + gp) * 4, v0[i]);
+          dev::lds_words<LW>(base[u] + R::SCALES + (h0 + 8 + i) * R::SCALE_ROW + (SW + gp) * 4, v1[i]);
+        }
+      }
+      uint32_t r[4];  // keys h0, h0 + 1 and keys h0 + 8, h0 + 9 at dims 4 qh .. 4 qh + 3 of group 2 gp, then of 2 gp + 1
+      dev::ldsm_x4_t(base[u] + R::VALUES + gp * 512 + lane * 16, r);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const __half2 sa = dev::as_half2(__byte_perm(v0[0][gp % LW], v0[1][gp % LW], h ? 0x7632 : 0x5410));
+        const __half2 sb = dev::as_half2(__byte_perm(v1[0][gp % LW], v1[1][gp % LW], h ? 0x7632 : 0x5410));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // dims 4 qh + 2 e (rows 0 .. 7 of the tile) and 4 qh + 2 e + 1
+          const uint32_t ra = r[2 * h] >> (8 * e), rb = r[2 * h + 1] >> (8 * e);
+          const uint32_t a[4] = {dev::as_word(__hmul2(dev::codes_lo(ra, true), sa)), dev::as_word(__hmul2(dev::codes_hi(ra, true), sa)),
+                                 dev::as_word(__hmul2(dev::codes_lo(rb, true), sb)), dev::as_word(__hmul2(dev::codes_hi(rb, true), sb))};
+          dev::mma_16816(o[4 * gp + 2 * h + e], a, pb[u][0], pb[u][1]);
+        }
+      }
+    }
+  }
+}
 
-    // ---- hand this warp's share of the split to the combiner warp ----
-    if (d.nbw > 0) {
+// ---------------------------------------------------------------------------------------------------
+// The 4-bit cache's decode kernel: one CTA per SM, the tasks, the scheduler warp and the combiner warp of the other formats,
+// and between them producer warps that copy a task's records, two blocks a stage, for the streaming warps.  A pair of blocks is
+// 4.6 KB at head_dim 128, and an SM's share of DRAM brings one every 200 cycles: with the copies issued by the streaming warps
+// themselves (as the larger blocks' are) a pair cost 700 cycles of issuing and waiting beside 1,200 of arithmetic, with
+// 16-byte copies by all lanes more.
+// ---------------------------------------------------------------------------------------------------
+
+// A task as the streaming warps see it.
+template <int D, int G, bool W>
+struct Int4Task {
+  using T = DecodeTraits<D, G, kKvInt4>;
+  int t, g, ctx, nst, base, nb;
+  typename T::Jump jump;
+  __device__ Int4Task(const DecodeParams& p, const typename T::Task& e) {
+    const int4 rec = e.rec;
+    t = rec.x;
+    g = rec.y & 0xFF;
+    ctx = rec.w;
+    base = (rec.y >> 8) * split_size<W>(p, ctx);
+    nst = e.nst;
+    nb = e.nb;
+    jump = W ? e.jump : 0;
+  }
+  __device__ __forceinline__ int pairs() const { return (nb + 1) / 2; }
+  // First position of the split's block b.
+  __device__ __forceinline__ int block_pos(int b) const {
+    const int gap = W && b >= (int)(jump & ((1u << T::JB) - 1)) ? (int)(jump >> T::JB) : 0;
+    return (base + b + gap) * kBS;
+  }
+  // Whether block b is not simply sixteen cached keys that the token sees: it has keys past the context, rows of this pass
+  // (append fused), or keys between the sinks and the window, whose first key is `low`.
+  __device__ __forceinline__ bool edge(const DecodeParams& p, int b, int low) const {
+    const int bpos = block_pos(b);
+    return bpos + kBS > ctx || (p.k_in != nullptr && bpos + kBS > nst) || (W && bpos < low && bpos + kBS > p.win.sinks);
+  }
+};
+
+// Such a block, whose record is at `base`.  Fused append: the rows of this pass's tokens in it come from the inputs, and the
+// block holding the token's own position writes that row into the cache.  Keys that are not seen: their weights will be 0, and so
+// that whatever lies there stays out, their scales too.
+template <int D, int G, bool W>
+__device__ __forceinline__ void edge_block(const DecodeParams& p, const Int4Task<D, G, W>& d, int b, uint32_t base, int low, int u,
+                                           int lane, uint32_t& hide) {
+  using R = Int4Record<D>;
+  const int bpos = d.block_pos(b);
+  const int ntok = min(kBS, d.ctx - bpos);
+  const int ov0 = max(bpos, d.nst), nov = p.k_in != nullptr ? bpos + ntok - ov0 : 0;  // this pass's rows: from position ov0 on
+  if (nov > 0) {
+    const int64_t token0 = d.t - (d.ctx - 1 - ov0);  // the packed token of position ov0
+    const int64_t slot = d.ctx - 1 < bpos + kBS ? __ldcg(p.slots + d.t) : -1;
+    uint4 first = make_uint4(0, 0, 0, 0);
+    if (lane < nov * NewRows<D>::CPT) first = NewRows<D>::load(p, lane, token0, d.g);
+    NewRows<D>::store(p, base, ov0 - bpos, nov, token0, d.g, lane, first);
+    if (slot != -1) write_row<D>(p, base, d.ctx - 1 - bpos, slot, d.g, lane);
+  }
+  if (ntok < kBS || (W && bpos < low)) {
+    auto sees = [&](int key) { return key < ntok && (!W || bpos + key >= low || bpos + key < p.win.sinks); };
+    hide |= (sees(lane >> 2) ? 0u : 1u) << (2 * u) | (sees((lane >> 2) + 8) ? 0u : 2u) << (2 * u);
+    __syncwarp();
+    for (int i = lane; i < kBS * R::GROUPS; i += 32)  // a row's scales are GROUPS words, K's and V's
+      if (!sees(i / R::GROUPS)) asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + R::SCALES + i * 4), "r"(0) : "memory");
+    __syncwarp();
+  }
+}
+
+// A producer warp: copies the pairs of the streaming warps w with w % NP == which, each into the next of that warp's own
+// stages (a stage's waits and phases are then between one producer and one streaming warp, in order), several at once, a lane
+// a record.
+template <int D, int G, bool W>
+struct Int4Producer {
+  using T = DecodeTraits<D, G, kKvInt4>;
+  using R = Int4Record<D>;
+  static constexpr int BATCH = 4;  // pairs at once
+  static_assert(T::NP == 2, "a task's pairs alternate between the producers");
+  const DecodeParams& p;
+  const DecodeSmem<D, G, kKvInt4>& sm;
+  uint64_t* full;
+  uint64_t* empty;
+  uint64_t pol;
+  int which, lane;
+  int count = 0;     // lane w: the pairs of streaming warp w in the tasks before the current one
+  int m = 0;         // the current task's own pairs copied so far (the i-th own pair is pair 2 i + parity)
+  int parity = 0;    // of the own pairs
+  int rot = 0;
+  int q_issued = 0;  // tasks whose q is copied (producer 0)
+
+  __device__ Int4Producer(const DecodeParams& p_, const DecodeSmem<D, G, kKvInt4>& sm_, int which_, int lane_)
+      : p(p_), sm(sm_), full(sm_.ring_bar), empty(sm_.ring_bar + T::NR), which(which_), lane(lane_) {
+    pol = dev::l2_policy_evict_first();
+  }
+  // The first n (up to BATCH) own pairs that are not copied yet.  False: a wait ran out, and nothing was copied.
+  __device__ bool copy(const typename T::Task& e, int n) {
+    const int j = lane >> 1, i = lane & 1, pr = 2 * (m + j) + parity;
+    const bool mine = j < n && pr < (e.nb + 1) / 2;
+    const int w = (int)((uint32_t)(pr + rot) % T::NW), c = __shfl_sync(0xffffffffu, count, w) + pr / T::NW;
+    const int slot = w * T::NRW + c % T::NRW, phase = c / T::NRW;
+    const bool got = !mine || phase == 0 || cta_wait(&empty[slot], (phase - 1) & 1, sm.abort, p.err);
+    if (!__all_sync(0xffffffffu, got)) return false;
+    const int blocks = min(2, e.nb - 2 * pr);
+    if (mine && i == 0) dev::mbar_arrive_expect_tx(&full[slot], blocks * R::BYTES);
+    __syncwarp();
+    if (mine && i < blocks)
+      dev::bulk_g2s(sm.ring + slot * T::RUN + i * R::BYTES,
+                    reinterpret_cast<const char*>(p.cache_k) + ((size_t)e.ids[2 * pr + i] * p.num_kv_heads + (e.rec.y & 0xFF)) * R::BYTES,
+                    R::BYTES, &full[slot], pol);
+    m += n;
+    return true;
+  }
+  __device__ __forceinline__ void start(const typename T::Task& e) {
+    rot = e.rot;
+    parity = (which - rot) & 1;
+  }
+  __device__ __forceinline__ int own_pairs(const typename T::Task& e) const { return max(0, ((e.nb + 1) / 2 - parity + 1) / 2); }
+  // Before the dependency wait: the first task's leading pairs, wherever nothing that the previous kernel writes can be in
+  // their blocks (positions the appended tokens never reach, or rows that are replaced from the inputs anyway).
+  __device__ void prologue() {
+    const bool got = cta_wait(&sm.qfull[0], 0, sm.abort, p.err);
+    if (!__all_sync(0xffffffffu, got)) return;
+    const typename T::Task& e = sm.queue[0];
+    if (e.rec.x < 0) return;
+    start(e);
+    if (!p.early) return;
+    const Int4Task<D, G, W> d(p, e);
+    const int own = min(own_pairs(e), T::NR / T::NP);  // (no stage twice)
+    const int last = min(4 * lane + 2 * parity + 1, e.nb - 1);
+    const bool may = lane < own && (p.k_in != nullptr || p.late_wait || d.block_pos(last) + kBS <= e.nst);
+    const int lead = __ffs(~__ballot_sync(0xffffffffu, may)) - 1;  // (all 32: -1 would need 32 own pairs ahead)
+    const int n = lead < 0 ? 32 : lead;
+    while (m < n)
+      if (!copy(e, min(BATCH, n - m))) return;
+  }
+  __device__ void run() {
+    for (int k = 0;; ++k) {
+      const bool got = cta_wait(&sm.qfull[k % T::QD], (k / T::QD) & 1, sm.abort, p.err);
+      if (!__all_sync(0xffffffffu, got)) return;
+      const typename T::Task& e = sm.queue[k % T::QD];
+      if (e.rec.x < 0) return;
+      start(e);
+      if (which == 0) {
+        if (lane == 0) {
+          dev::fence_proxy_async_smem();  // the reads of the buffer's previous q (its task is done with) precede this copy
+          dev::mbar_arrive_expect_tx(&sm.qbar[k % T::QD], T::QB);
+          dev::bulk_g2s(sm.qbuf + (k % T::QD) * T::QB, p.q + ((size_t)e.rec.x * p.num_q_heads + (size_t)(e.rec.y & 0xFF) * G) * D,
+                        T::QB, &sm.qbar[k % T::QD], pol);
+        }
+        ++q_issued;
+      }
+      const int own = own_pairs(e);
+      while (m < own)
+        if (!copy(e, min(BATCH, own - m))) return;
+      if (lane < T::NW) count += dealt_pairs(e.nb, lane, 0x7FFFFFFF);
+      m = 0;
+      __syncwarp();
+      if (lane == 0) dev::mbar_arrive(&sm.qempty[k % T::QD]);
+    }
+  }
+  // Pairs below `limit` that are dealt to streaming warp w.
+  __device__ __forceinline__ int dealt_pairs(int nb, int w, int limit) const {
+    const int first = dealt<T::NW>(w, rot), n = min((nb + 1) / 2, limit);
+    return n > first ? (n - first + T::NW - 1) / T::NW : 0;
+  }
+  // The copies must land before the CTA leaves (each wait bounded).
+  __device__ void drain() {
+    if (lane < T::NW && lane % T::NP == which) {
+      const int n = count + (m > 0 ? dealt_pairs(2 * kMaxSplitBlocksInt4, lane, 2 * m + parity) : 0);
+      for (int c = max(0, n - T::NRW); c < n; ++c) dev::mbar_wait(&full[lane * T::NRW + c % T::NRW], (c / T::NRW) & 1);
+    }
+    if (lane == 0)
+      for (int k = max(0, q_issued - T::QD); k < q_issued; ++k) dev::mbar_wait(&sm.qbar[k % T::QD], (k / T::QD) & 1);
+  }
+};
+
+// A streaming warp: of every task the pairs dealt to it, and its share to the combiner warp.
+template <int D, int G, bool W>
+__device__ __forceinline__ void stream_int4(const DecodeParams& p, const DecodeSmem<D, G, kKvInt4>& sm, int warp, int lane) {
+  using T = DecodeTraits<D, G, kKvInt4>;
+  using R = Int4Record<D>;
+  uint64_t* full = sm.ring_bar;
+  uint64_t* empty = sm.ring_bar + T::NR;
+  const uint32_t ring = dev::smem_addr(sm.ring);
+  int shares = 0;        // shares this warp has handed to the combiner warp
+  int at = 0;            // the warp's stage (of NRW) that its next pair comes in
+  uint32_t phase = 0;    // and the phase of that stage
+  float* my_o = sm.sh_o + warp * T::OV * T::SHL;
+  float2* my_ml = sm.sh_ml + warp * kHeadsTile;
+  for (int k = 0;; ++k) {
+    bool got = cta_wait(&sm.qfull[k % T::QD], (k / T::QD) & 1, sm.abort, p.err);
+    if (!__all_sync(0xffffffffu, got)) return;
+    const typename T::Task& e = sm.queue[k % T::QD];
+    if (e.rec.x < 0) return;
+    const Int4Task<D, G, W> d(p, e);
+    const int first = dealt<T::NW>(warp, e.rot);                 // the warp's pairs: first, first + NW, ...
+    const int np = d.pairs() > first ? (d.pairs() - first + T::NW - 1) / T::NW : 0;
+    int half_left = np / 2;                                      // pairs to go until the half-way signal (Scheduler)
+    if (half_left == 0 && lane == 0) dev::mbar_arrive(&sm.qmid[k % T::QD]);
+    if (np > 0) {
+      const int low = W ? window_low(d.ctx, p.win.window) : 0;  // the window's first key
+      const int b0 = 2 * (first + T::NW * lane);
+      const uint32_t edges = __ballot_sync(0xffffffffu, lane < np && (b0 + 1 >= d.nb || d.edge(p, b0, low) || d.edge(p, b0 + 1, low)));
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // references and sums
+      float o[T::MT][4];
+#pragma unroll
+      for (int mt = 0; mt < T::MT; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+
+      // q as the MMAs' B operand (k = dims, n = heads; the columns of heads G .. 7 repeat head 0).  K's fragments: lane l's
+      // word of a 32-value group is values 8t .. 8t + 7 (t = l % 4), which unpack in pairs (i, i + 4); pairs 0 and 1 are MMA k
+      // indices 2t, 2t + 1 and 2t + 8, 2t + 9 of the group's first step, pairs 2 and 3 of its second.  q takes the same
+      // order, which leaves every dot product as it is.
+      uint32_t qb[T::KS][2];
+      got = cta_wait(&sm.qbar[k % T::QD], (k / T::QD) & 1, sm.abort, p.err);
+      if (!__all_sync(0xffffffffu, got)) return;
+      const uint32_t qs = dev::smem_addr(sm.qbuf) + (k % T::QD) * T::QB + ((lane >> 2) < G ? lane >> 2 : 0) * (D * 2) + (lane & 3) * 16;
+#pragma unroll
+      for (int g = 0; g < D / 32; ++g) {
+        uint32_t x[4];
+        dev::lds_words<4>(qs + g * 64, x);
+        qb[2 * g][0] = __byte_perm(x[0], x[2], 0x5410);
+        qb[2 * g][1] = __byte_perm(x[0], x[2], 0x7632);
+        qb[2 * g + 1][0] = __byte_perm(x[1], x[3], 0x5410);
+        qb[2 * g + 1][1] = __byte_perm(x[1], x[3], 0x7632);
+      }
+
+      for (int i = 0; i < np; ++i) {
+        const int pr = first + T::NW * i, slot = warp * T::NRW + at;
+        got = cta_wait(&full[slot], phase, sm.abort, p.err);
+        if (!__all_sync(0xffffffffu, got)) return;
+        uint32_t base[2] = {ring + slot * T::RUN, ring + slot * T::RUN + R::BYTES};
+        uint32_t hide = 0;  // bit 2u: key lane / 4 of block u is not seen, bit 2u + 1: key lane / 4 + 8
+        if (edges >> i & 1) {
+          const int n = min(2, d.nb - 2 * pr);
+#pragma unroll 1
+          for (int u = 0; u < n; ++u) edge_block<D, G, W>(p, d, 2 * pr + u, u == 0 ? base[0] : base[1], low, u, lane, hide);
+          if (n < 2) {  // an odd last block is its own twin, of which nothing is seen
+            base[1] = base[0];
+            hide |= 12u;
+          }
+          dev::fence_proxy_async_smem();  // generic writes precede the stage's next bulk copy
+        }
+        attend_pair<D>(base, hide, qb, p.scale_log2, lane, m0, m1, l0, l1, o);
+        __syncwarp();  // every lane has read the stage
+        if (lane == 0) dev::mbar_arrive(&empty[slot]);
+        if (++at == T::NRW) {
+          at = 0;
+          phase ^= 1;
+        }
+        if (half_left > 0 && --half_left == 0 && lane == 0) dev::mbar_arrive(&sm.qmid[k % T::QD]);
+      }
+
+      // ---- hand this warp's share of the split to the combiner warp ----
 #pragma unroll
       for (int m = 4; m < 32; m <<= 1) {
         l0 += __shfl_xor_sync(0xffffffffu, l0, m);
         l1 += __shfl_xor_sync(0xffffffffu, l1, m);
       }
       if (shares > 0) {  // the slot is free once the combiner warp has taken the previous share
-        const bool got = cta_wait(&sm.share_empty[warp], (shares - 1) & 1, sm.abort, p.err);
-        if (!__all_sync(0xffffffffu, got)) {
-          w.ok = false;
-          break;
-        }
+        got = cta_wait(&sm.share_empty[warp], (shares - 1) & 1, sm.abort, p.err);
+        if (!__all_sync(0xffffffffu, got)) return;
       }
       const int hg = lane & 3;
       if (hg < T::LG) {
         const int ci = (lane >> 2) * T::LG + hg;
 #pragma unroll
-        for (int r = 0; r < T::OV; ++r) my_o[r * T::SHL + ci] = o[r >> 2][r & 3] * ((r & 2) ? 0x1p20f : 0x1p24f);
+        for (int mt = 0; mt < T::MT; ++mt)  // (the values were halved)
+          reinterpret_cast<float4*>(my_o)[mt * T::SHL + ci] = make_float4(2.f * o[mt][0], 2.f * o[mt][1], 2.f * o[mt][2], 2.f * o[mt][3]);
         if (lane < T::LG) {
-          my_ml[h0] = make_float2(m0, l0);
-          my_ml[h0 + 1] = make_float2(m1, l1);
+          my_ml[2 * lane] = make_float2(m0, l0);
+          my_ml[2 * lane + 1] = make_float2(m1, l1);
         }
       }
       __syncwarp();
@@ -335,8 +526,100 @@ __device__ __forceinline__ void stream_loop_int4(const DecodeParams& p, const De
       ++shares;
     }
     __syncwarp();
-    if (lane == 0) dev::mbar_arrive(&sm.qempty[w.k % T::QD]);  // done with the task's queue entry
-    w.advance();
+    if (lane == 0) dev::mbar_arrive(&sm.qempty[k % T::QD]);  // done with the task's queue entry
+  }
+}
+
+template <int D, int G, bool W>
+__global__ void __launch_bounds__(DecodeTraits<D, G, kKvInt4>::NTHREADS, 1) decode_int4_kernel(const __grid_constant__ DecodeParams p) {
+  using T = DecodeTraits<D, G, kKvInt4>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const DecodeSmem<D, G, kKvInt4> sm(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // set-up that reads nothing written by earlier kernels runs before the dependency wait
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < T::RB; ++i) dev::mbar_init(&sm.ring_bar[i], 1);
+    for (int i = 0; i < T::NW; ++i) {
+      dev::mbar_init(&sm.share_full[i], 1);
+      dev::mbar_init(&sm.share_empty[i], 1);
+    }
+    for (int i = 0; i < T::QD; ++i) {
+      dev::mbar_init(&sm.qfull[i], 1);
+      dev::mbar_init(&sm.qempty[i], T::NW + 1 + T::NP);  // the streaming warps, the combiner and the producers
+      dev::mbar_init(&sm.qmid[i], T::NW);                // the streaming warps
+    }
+    for (int i = 0; i < T::NQ; ++i) dev::mbar_init(&sm.qbar[i], 1);
+    dev::mbar_init(sm.pbar, 1);
+    *sm.abort = 0;
+    dev::fence_mbar_init();
+  }
+  __syncwarp();
+  __syncthreads();
+  // What is read before the dependency wait: see decode_kernel (decode.cuh).
+  Int4Producer<D, G, W> pr(p, sm, warp - T::NW - 2, lane);
+  Scheduler<D, G, kKvInt4, W> sch(p, sm, lane);
+  if (warp == T::NW + 1) sch.prologue();
+  if (warp > T::NW + 1) pr.prologue();
+  __syncwarp();
+  if (!p.late_wait) dev::griddep_wait();
+  dev::griddep_launch_dependents();
+  // one CTA-uniform decision (a racing error-word update must not split the CTA)
+  int pz = 0;
+  if (threadIdx.x == 0) pz = dev::pool_poisoned(p.err) ? 1 : 0;
+  __syncwarp();
+  const bool poisoned = __syncthreads_or(pz);
+  if (warp > T::NW + 1) {
+    if (!poisoned) pr.run();
+    __syncwarp();
+    pr.drain();
+  } else if (!poisoned) {
+    if (warp < T::NW) stream_int4<D, G, W>(p, sm, warp, lane);
+    else if (warp == T::NW) Combiner<D, G, kKvInt4, W>(p, sm, lane).run();
+    else sch.run();
+  }
+  // The last CTA out resets the task counter for the next launch on this plan (no fence: decode_kernel).
+  __syncwarp();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (atomicAdd(&p.hdr->done, 1) == (int)gridDim.x - 1) {
+      p.hdr->work = 0;
+      p.hdr->done = 0;
+    }
+  }
+  if (p.late_wait) dev::griddep_wait();  // complete only after the prefill kernel ahead of it
+}
+
+template <int D, int G, bool W>
+static cudaError_t launch_int4(const DecodeParams& p, pkv_pool* pool, int64_t max_tasks, cudaStream_t stream) {
+  using T = DecodeTraits<D, G, kKvInt4>;
+  const cudaError_t e = prepare_kernel(pool, decode_int4_kernel<D, G, W>, T::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(pool->num_sms, max_tasks));  // persistent: one CTA per SM
+  return launch_pdl(decode_int4_kernel<D, G, W>, dim3((unsigned)grid), dim3(T::NTHREADS), T::SMEM, stream, p);
+}
+
+template <bool W>
+static cudaError_t launch_int4_shape(int head_dim, int group, const DecodeParams& p, pkv_pool* pool, int64_t max_tasks,
+                                     cudaStream_t stream) {
+  switch (head_dim * 16 + group) {
+    case 64 * 16 + 1: return launch_int4<64, 1, W>(p, pool, max_tasks, stream);
+    case 64 * 16 + 2: return launch_int4<64, 2, W>(p, pool, max_tasks, stream);
+    case 64 * 16 + 4: return launch_int4<64, 4, W>(p, pool, max_tasks, stream);
+    case 64 * 16 + 6: return launch_int4<64, 6, W>(p, pool, max_tasks, stream);
+    case 64 * 16 + 8: return launch_int4<64, 8, W>(p, pool, max_tasks, stream);
+    case 128 * 16 + 1: return launch_int4<128, 1, W>(p, pool, max_tasks, stream);
+    case 128 * 16 + 2: return launch_int4<128, 2, W>(p, pool, max_tasks, stream);
+    case 128 * 16 + 4: return launch_int4<128, 4, W>(p, pool, max_tasks, stream);
+    case 128 * 16 + 6: return launch_int4<128, 6, W>(p, pool, max_tasks, stream);
+    case 128 * 16 + 8: return launch_int4<128, 8, W>(p, pool, max_tasks, stream);
+    case 256 * 16 + 1: return launch_int4<256, 1, W>(p, pool, max_tasks, stream);
+    case 256 * 16 + 2: return launch_int4<256, 2, W>(p, pool, max_tasks, stream);
+    case 256 * 16 + 4: return launch_int4<256, 4, W>(p, pool, max_tasks, stream);
+    case 256 * 16 + 6: return launch_int4<256, 6, W>(p, pool, max_tasks, stream);
+    case 256 * 16 + 8: return launch_int4<256, 8, W>(p, pool, max_tasks, stream);
+    default: return cudaErrorInvalidValue;
   }
 }
 

@@ -44,7 +44,7 @@ PKV_KV_F16 = 0
 PKV_KV_E4M3 = 1
 PKV_KV_INT4 = 4
 
-DEFAULT_SPLIT_BLOCKS = 32  # pkv_config.split_blocks = 0 selects this many blocks per split-K partition
+DEFAULT_SPLIT_BLOCKS = 32  # pkv_config.split_blocks = 0 selects this many blocks per split-K partition (4-bit cache: 128)
 
 _p = ctypes.c_void_p
 _i32 = ctypes.c_int32

@@ -117,7 +117,7 @@ typedef struct {
   int32_t head_dim;
   int32_t block_size;    /* tokens per block; must be 16 */
   int32_t num_blocks;    /* physical blocks per layer    */
-  int32_t split_blocks;  /* blocks per split-K partition of a decode row; 0 = library default (32) */
+  int32_t split_blocks;  /* blocks per split-K partition of a decode row, at most 32 (4-bit cache: 128); 0 = that many */
   int32_t kv_dtype;      /* PKV_KV_F16 (0), PKV_KV_E4M3 or PKV_KV_INT4 */
 } pkv_config;
 
@@ -233,8 +233,7 @@ pkv_status pkv_gather(pkv_pool* pool, int32_t layer, const int64_t* slot_mapping
  * still being computed): that many hold them all.
  *
  * 4-bit cache: attention reads the values code * s exactly; scores are scaled by group in fp32, and each softmax
- * weight is rounded to fp16 together with the value scale that it is multiplied by.  Rows with 16 or more new tokens take
- * the same fp16 shadow, with the same workspace.
+ * weight is rounded to fp16.  Rows with 16 or more new tokens take the same fp16 shadow, with the same workspace.
  *
  * Rows are there to be attended: each has a new token.  A pass with rows that have none is reported
  * (PKV_DEVERR_ROW_META) and its other rows get their results by the decode path, however long; one whose

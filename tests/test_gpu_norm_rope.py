@@ -279,5 +279,5 @@ def test_a_decode_step_of_a_model_with_norms(cuda, built, kv):
         kk, vv = ko[s].astype(np.float64), vo[s].astype(np.float64)
         want = oracle.window_attention_row(tn[b:b + 1], kk, vv, 1 << 30, 0)[0]
         a = oracle.window_attention_row(tn[b:b + 1], kk, np.abs(vv), 1 << 30, 0)[0]
-        # weights and output rounded to fp16, scores in fp32 (the 4-bit cache's tests derive the same)
+        # weights and output rounded to fp16, scores in fp32: derived in the 4-bit cache's tests
         assert (np.abs(got[b].astype(np.float64) - want) <= 2.0**-11 * 1.001 * (a + np.abs(want)) + 2.0**-13 * a + 2.0**-24).all()
