@@ -68,25 +68,6 @@ constexpr int kMaxTokens = 4;  // per CTA
 
 __device__ __forceinline__ uint4 ld16(const __half* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
-__device__ __forceinline__ void to_floats(const uint4& r, float (&x)[8]) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-    x[2 * j] = f.x;
-    x[2 * j + 1] = f.y;
-  }
-}
-__device__ __forceinline__ uint4 to_halves(const float (&x)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const __half2 h = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
-    w[j] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // One rotated pair of fp16 vectors of 8 values: pair j is (a_j, b_j).
 __device__ __forceinline__ void rotate8(uint4& a, uint4& b, const float (&c)[8], const float (&s)[8]) {
   uint32_t* pa = reinterpret_cast<uint32_t*>(&a);
@@ -117,10 +98,9 @@ __device__ __forceinline__ void rotate8_interleaved(uint4& a, uint4& b, const fl
 // for every few heads, 8192 tokens took 15 to 21 us).  The unit of the rest is an item: 16 values of a q or KV head (two
 // 16-byte chunks that hold 8 whole pairs, or 16 values past the rotated part; of a KV head the key's and the value's).
 // A thread loads its first items before it computes its angles, so that neither waits for the other.
-// With norms (NORM) a head's mean square is a sum over its items' lanes, and a thread, whose items are all the same piece
-// of some head, holds its piece of both weights from the start.  On a 4-bit cache a scale's 32 values are four 8-value
+// On a 4-bit cache a scale's 32 values are four 8-value
 // chunks of up to four items: the chunks' largest magnitudes meet in shared memory.
-template <int D, int KV, bool INTER, bool NORM>
+template <int D, int KV, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams p, const __grid_constant__ RopeTurns turns) {
   constexpr int PC = D / 16;  // items per head: a power of two within a warp
   constexpr int U = 2;        // items in flight a thread
@@ -136,20 +116,6 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
   const uint32_t per = heads * PC, items = n * per;
   dev::griddep_wait();
   dev::griddep_launch_dependents();
-  uint4 wqa, wqb, wka, wkb;
-  if constexpr (NORM) {
-    const int pc = threadIdx.x % PC;
-    const int c0 = !INTER && pc < pieces ? pc : 2 * pc, c1 = !INTER && pc < pieces ? pc + half / 8 : 2 * pc + 1;
-    wqa = wqb = wka = wkb = make_uint4(0, 0, 0, 0);
-    if (p.q_weight) {
-      wqa = ld16(p.q_weight + 8 * c0);
-      wqb = ld16(p.q_weight + 8 * c1);
-    }
-    if (p.k_weight) {
-      wka = ld16(p.k_weight + 8 * c0);
-      wkb = ld16(p.k_weight + 8 * c1);
-    }
-  }
   for (uint32_t i0 = 0; i0 < items; i0 += U * kThreads) {  // the same number of rounds in every thread
     uint4 a[U], b[U], va[U], vb[U];
     int64_t slot[U];
@@ -207,39 +173,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
           sn[2 * j + 1] = x.w;
         }
       }
-      if constexpr (NORM) {
-        float xa[8], xb[8], sum = 0.f;
-        to_floats(a[u], xa);
-        to_floats(b[u], xb);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], sum));
-#pragma unroll
-        for (int o = 1; o < PC; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);  // every lane of the warp is here
-        if (g < 0 ? p.q_weight != nullptr : p.k_weight != nullptr) {
-          const float r = 1.f / sqrtf(sum * (1.f / D) + p.eps);
-          float wa[8], wb[8];
-          to_floats(g < 0 ? wqa : wka, wa);
-          to_floats(g < 0 ? wqb : wkb, wb);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            xa[j] *= r * (p.weight_offset + wa[j]);
-            xb[j] *= r * (p.weight_offset + wb[j]);
-          }
-        }
-        if (rot) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            // pair j: (a_j, b_j), or side by side
-            float& x = INTER ? (j < 4 ? xa[2 * j] : xb[2 * j - 8]) : xa[j];
-            float& y = INTER ? (j < 4 ? xa[2 * j + 1] : xb[2 * j - 7]) : xb[j];
-            const float x0 = x, y0 = y;
-            x = x0 * cs[j] - y0 * sn[j];
-            y = y0 * cs[j] + x0 * sn[j];
-          }
-        }
-        a[u] = to_halves(xa);
-        b[u] = to_halves(xb);
-      } else if (in && rot) {
+      if (in && rot) {
         if constexpr (INTER) rotate8_interleaved(a[u], b[u], cs, sn); else rotate8(a[u], b[u], cs, sn);
       }
       if (in && g < 0) {
@@ -301,6 +235,253 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
   }
 }
 
+// ---- with norms ----
+
+// Pairs of 32-bit floats in one operation each.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)), "l"(reinterpret_cast<const uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ void to_floats(const uint4& r, float2 (&x)[4]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+}
+__device__ __forceinline__ uint4 to_halves(const float2 (&x)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __half2 h = __floats2half2_rn(x[j].x, x[j].y);
+    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The norms' kernel.  Its unit is a step: a warp's 32 lanes hold 512 values of a token, 16 each (the pieces of the items
+// above), of whole q heads, of whole key heads or of whole value heads, so that what a step does is the same for the warp.
+// The steps of all tokens are dealt out in equal runs, one to a warp of the whole grid; a warp goes through its run with the
+// next two steps' loads under way and the next token's position and slot at hand, computes a token's angles when it comes to it
+// (its lanes share them out) and keeps those of its piece in registers; the weights, offset added, lie in shared memory.
+// One token of 12 / 2 heads at d 128: 7.0 us, nearly all of it the launch; 8192 such tokens (67 MB): 17.2 us, what the bytes
+// take over that.  (The items above with a norm in them, all heads' weights in registers: 21.5 us at 460 instructions an item,
+// where a step's are under 200: a step has one weight and no lane of another kind, and its arithmetic is two values to an
+// instruction.)
+template <int D>
+struct NormSteps {
+  static constexpr int PC = D / 16, HP = 32 / PC;  // lanes of a head, heads of a step
+  int q, kv;                                       // steps of a token's queries, and of its keys (and of its values)
+  __host__ __device__ NormSteps(int q_heads, int kv_heads) : q((q_heads + HP - 1) / HP), kv((kv_heads + HP - 1) / HP) {}
+  __host__ __device__ int all() const { return q + 2 * kv; }
+};
+
+// CTAs per SM, 80 registers a thread.  8192 tokens took 19.7 us with four, 17.8 with five, 17.2 with six, 19.2 with eight (which
+// spill); with one step ahead instead of two 18.5 with six, 17.3 with eight; with four ahead 17.4 with four or five.
+constexpr int kNormCtas = 6;
+
+template <int D, int KV, bool INTER>
+__global__ void __launch_bounds__(kThreads, kNormCtas) norm_rope_append_kernel(const RopeParams p, const __grid_constant__ RopeTurns turns) {
+  using S = NormSteps<D>;
+  constexpr int PC = S::PC, HP = S::HP, WARPS = kThreads / 32;
+  __shared__ uint4 chunk_amax[KV == PKV_KV_INT4 ? kThreads / 2 : 1];  // [thread's head][chunk] largest magnitude
+  __shared__ uint64_t turn[D / 2];
+  __shared__ float4 weight[2][4][PC];     // q's and k's: values 4 j .. 4 j + 3 of a lane's 16 at [j][lane's piece]
+  __shared__ float4 angle[WARPS][4][PC];  // (cos, cos, sin, sin) of a piece's pairs 2 j and 2 j + 1
+  const int half = p.rot_dim / 2, pieces = p.rot_dim / 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pc = lane % PC, hl = lane / PC;
+  const bool rot = pc < pieces;
+  const int c0 = !INTER && rot ? pc : 2 * pc, c1 = !INTER && rot ? pc + half / 8 : 2 * pc + 1;  // the lane's two 8-value chunks
+  const S steps(p.num_q_heads, p.num_kv_heads);
+  const int64_t total = (int64_t)p.num_tokens * steps.all(), warps = (int64_t)gridDim.x * WARPS, me = (int64_t)blockIdx.x * WARPS + warp;
+  const int64_t begin = total * me / warps;
+  const int count = (int)(total * (me + 1) / warps - begin);
+  for (int k = threadIdx.x; k < half; k += kThreads) turn[k] = turns.turn[k];
+  dev::griddep_wait();
+  dev::griddep_launch_dependents();
+
+  struct Step {
+    int64_t t;
+    int s;
+  };
+  auto advance = [&](Step& x) {
+    if (++x.s == steps.all()) {
+      x.s = 0;
+      ++x.t;
+    }
+  };
+  auto load = [&](const Step& x, bool there, uint4& a, uint4& b) {
+    const bool q = x.s < steps.q, v = x.s >= steps.q + steps.kv;
+    const int h = (q ? x.s : v ? x.s - steps.q - steps.kv : x.s - steps.q) * HP + hl;
+    a = b = make_uint4(0, 0, 0, 0);
+    if (!there || h >= (q ? p.num_q_heads : p.num_kv_heads)) return;
+    const uint4* src = reinterpret_cast<const uint4*>((q ? p.q + x.t * p.q_stride : v ? p.v + x.t * p.v_stride : p.k + x.t * p.k_stride) +
+                                                      (int64_t)h * D);
+    a = src[c0];  // plain loads: q_out may be q
+    b = src[c1];
+  };
+  Step cur{begin / steps.all(), 0}, ahead;
+  cur.s = (int)(begin - cur.t * steps.all());
+  ahead = cur;
+  uint4 a[2], b[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    load(ahead, u < count, a[u], b[u]);
+    advance(ahead);
+  }
+  const int64_t last = p.num_tokens - 1;
+  int64_t slot = count > 0 ? __ldg(p.slots + cur.t) : -1, next_slot = -1;
+  int pos = count > 0 && half > 0 ? __ldg(p.positions + cur.t) : 0, next_pos = 0;
+  for (int i = threadIdx.x; i < 8 * PC; i += kThreads) {  // both weights, four values at a time
+    const int k = i / (4 * PC), j = i / PC % 4, pi = i % PC;
+    const __half* w = k ? p.k_weight : p.q_weight;
+    const int chunk = !INTER && pi < pieces ? pi + (j >> 1) * (half / 8) : 2 * pi + (j >> 1);
+    if (w == nullptr) continue;
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(w + 8 * chunk + 4 * (j & 1)));
+    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&x.x)), hi = __half22float2(*reinterpret_cast<const __half2*>(&x.y));
+    weight[k][j][pi] = make_float4(p.weight_offset + lo.x, p.weight_offset + lo.y, p.weight_offset + hi.x, p.weight_offset + hi.y);
+  }
+  __syncthreads();
+
+  float2 cs[4], sn[4];
+  bool fresh = true;  // the current token's angles are still to be computed
+  auto process = [&](uint4& a, uint4& b) {
+    if (fresh) {
+      fresh = false;
+      if (cur.t < last) {
+        next_slot = __ldg(p.slots + cur.t + 1);
+        if (half > 0) next_pos = __ldg(p.positions + cur.t + 1);
+      }
+      for (int k = lane; k < half; k += 32) {  // pair k: of piece k / 8, its pair k % 8
+        float s, c;
+        sincospif((float)(int32_t)(((uint64_t)(int64_t)pos * turn[k]) >> 32) * 0x1p-31f, &s, &c);
+        float* at = reinterpret_cast<float*>(&angle[warp][(k & 7) >> 1][k >> 3]) + (k & 1);
+        at[0] = c * p.out_scale;
+        at[2] = s * p.out_scale;
+      }
+      __syncwarp();
+      if (rot) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 x = angle[warp][j][pc];
+          cs[j] = make_float2(x.x, x.y);
+          sn[j] = make_float2(x.z, x.w);
+        }
+      }
+      __syncwarp();
+    }
+    const bool q = cur.s < steps.q, v = cur.s >= steps.q + steps.kv;
+    const int h = (q ? cur.s : v ? cur.s - steps.q - steps.kv : cur.s - steps.q) * HP + hl;
+    const bool in = h < (q ? p.num_q_heads : p.num_kv_heads);
+    if (!v) {
+      float2 xa[4], xb[4];
+      to_floats(a, xa);
+      to_floats(b, xb);
+      if (q ? p.q_weight != nullptr : p.k_weight != nullptr) {
+        float2 s2 = mul2(xa[0], xa[0]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) s2 = fma2(xa[j], xa[j], s2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s2 = fma2(xb[j], xb[j], s2);
+        float sum = s2.x + s2.y;
+#pragma unroll
+        for (int o = 1; o < PC; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float r = rsqrtf(fmaf(sum, 1.f / D, p.eps));  // (within 2^-22 of it)
+        const float2 r2 = make_float2(r, r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 w = weight[q ? 0 : 1][j][pc];
+          float2* x = j < 2 ? xa + 2 * j : xb + 2 * j - 4;
+          x[0] = mul2(x[0], mul2(r2, make_float2(w.x, w.y)));
+          x[1] = mul2(x[1], mul2(r2, make_float2(w.z, w.w)));
+        }
+      }
+      if (rot) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (INTER) {  // pairs 2 j and 2 j + 1 side by side
+            float2* x = j < 2 ? xa + 2 * j : xb + 2 * j - 4;
+            x[0] = make_float2(fmaf(x[0].x, cs[j].x, -(x[0].y * sn[j].x)), fmaf(x[0].y, cs[j].x, x[0].x * sn[j].x));
+            x[1] = make_float2(fmaf(x[1].x, cs[j].y, -(x[1].y * sn[j].y)), fmaf(x[1].y, cs[j].y, x[1].x * sn[j].y));
+          } else {
+            const float2 ys = mul2(xb[j], sn[j]), xs = mul2(xa[j], sn[j]);
+            xa[j] = make_float2(fmaf(xa[j].x, cs[j].x, -ys.x), fmaf(xa[j].y, cs[j].y, -ys.y));
+            xb[j] = fma2(xb[j], cs[j], xs);
+          }
+        }
+      }
+      a = to_halves(xa);
+      b = to_halves(xb);
+    }
+    if (q) {
+      if (in) {
+        uint4* dst = reinterpret_cast<uint4*>(p.q_out + (cur.t * p.num_q_heads + h) * D);
+        dst[c0] = a;
+        dst[c1] = b;
+      }
+    } else {
+      const bool valid = slot >= 0 && slot < p.num_slots, put = in && valid;
+      if (lane == 0 && cur.s == steps.q && slot != -1 && !valid) dev::set_error(p.err, PKV_DEVERR_SLOT_RANGE);
+      const int64_t rec = valid ? (slot >> 4) * p.num_kv_heads + h : 0;  // the head's block
+      const int r = (int)(slot & 15);
+      if constexpr (KV == PKV_KV_INT4) {
+        uint32_t* amax = reinterpret_cast<uint32_t*>(chunk_amax) + 2 * (threadIdx.x - pc);  // this head's chunks
+        amax[c0] = dev::f16x8_amax_bits(a);
+        amax[c1] = dev::f16x8_amax_bits(b);
+        __syncwarp();
+        const uint4 m0 = reinterpret_cast<const uint4*>(amax)[c0 >> 2], m1 = reinterpret_cast<const uint4*>(amax)[c1 >> 2];
+        __syncwarp();  // read before the next step's go over them
+        if (put) {
+          using R = Int4Record<D>;
+          const __half s0 = dev::int4_scale(max(max(m0.x, m0.y), max(m0.z, m0.w)));
+          const __half s1 = dev::int4_scale(max(max(m1.x, m1.y), max(m1.z, m1.w)));
+          unsigned char* dst = p.cache_k + rec * R::BYTES;
+          *reinterpret_cast<uint32_t*>(dst + R::code_at(v, r, c0)) = dev::int4_encode8(a, s0);
+          *reinterpret_cast<uint32_t*>(dst + R::code_at(v, r, c1)) = dev::int4_encode8(b, s1);
+          if ((c0 & 3) == 0) *reinterpret_cast<__half*>(dst + R::scale_at(v, r, c0)) = s0;
+          if ((c1 & 3) == 0) *reinterpret_cast<__half*>(dst + R::scale_at(v, r, c1)) = s1;
+        }
+      } else if constexpr (KV == PKV_KV_E4M3) {
+        const uint32_t m = dev::row_amax_bits<PC>(max(dev::f16x8_amax_bits(a), dev::f16x8_amax_bits(b)));
+        if (put) {
+          const int sb = dev::e4m3_scale_byte(m);
+          uint2* dst = reinterpret_cast<uint2*>((v ? p.cache_v : p.cache_k) + (rec * 16 + r) * D);
+          dst[c0] = dev::e4m3_encode8(a, sb);
+          dst[c1] = dev::e4m3_encode8(b, sb);
+          if (pc == 0) p.scales[rec * 32 + (v ? 16 : 0) + r] = (unsigned char)sb;
+        }
+      } else if (put) {
+        uint4* dst = reinterpret_cast<uint4*>((v ? p.cache_v : p.cache_k) + (rec * 16 + r) * (2 * D));
+        dst[c0] = a;
+        dst[c1] = b;
+      }
+    }
+    if (cur.s + 1 == steps.all()) {
+      fresh = true;
+      slot = next_slot;
+      pos = next_pos;
+    }
+    advance(cur);
+  };
+  for (int i = 0; i < count; i += 2) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (u > 0 && i + u >= count) break;
+      process(a[u], b[u]);
+      load(ahead, i + u + 2 < count, a[u], b[u]);
+      advance(ahead);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(256) positions_kernel(const int32_t* __restrict__ context_lens,
                                                         const int32_t* __restrict__ qsl, int num_seqs, int num_tokens,
                                                         int32_t* __restrict__ positions, int32_t* err) {
@@ -315,14 +496,25 @@ __global__ void __launch_bounds__(256) positions_kernel(const int32_t* __restric
   }
 }
 
-template <int D, bool NORM>
+template <int D>
 cudaError_t launch_rope(const RopeParams& p, const RopeTurns& turns, int kv_dtype, bool inter, cudaStream_t s) {
   const dim3 grid((unsigned)((p.num_tokens + p.tokens - 1) / p.tokens)), block(kThreads);
-  auto* kernel = kv_dtype == PKV_KV_INT4
-                     ? (inter ? rope_append_kernel<D, PKV_KV_INT4, true, NORM> : rope_append_kernel<D, PKV_KV_INT4, false, NORM>)
+  auto* kernel = kv_dtype == PKV_KV_INT4 ? (inter ? rope_append_kernel<D, PKV_KV_INT4, true> : rope_append_kernel<D, PKV_KV_INT4, false>)
                  : kv_dtype == PKV_KV_E4M3
-                     ? (inter ? rope_append_kernel<D, PKV_KV_E4M3, true, NORM> : rope_append_kernel<D, PKV_KV_E4M3, false, NORM>)
-                     : (inter ? rope_append_kernel<D, PKV_KV_F16, true, NORM> : rope_append_kernel<D, PKV_KV_F16, false, NORM>);
+                     ? (inter ? rope_append_kernel<D, PKV_KV_E4M3, true> : rope_append_kernel<D, PKV_KV_E4M3, false>)
+                     : (inter ? rope_append_kernel<D, PKV_KV_F16, true> : rope_append_kernel<D, PKV_KV_F16, false>);
+  return launch_pdl(kernel, grid, block, 0, s, p, turns);
+}
+
+template <int D>
+cudaError_t launch_norm(const RopeParams& p, const RopeTurns& turns, int kv_dtype, bool inter, int num_sms, cudaStream_t s) {
+  const int64_t steps = (int64_t)p.num_tokens * NormSteps<D>(p.num_q_heads, p.num_kv_heads).all();
+  const dim3 grid((unsigned)std::min<int64_t>((steps + kThreads / 32 - 1) / (kThreads / 32), (int64_t)num_sms * kNormCtas)), block(kThreads);
+  auto* kernel =
+      kv_dtype == PKV_KV_INT4 ? (inter ? norm_rope_append_kernel<D, PKV_KV_INT4, true> : norm_rope_append_kernel<D, PKV_KV_INT4, false>)
+      : kv_dtype == PKV_KV_E4M3
+          ? (inter ? norm_rope_append_kernel<D, PKV_KV_E4M3, true> : norm_rope_append_kernel<D, PKV_KV_E4M3, false>)
+          : (inter ? norm_rope_append_kernel<D, PKV_KV_F16, true> : norm_rope_append_kernel<D, PKV_KV_F16, false>);
   return launch_pdl(kernel, grid, block, 0, s, p, turns);
 }
 
@@ -493,12 +685,12 @@ static pkv_status rope_append(pkv_pool* pool, int32_t layer, const pkv_rope* rop
   const int kv = c.kv_dtype;
   const cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e =
-      norms ? (c.head_dim == 64    ? launch_rope<64, true>(p, turns, kv, inter, s)
-               : c.head_dim == 128 ? launch_rope<128, true>(p, turns, kv, inter, s)
-                                   : launch_rope<256, true>(p, turns, kv, inter, s))
-            : (c.head_dim == 64    ? launch_rope<64, false>(p, turns, kv, inter, s)
-               : c.head_dim == 128 ? launch_rope<128, false>(p, turns, kv, inter, s)
-                                   : launch_rope<256, false>(p, turns, kv, inter, s));
+      norms ? (c.head_dim == 64    ? launch_norm<64>(p, turns, kv, inter, pool->num_sms, s)
+               : c.head_dim == 128 ? launch_norm<128>(p, turns, kv, inter, pool->num_sms, s)
+                                   : launch_norm<256>(p, turns, kv, inter, pool->num_sms, s))
+            : (c.head_dim == 64    ? launch_rope<64>(p, turns, kv, inter, s)
+               : c.head_dim == 128 ? launch_rope<128>(p, turns, kv, inter, s)
+                                   : launch_rope<256>(p, turns, kv, inter, s));
   if (e != cudaSuccess) return cuda_fail(e, "rope_append launch");
   note_append(pool, layer);
   pool->last_launches = 1;
