@@ -1266,7 +1266,8 @@ struct Combiner {
   using T = DecodeTraits<D, G, KV>;
   static constexpr int NG = G * D / 4;         // groups of 4 consecutive dims of one head (the G heads)
   static constexpr int EG = (NG + 31) / 32;    // groups per lane
-  static constexpr int R = EG <= 6 ? 2 : 1;    // other splits whose loads are in flight together
+  static constexpr int CH = T::I4 && EG > 3 ? 3 : EG;  // of them merged at a time (4-bit: the warp's registers are few)
+  static constexpr int R = CH <= 6 ? 2 : 1;    // other splits whose loads are in flight together
   const DecodeParams& p;
   const DecodeSmem<D, G, KV>& sm;
   int lane;
@@ -1278,11 +1279,15 @@ struct Combiner {
   // warp's and was never written out: its o is in the staging buffer stg ([G][D] fp32), its (m, l) in mml.
   // The others are read from L2 (.cg): they were written by other CTAs during this launch.
   __device__ void merge(int tg, int nsplit, int own) {
+    for (int j0 = 0; j0 < EG; j0 += CH) merge_groups(tg, nsplit, own, j0);
+  }
+  // Its groups j0 .. j0 + CH - 1 of every lane.
+  __device__ __forceinline__ void merge_groups(int tg, int nsplit, int own, int j0) {
     const size_t sb = (size_t)tg * p.max_splits;
-    float M[EG], L[EG];
-    float4 acc[EG];
+    float M[CH], L[CH];
+    float4 acc[CH];
 #pragma unroll
-    for (int j = 0; j < EG; ++j) {
+    for (int j = 0; j < CH; ++j) {
       M[j] = -INFINITY;
       L[j] = 0.f;
       acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1293,15 +1298,15 @@ struct Combiner {
       const int n = min(R, nrem - r0);
       const bool own_in = own >= s0 && own <= s0 + n;
       const int s1 = min(nsplit, s0 + n + (own_in ? 1 : 0));
-      float4 o[R][EG];
-      float2 ml[R][EG];
+      float4 o[R][CH];
+      float2 ml[R][CH];
 #pragma unroll
       for (int u = 0; u < R; ++u) {
         if (u >= n) break;
         const int su = s0 + u + (own_in && own <= s0 + u ? 1 : 0);
 #pragma unroll
-        for (int j = 0; j < EG; ++j) {
-          const int e4 = lane + 32 * j;
+        for (int j = 0; j < CH; ++j) {
+          const int e4 = lane + 32 * (j0 + j);
           if (e4 < NG) {
             ml[u][j] = __ldcg(p.part_ml + (sb + su) * kHeadsTile + (4 * e4) / D);
             o[u][j] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (sb + su) * kHeadsTile * D) + e4);
@@ -1311,8 +1316,8 @@ struct Combiner {
       int u = 0;
       for (int s = s0; s < s1; ++s) {
 #pragma unroll
-        for (int j = 0; j < EG; ++j) {
-          const int e4 = lane + 32 * j;
+        for (int j = 0; j < CH; ++j) {
+          const int e4 = lane + 32 * (j0 + j);
           if (e4 >= NG) continue;
           float2 m;
           float4 v;
@@ -1344,8 +1349,8 @@ struct Combiner {
     }
     const int t = tg / p.num_kv_heads, g = tg % p.num_kv_heads;
 #pragma unroll
-    for (int j = 0; j < EG; ++j) {
-      const int e4 = lane + 32 * j;
+    for (int j = 0; j < CH; ++j) {
+      const int e4 = lane + 32 * (j0 + j);
       if (e4 >= NG) continue;
       const float il = 1.f / L[j];
       const __half2 lo = __floats2half2_rn(acc[j].x * il, acc[j].y * il);
@@ -1475,28 +1480,35 @@ struct Combiner {
         }
         taken ^= there;
         if (real) {
-          for (int w = 0; w < T::NW; ++w)
-            if (there >> w & 1) {
-              const float4 ml = *reinterpret_cast<const float4*>(sm.sh_ml + w * kHeadsTile + 2 * hg);
-              M0 = fmaxf(M0, ml.x);
-              M1 = fmaxf(M1, ml.z);
-            }
-          for (int w = 0; w < T::NW; ++w)
-            if (there >> w & 1) {
-              const float4 ml = *reinterpret_cast<const float4*>(sm.sh_ml + w * kHeadsTile + 2 * hg);
-              const float f0 = dev::ex2_approx(ml.x - M0), f1 = dev::ex2_approx(ml.z - M1);
-              L0 = fmaf(ml.y, f0, L0);
-              L1 = fmaf(ml.w, f1, L1);
-              const float4* so = reinterpret_cast<const float4*>(sm.sh_o + w * T::OV * T::SHL) + ci;
+          float4 ml[T::NW];
 #pragma unroll
-              for (int mt = 0; mt < T::MT; ++mt) {
-                const float4 v = so[mt * T::SHL];
-                acc[4 * mt] = fmaf(v.x, f0, acc[4 * mt]);
-                acc[4 * mt + 1] = fmaf(v.y, f1, acc[4 * mt + 1]);
-                acc[4 * mt + 2] = fmaf(v.z, f0, acc[4 * mt + 2]);
-                acc[4 * mt + 3] = fmaf(v.w, f1, acc[4 * mt + 3]);
-              }
+          for (int w = 0; w < T::NW; ++w) {
+            ml[w] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+            if (there >> w & 1) ml[w] = *reinterpret_cast<const float4*>(sm.sh_ml + w * kHeadsTile + 2 * hg);
+            M0 = fmaxf(M0, ml[w].x);
+            M1 = fmaxf(M1, ml[w].z);
+          }
+#pragma unroll
+          for (int w = 0; w < T::NW; ++w) {
+            ml[w].x = dev::ex2_approx(ml[w].x - M0);
+            ml[w].z = dev::ex2_approx(ml[w].z - M1);
+            L0 = fmaf(ml[w].y, ml[w].x, L0);
+            L1 = fmaf(ml[w].w, ml[w].z, L1);
+          }
+#pragma unroll
+          for (int w = 0; w < T::NW; ++w) {
+            if (!(there >> w & 1)) continue;
+            const float f0 = ml[w].x, f1 = ml[w].z;
+            const float4* so = reinterpret_cast<const float4*>(sm.sh_o + w * T::OV * T::SHL) + ci;
+#pragma unroll
+            for (int mt = 0; mt < T::MT; ++mt) {
+              const float4 v = so[mt * T::SHL];
+              acc[4 * mt] = fmaf(v.x, f0, acc[4 * mt]);
+              acc[4 * mt + 1] = fmaf(v.y, f1, acc[4 * mt + 1]);
+              acc[4 * mt + 2] = fmaf(v.z, f0, acc[4 * mt + 2]);
+              acc[4 * mt + 3] = fmaf(v.w, f1, acc[4 * mt + 3]);
             }
+          }
         }
         __syncwarp();
         if (there >> lane & 1) dev::mbar_arrive(&sm.share_empty[lane]);
@@ -1532,8 +1544,36 @@ struct Combiner {
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(&sm.share_empty[w]);
       }
-      // ---- stage the result in shared memory (the fragment layout is not the output layout) ----
-      if (real) {
+      // ---- stage the result in shared memory (the fragment layout is not the output layout; of the 4-bit cache's a lane's
+      // values are fours of consecutive dims, which go straight where they belong) ----
+      if constexpr (T::I4) {
+        if (real && !pre) {
+          const float i0 = 1.f / L0, i1 = 1.f / L1;
+          const size_t pidx = (size_t)tg * p.max_splits + s;
+          __half* out = p.out + ((size_t)t * p.num_q_heads + (size_t)g * G) * D;
+          float* part = m2 ? sm.stg : p.part_o + pidx * kHeadsTile * D;
+#pragma unroll
+          for (int j = 0; j < T::MT / 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int head = 2 * hg + e, at = head * D + 32 * j + 4 * (lane >> 2);
+              float4 v = make_float4(acc[8 * j + e], acc[8 * j + 2 + e], acc[8 * j + 4 + e], acc[8 * j + 6 + e]);
+              if (head >= G) continue;
+              if (nsplit == 1) {
+                const float il = e ? i1 : i0;
+                const __half2 lo = __floats2half2_rn(v.x * il, v.y * il), hi = __floats2half2_rn(v.z * il, v.w * il);
+                *reinterpret_cast<uint2*>(out + at) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+              } else {
+                *reinterpret_cast<float4*>(part + at) = v;
+              }
+            }
+          if (m2 && lane < T::LG) {
+            sm.mml[2 * lane] = make_float2(M0, L0);
+            sm.mml[2 * lane + 1] = make_float2(M1, L1);
+          }
+        }
+      } else if (real) {
         if (nsplit == 1) {
           __half* sh = reinterpret_cast<__half*>(sm.stg);
           const float i0 = 1.f / L0, i1 = 1.f / L1;
@@ -1580,12 +1620,14 @@ struct Combiner {
       __syncwarp();
       if (nsplit == 1) {
         uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)t * p.num_q_heads + (size_t)g * G) * D);
-        for (int c = lane; c < G * D / 8; c += 32) dst[c] = reinterpret_cast<const uint4*>(sm.stg)[c];
+        if constexpr (!T::I4)
+          for (int c = lane; c < G * D / 8; c += 32) dst[c] = reinterpret_cast<const uint4*>(sm.stg)[c];
       } else if (m2) {
       } else {
         const size_t pidx = (size_t)tg * p.max_splits + s;
         float4* dst = reinterpret_cast<float4*>(p.part_o + pidx * kHeadsTile * D);
-        for (int c = lane; c < G * D / 4; c += 32) dst[c] = reinterpret_cast<const float4*>(sm.stg)[c];
+        if constexpr (!T::I4)
+          for (int c = lane; c < G * D / 4; c += 32) dst[c] = reinterpret_cast<const float4*>(sm.stg)[c];
         if (real && lane < T::LG) {
           if (2 * lane < G) p.part_ml[pidx * kHeadsTile + 2 * lane] = make_float2(M0, L0);
           if (2 * lane + 1 < G) p.part_ml[pidx * kHeadsTile + 2 * lane + 1] = make_float2(M1, L1);
