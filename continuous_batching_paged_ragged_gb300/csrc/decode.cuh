@@ -37,7 +37,7 @@ struct TaskEntry {
   int4 rec;  // {token (-1: no more tasks), kv head | split << 8, row, causal context}
   int nst;   // the row's first position appended this pass
   int nb;    // blocks in the split
-  int rot;   // block i of the split (4-bit: pair of blocks i) goes to streaming warp (i + rot) % NW (a function of the row alone)
+  int rot;   // block i of the split goes to streaming warp (i + rot) % NW (a function of the row alone; 4-bit: see spread)
   Jump jump;  // windowed: split blocks ahead of the gap behind the sinks (JB bits) | row blocks in the gap << JB
   int ids[MAXB];  // the split's physical block ids
 };
@@ -283,6 +283,18 @@ __device__ __forceinline__ int dealt(int w, int rot) { return NW == 4 ? (w - rot
 // (scattered 4 KB runs): one issuing thread per CTA cannot keep HBM busy, many independent issuers per
 // SM can -- hence every streaming warp issues its own copies.
 // ---------------------------------------------------------------------------------------------------
+// 4-bit: a task's pairs of blocks go around the first of its P warps, P a function of their number: three pairs a warp at least,
+// so that a small task does not cost every warp its share (and the combiner as many to fold); the next task begins behind them.
+// Pair i is at place i % P, its warp is (place + rot) % NW; shares are folded by place, so that rot, which is whatever the tasks
+// before came to, moves no result.
+constexpr int kLeastPairs = 3;
+template <int NW>
+__device__ __forceinline__ int spread(int pairs) { return min(NW, (pairs + kLeastPairs - 1) / kLeastPairs); }
+// The pairs at a place.
+__device__ __forceinline__ int place_pairs(int pairs, int around, int place) {
+  return place < around && place < pairs ? (pairs - place + around - 1) / around : 0;
+}
+
 template <int D, int G, int KV, bool W>
 struct Streamer {
   using T = DecodeTraits<D, G, KV>;
@@ -1075,6 +1087,7 @@ struct Scheduler {
   int filled = 0;        // queue entries published so far (task sequence numbers 0 .. filled-1)
   bool ended = false;    // an end-of-work entry has been published
   int last_nb = 1 << 30; // blocks of the task published last
+  int turn = 0;     // 4-bit: the warp that the next task begins with
   int last_idx = 0;      // list index of the task published last
 
   __device__ Scheduler(const DecodeParams& p_, const DecodeSmem<D, G, KV>& sm_, int lane_) : p(p_), sm(sm_), lane(lane_) {}
@@ -1135,7 +1148,13 @@ struct Scheduler {
           }
         const int qi = rec[j].x - q0[j];  // the token's index among its row's new tokens
         nst = ctx - 1 - qi;
-        rot = (uint32_t)(qi + g + s) % T::NW;  // row-local, so the dealing (and the result) does not depend on the batch
+        if constexpr (T::I4) {
+          const int pairs = (nb + 1) / 2, around = spread<T::NW>(pairs);
+          rot = turn;
+          turn = (turn + (around == T::NW ? pairs : around)) % T::NW;
+        } else {
+          rot = (uint32_t)(qi + g + s) % T::NW;  // row-local, so the dealing (and the result) does not depend on the batch
+        }
       }
       if (lane == 0) {
         e->rec = rec[j];
@@ -1210,7 +1229,7 @@ struct Scheduler {
       const int m = filled;
       // A long list (many tasks per CTA) balances itself; there the next task is claimed as soon as the
       // previous one has been handed on, for the deepest look-ahead.
-      const bool small = last_nb <= T::EAGER || n_tasks > 4 * (int)gridDim.x;
+      const bool small = last_nb <= T::EAGER || n_tasks > (T::I4 ? 16 : 4) * (int)gridDim.x;
       // Near the end of the list (this CTA's last claim was within two grids of it), the counter is read
       // before waiting: once every task has been claimed (the counter may lag, never run ahead) the end of
       // the work is published at once, and the warps finish without waiting for a claim that can only come
@@ -1366,7 +1385,7 @@ struct Combiner {
   // buffers (stg [G][D] fp32, mml [8]) while the task streamed.  The same fold as merge, element by element,
   // in split order, so the bits do not depend on which path merged.  The fp16 result is staged over stg and
   // written out coalesced.
-  __device__ void merge_two(int tg, int own, float (&acc)[T::OV], float M0, float L0, float M1, float L1) {
+  __device__ void merge_two(int tg, int own, float (&acc)[T::I4 ? 1 : T::OV], float M0, float L0, float M1, float L1) {
     const bool real = (lane & 3) < T::LG;
     if (real) {
 #pragma unroll
@@ -1462,16 +1481,20 @@ struct Combiner {
         if (pre) dev::mbar_wait(sm.pbar, pcopies & 1);
       };
       // ---- combine the shares in warp order (a fixed order: the result does not depend on timing) ----
-      float acc[T::OV];
+      float acc[T::I4 ? 1 : T::OV];
+      if constexpr (!T::I4) {
 #pragma unroll
-      for (int r = 0; r < T::OV; ++r) acc[r] = 0.f;
+        for (int r = 0; r < T::OV; ++r) acc[r] = 0.f;
+      }
       float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
       if constexpr (T::I4) {
         // The 4-bit cache's shares are more and come sooner one after another: all of them first, then one reference for all
         // and a single pass (one by one, twelve shares took 9 us, longer than their task).
         uint32_t there = 0;
-        for (int w = 0; w < T::NW; ++w) {
-          if (dealt<T::NW>(w, rot) >= (nb + 1) / 2) continue;  // (dealt in pairs)
+        const int around = spread<T::NW>((nb + 1) / 2);
+        auto warp_at = [&](int place) { return place + rot < T::NW ? place + rot : place + rot - T::NW; };
+        for (int place = 0; place < around; ++place) {
+          const int w = warp_at(place);
           if (!cta_wait(&sm.share_full[w], (taken >> w) & 1, sm.abort, p.err)) {
             bail();
             return;
@@ -1479,35 +1502,116 @@ struct Combiner {
           there |= 1u << w;
         }
         taken ^= there;
+        // the references, sums and factors: lane 4 i + hg has the two heads of places i and i + 8 (the same tree whatever rot is)
+        float4 ml[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int place = (lane >> 2) + 8 * i;
+          ml[i] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+          if (real && place < around) ml[i] = *reinterpret_cast<const float4*>(sm.sh_ml + warp_at(place) * kHeadsTile + 2 * hg);
+        }
+        M0 = fmaxf(ml[0].x, ml[1].x);
+        M1 = fmaxf(ml[0].z, ml[1].z);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          M0 = fmaxf(M0, __shfl_xor_sync(0xffffffffu, M0, o));
+          M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, o));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int place = (lane >> 2) + 8 * i;
+          if (real && place < around) {
+            ml[i].x = dev::ex2_approx(ml[i].x - M0);
+            ml[i].z = dev::ex2_approx(ml[i].z - M1);
+            L0 = fmaf(ml[i].y, ml[i].x, L0);
+            L1 = fmaf(ml[i].w, ml[i].z, L1);
+            *reinterpret_cast<float4*>(sm.sh_ml + warp_at(place) * kHeadsTile + 2 * hg) = ml[i];
+          }
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          L0 += __shfl_xor_sync(0xffffffffu, L0, o);
+          L1 += __shfl_xor_sync(0xffffffffu, L1, o);
+        }
+        __syncwarp();
+        if (pre) {
+          const bool got = cta_wait(sm.pbar, pcopies & 1, sm.abort, p.err);
+          ++pcopies;
+          if (!__all_sync(0xffffffffu, got)) {
+            dev::mbar_wait(sm.pbar, (pcopies - 1) & 1);
+            return;
+          }
+        }
+        // The values, FG fragments at a time, two to an instruction (the warp gets about one instruction in six cycles: at
+        // 60 a share it took 4.5 us a task of twelve).  A lane's are fours of consecutive dims and go straight where they
+        // belong: the output (of a two-split token merged here with its other split, as merge does it), the split's partial,
+        // or the staging buffers.
         if (real) {
-          float4 ml[T::NW];
+          constexpr int FG = T::MT < 8 ? T::MT : 8;
+          static_assert(T::MT % FG == 0, "fragments");
+          const int h0 = 2 * hg, h1 = min(h0 + 1, G - 1);
+          float il[2] = {1.f / L0, 1.f / L1}, wo[2] = {1.f, 1.f}, wp[2] = {0.f, 0.f}, wa[2] = {0.f, 0.f};
+          if (pre) {
 #pragma unroll
-          for (int w = 0; w < T::NW; ++w) {
-            ml[w] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-            if (there >> w & 1) ml[w] = *reinterpret_cast<const float4*>(sm.sh_ml + w * kHeadsTile + 2 * hg);
-            M0 = fmaxf(M0, ml[w].x);
-            M1 = fmaxf(M1, ml[w].z);
-          }
-#pragma unroll
-          for (int w = 0; w < T::NW; ++w) {
-            ml[w].x = dev::ex2_approx(ml[w].x - M0);
-            ml[w].z = dev::ex2_approx(ml[w].z - M1);
-            L0 = fmaf(ml[w].y, ml[w].x, L0);
-            L1 = fmaf(ml[w].w, ml[w].z, L1);
-          }
-#pragma unroll
-          for (int w = 0; w < T::NW; ++w) {
-            if (!(there >> w & 1)) continue;
-            const float f0 = ml[w].x, f1 = ml[w].z;
-            const float4* so = reinterpret_cast<const float4*>(sm.sh_o + w * T::OV * T::SHL) + ci;
-#pragma unroll
-            for (int mt = 0; mt < T::MT; ++mt) {
-              const float4 v = so[mt * T::SHL];
-              acc[4 * mt] = fmaf(v.x, f0, acc[4 * mt]);
-              acc[4 * mt + 1] = fmaf(v.y, f1, acc[4 * mt + 1]);
-              acc[4 * mt + 2] = fmaf(v.z, f0, acc[4 * mt + 2]);
-              acc[4 * mt + 3] = fmaf(v.w, f1, acc[4 * mt + 3]);
+            for (int e = 0; e < 2; ++e) {
+              const float2 mo = e ? make_float2(M1, L1) : make_float2(M0, L0), mp = sm.mml[e ? h1 : h0];
+              float M = -INFINITY, L = 0.f;
+              fold_weights(M, L, s == 0 ? mo : mp, wa[e], wo[e]);
+              fold_weights(M, L, s == 0 ? mp : mo, wa[e], wp[e]);
+              il[e] = 1.f / L;
             }
+          }
+          const size_t pidx = (size_t)tg * p.max_splits + s;
+          __half* out = p.out + ((size_t)t * p.num_q_heads + (size_t)g * G) * D;
+          float* part = m2 ? sm.stg : p.part_o + pidx * kHeadsTile * D;
+#pragma unroll 1
+          for (int m0 = 0; m0 < T::MT; m0 += FG) {
+            float2 x[FG][2];
+#pragma unroll
+            for (int i = 0; i < FG; ++i) x[i][0] = x[i][1] = make_float2(0.f, 0.f);
+#pragma unroll 1
+            for (int place = 0; place < around; ++place) {
+              const int w = warp_at(place);
+              const float4 f = *reinterpret_cast<const float4*>(sm.sh_ml + w * kHeadsTile + 2 * hg);
+              const float2 f2 = make_float2(f.x, f.z);
+              const float4* so = reinterpret_cast<const float4*>(sm.sh_o + w * T::OV * T::SHL) + m0 * T::SHL + ci;
+              float4 v[FG];
+#pragma unroll
+              for (int i = 0; i < FG; ++i) v[i] = so[i * T::SHL];
+#pragma unroll
+              for (int i = 0; i < FG; ++i) {
+                x[i][0] = dev::fma2(make_float2(v[i].x, v[i].y), f2, x[i][0]);
+                x[i][1] = dev::fma2(make_float2(v[i].z, v[i].w), f2, x[i][1]);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < FG; i += 2)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int head = h0 + e, at = head * D + 16 * (m0 + i) + 4 * (lane >> 2);
+                if (head >= G) continue;
+                float4 y = e ? make_float4(x[i][0].y, x[i][1].y, x[i + 1][0].y, x[i + 1][1].y)
+                             : make_float4(x[i][0].x, x[i][1].x, x[i + 1][0].x, x[i + 1][1].x);
+                if (pre) {
+                  const float4 z = *reinterpret_cast<const float4*>(sm.stg + at);
+                  auto both = [&](float own, float other) {
+                    const float first = fold_value(0.f, 0.f, s == 0 ? own : other, wo[e]);
+                    return fold_value(first, wa[e], s == 0 ? other : own, wp[e]);
+                  };
+                  y = make_float4(both(y.x, z.x), both(y.y, z.y), both(y.z, z.z), both(y.w, z.w));
+                }
+                if (pre || nsplit == 1) {
+                  const __half2 lo = __floats2half2_rn(y.x * il[e], y.y * il[e]), hi = __floats2half2_rn(y.z * il[e], y.w * il[e]);
+                  *reinterpret_cast<uint2*>(out + at) =
+                      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                } else {
+                  *reinterpret_cast<float4*>(part + at) = y;
+                }
+              }
+          }
+          if (m2 && !pre && lane < T::LG) {
+            sm.mml[2 * lane] = make_float2(M0, L0);
+            sm.mml[2 * lane + 1] = make_float2(M1, L1);
           }
         }
         __syncwarp();
@@ -1544,36 +1648,8 @@ struct Combiner {
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(&sm.share_empty[w]);
       }
-      // ---- stage the result in shared memory (the fragment layout is not the output layout; of the 4-bit cache's a lane's
-      // values are fours of consecutive dims, which go straight where they belong) ----
-      if constexpr (T::I4) {
-        if (real && !pre) {
-          const float i0 = 1.f / L0, i1 = 1.f / L1;
-          const size_t pidx = (size_t)tg * p.max_splits + s;
-          __half* out = p.out + ((size_t)t * p.num_q_heads + (size_t)g * G) * D;
-          float* part = m2 ? sm.stg : p.part_o + pidx * kHeadsTile * D;
-#pragma unroll
-          for (int j = 0; j < T::MT / 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int head = 2 * hg + e, at = head * D + 32 * j + 4 * (lane >> 2);
-              float4 v = make_float4(acc[8 * j + e], acc[8 * j + 2 + e], acc[8 * j + 4 + e], acc[8 * j + 6 + e]);
-              if (head >= G) continue;
-              if (nsplit == 1) {
-                const float il = e ? i1 : i0;
-                const __half2 lo = __floats2half2_rn(v.x * il, v.y * il), hi = __floats2half2_rn(v.z * il, v.w * il);
-                *reinterpret_cast<uint2*>(out + at) =
-                    make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-              } else {
-                *reinterpret_cast<float4*>(part + at) = v;
-              }
-            }
-          if (m2 && lane < T::LG) {
-            sm.mml[2 * lane] = make_float2(M0, L0);
-            sm.mml[2 * lane + 1] = make_float2(M1, L1);
-          }
-        }
-      } else if (real) {
+      // ---- stage the result in shared memory (the fragment layout is not the output layout) ----
+      if constexpr (!T::I4) if (real) {
         if (nsplit == 1) {
           __half* sh = reinterpret_cast<__half*>(sm.stg);
           const float i0 = 1.f / L0, i1 = 1.f / L1;
@@ -1601,13 +1677,15 @@ struct Combiner {
       if (m2 && lane == 0) p.merge_cnt[tg] = 0;  // nobody else counts this token again in this launch
       __syncwarp();
       if (pre) {
-        const bool got = cta_wait(sm.pbar, pcopies & 1, sm.abort, p.err);
-        ++pcopies;
-        if (!__all_sync(0xffffffffu, got)) {
-          dev::mbar_wait(sm.pbar, (pcopies - 1) & 1);
-          return;
+        if constexpr (!T::I4) {
+          const bool got = cta_wait(sm.pbar, pcopies & 1, sm.abort, p.err);
+          ++pcopies;
+          if (!__all_sync(0xffffffffu, got)) {
+            dev::mbar_wait(sm.pbar, (pcopies - 1) & 1);
+            return;
+          }
+          merge_two(tg, s, acc, M0, L0, M1, L1);
         }
-        merge_two(tg, s, acc, M0, L0, M1, L1);
       } else if (m2) {
         pm_tg = tg;
         pm_ns = nsplit;

@@ -318,53 +318,61 @@ __device__ __forceinline__ void edge_block(const DecodeParams& p, const Int4Task
 }
 
 // A producer warp: copies the pairs of the streaming warps w with w % NP == which, each into the next of that warp's own
-// stages (a stage's waits and phases are then between one producer and one streaming warp, in order), several at once, a lane
-// a record.
+// stages (a stage's waits and phases are then between one producer and one streaming warp, in order).  Two lanes serve a
+// streaming warp, one for each record of its pair, and the warp's pairs of one lap around a task go out at once.
 template <int D, int G, bool W>
 struct Int4Producer {
   using T = DecodeTraits<D, G, kKvInt4>;
   using R = Int4Record<D>;
-  static constexpr int BATCH = 4;  // pairs at once
-  static_assert(T::NP == 2, "a task's pairs alternate between the producers");
+  static_assert(2 * T::NW / T::NP <= 32, "two lanes a streaming warp");
   const DecodeParams& p;
   const DecodeSmem<D, G, kKvInt4>& sm;
   uint64_t* full;
   uint64_t* empty;
   uint64_t pol;
   int which, lane;
-  int count = 0;     // lane w: the pairs of streaming warp w in the tasks before the current one
-  int m = 0;         // the current task's own pairs copied so far (the i-th own pair is pair 2 i + parity)
-  int parity = 0;    // of the own pairs
-  int rot = 0;
+  int w;             // the lane's streaming warp (at or past NW: none)
+  int at = 0;        // the warp's stage that its next pair goes to,
+  int used = 0;      // and the pairs it has had so far
+  uint32_t phase = 1;  // of the stage's emptying (the first passes at once)
+  int m = 0, lap = 0;  // of the current task's pairs the first m are copied, the lap's first is `lap`
+  int pairs = 0, around = 1, place = 0;  // the current task's (spread); the lane's place in it
   int q_issued = 0;  // tasks whose q is copied (producer 0)
 
   __device__ Int4Producer(const DecodeParams& p_, const DecodeSmem<D, G, kKvInt4>& sm_, int which_, int lane_)
-      : p(p_), sm(sm_), full(sm_.ring_bar), empty(sm_.ring_bar + T::NR), which(which_), lane(lane_) {
+      : p(p_), sm(sm_), full(sm_.ring_bar), empty(sm_.ring_bar + T::NR), which(which_), lane(lane_), w((lane_ >> 1) * T::NP + which_) {
     pol = dev::l2_policy_evict_first();
   }
-  // The first n (up to BATCH) own pairs that are not copied yet.  False: a wait ran out, and nothing was copied.
-  __device__ bool copy(const typename T::Task& e, int n) {
-    const int j = lane >> 1, i = lane & 1, pr = 2 * (m + j) + parity;
-    const bool mine = j < n && pr < (e.nb + 1) / 2;
-    const int w = (int)((uint32_t)(pr + rot) % T::NW), c = __shfl_sync(0xffffffffu, count, w) + pr / T::NW;
-    const int slot = w * T::NRW + c % T::NRW, phase = c / T::NRW;
-    const bool got = !mine || phase == 0 || cta_wait(&empty[slot], (phase - 1) & 1, sm.abort, p.err);
+  // The own among the pairs of this lap that are not copied yet and below `end`.  False: a wait ran out, and none was copied.
+  __device__ bool copy(const typename T::Task& e, int end) {
+    const int i = lane & 1, pr = lap + place;
+    const bool mine = w < T::NW && place < around && pr >= m && pr < end;
+    const int slot = w * T::NRW + at;
+    const bool got = !mine || cta_wait(&empty[slot], phase, sm.abort, p.err);
     if (!__all_sync(0xffffffffu, got)) return false;
     const int blocks = min(2, e.nb - 2 * pr);
     if (mine && i == 0) dev::mbar_arrive_expect_tx(&full[slot], blocks * R::BYTES);
     __syncwarp();
-    if (mine && i < blocks)
-      dev::bulk_g2s(sm.ring + slot * T::RUN + i * R::BYTES,
-                    reinterpret_cast<const char*>(p.cache_k) + ((size_t)e.ids[2 * pr + i] * p.num_kv_heads + (e.rec.y & 0xFF)) * R::BYTES,
-                    R::BYTES, &full[slot], pol);
-    m += n;
+    if (mine) {
+      if (i < blocks)
+        dev::bulk_g2s(sm.ring + slot * T::RUN + i * R::BYTES,
+                      reinterpret_cast<const char*>(p.cache_k) + ((size_t)e.ids[2 * pr + i] * p.num_kv_heads + (e.rec.y & 0xFF)) * R::BYTES,
+                      R::BYTES, &full[slot], pol);
+      ++used;
+      if (++at == T::NRW) {
+        at = 0;
+        phase ^= 1;
+      }
+    }
+    m = min(end, lap + around);
+    if (m == lap + around) lap = m;
     return true;
   }
   __device__ __forceinline__ void start(const typename T::Task& e) {
-    rot = e.rot;
-    parity = (which - rot) & 1;
+    pairs = (e.nb + 1) / 2;
+    around = spread<T::NW>(pairs);
+    place = dealt<T::NW>(w, e.rot);
   }
-  __device__ __forceinline__ int own_pairs(const typename T::Task& e) const { return max(0, ((e.nb + 1) / 2 - parity + 1) / 2); }
   // Before the dependency wait: the first task's leading pairs, wherever nothing that the previous kernel writes can be in
   // their blocks (positions the appended tokens never reach, or rows that are replaced from the inputs anyway).
   __device__ void prologue() {
@@ -375,13 +383,11 @@ struct Int4Producer {
     start(e);
     if (!p.early) return;
     const Int4Task<D, G, W> d(p, e);
-    const int own = min(own_pairs(e), T::NR / T::NP);  // (no stage twice)
-    const int last = min(4 * lane + 2 * parity + 1, e.nb - 1);
-    const bool may = lane < own && (p.k_in != nullptr || p.late_wait || d.block_pos(last) + kBS <= e.nst);
-    const int lead = __ffs(~__ballot_sync(0xffffffffu, may)) - 1;  // (all 32: -1 would need 32 own pairs ahead)
-    const int n = lead < 0 ? 32 : lead;
-    while (m < n)
-      if (!copy(e, min(BATCH, n - m))) return;
+    const int most = min(pairs, around * T::NRW);  // (no stage twice)
+    const bool may = lane < most && (p.k_in != nullptr || p.late_wait || d.block_pos(min(2 * lane + 1, e.nb - 1)) + kBS <= e.nst);
+    const int lead = __ffs(~__ballot_sync(0xffffffffu, may)) - 1, end = lead < 0 ? 32 : lead;
+    while (m < end)
+      if (!copy(e, end)) return;
   }
   __device__ void run() {
     for (int k = 0;; ++k) {
@@ -399,26 +405,17 @@ struct Int4Producer {
         }
         ++q_issued;
       }
-      const int own = own_pairs(e);
-      while (m < own)
-        if (!copy(e, min(BATCH, own - m))) return;
-      if (lane < T::NW) count += dealt_pairs(e.nb, lane, 0x7FFFFFFF);
-      m = 0;
+      while (m < pairs)
+        if (!copy(e, pairs)) return;
+      m = lap = 0;
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(&sm.qempty[k % T::QD]);
     }
   }
-  // Pairs below `limit` that are dealt to streaming warp w.
-  __device__ __forceinline__ int dealt_pairs(int nb, int w, int limit) const {
-    const int first = dealt<T::NW>(w, rot), n = min((nb + 1) / 2, limit);
-    return n > first ? (n - first + T::NW - 1) / T::NW : 0;
-  }
   // The copies must land before the CTA leaves (each wait bounded).
   __device__ void drain() {
-    if (lane < T::NW && lane % T::NP == which) {
-      const int n = count + (m > 0 ? dealt_pairs(2 * kMaxSplitBlocksInt4, lane, 2 * m + parity) : 0);
-      for (int c = max(0, n - T::NRW); c < n; ++c) dev::mbar_wait(&full[lane * T::NRW + c % T::NRW], (c / T::NRW) & 1);
-    }
+    if (w < T::NW && (lane & 1) == 0)
+      for (int c = max(0, used - T::NRW); c < used; ++c) dev::mbar_wait(&full[w * T::NRW + c % T::NRW], (c / T::NRW) & 1);
     if (lane == 0)
       for (int k = max(0, q_issued - T::QD); k < q_issued; ++k) dev::mbar_wait(&sm.qbar[k % T::QD], (k / T::QD) & 1);
   }
@@ -443,13 +440,14 @@ __device__ __forceinline__ void stream_int4(const DecodeParams& p, const DecodeS
     const typename T::Task& e = sm.queue[k % T::QD];
     if (e.rec.x < 0) return;
     const Int4Task<D, G, W> d(p, e);
-    const int first = dealt<T::NW>(warp, e.rot);                 // the warp's pairs: first, first + NW, ...
-    const int np = d.pairs() > first ? (d.pairs() - first + T::NW - 1) / T::NW : 0;
+    const int around = spread<T::NW>(d.pairs());
+    const int first = dealt<T::NW>(warp, e.rot);                 // the warp's pairs: first, first + around, ...
+    const int np = place_pairs(d.pairs(), around, first);
     int half_left = np / 2;                                      // pairs to go until the half-way signal (Scheduler)
     if (half_left == 0 && lane == 0) dev::mbar_arrive(&sm.qmid[k % T::QD]);
     if (np > 0) {
       const int low = W ? window_low(d.ctx, p.win.window) : 0;  // the window's first key
-      const int b0 = 2 * (first + T::NW * lane);
+      const int b0 = 2 * (first + around * lane);
       const uint32_t edges = __ballot_sync(0xffffffffu, lane < np && (b0 + 1 >= d.nb || d.edge(p, b0, low) || d.edge(p, b0 + 1, low)));
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // references and sums
       float o[T::MT][4];
@@ -475,7 +473,7 @@ __device__ __forceinline__ void stream_int4(const DecodeParams& p, const DecodeS
       }
 
       for (int i = 0; i < np; ++i) {
-        const int pr = first + T::NW * i, slot = warp * T::NRW + at;
+        const int pr = first + around * i, slot = warp * T::NRW + at;
         got = cta_wait(&full[slot], phase, sm.abort, p.err);
         if (!__all_sync(0xffffffffu, got)) return;
         uint32_t base[2] = {ring + slot * T::RUN, ring + slot * T::RUN + R::BYTES};

@@ -237,21 +237,6 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
 
 // ---- with norms ----
 
-// Pairs of 32-bit floats in one operation each.
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)), "l"(reinterpret_cast<const uint64_t&>(c)));
-  return d;
-}
 __device__ __forceinline__ void to_floats(const uint4& r, float2 (&x)[4]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -386,11 +371,11 @@ __global__ void __launch_bounds__(kThreads, kNormCtas) norm_rope_append_kernel(c
       to_floats(a, xa);
       to_floats(b, xb);
       if (q ? p.q_weight != nullptr : p.k_weight != nullptr) {
-        float2 s2 = mul2(xa[0], xa[0]);
+        float2 s2 = dev::mul2(xa[0], xa[0]);
 #pragma unroll
-        for (int j = 1; j < 4; ++j) s2 = fma2(xa[j], xa[j], s2);
+        for (int j = 1; j < 4; ++j) s2 = dev::fma2(xa[j], xa[j], s2);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s2 = fma2(xb[j], xb[j], s2);
+        for (int j = 0; j < 4; ++j) s2 = dev::fma2(xb[j], xb[j], s2);
         float sum = s2.x + s2.y;
 #pragma unroll
         for (int o = 1; o < PC; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -400,8 +385,8 @@ __global__ void __launch_bounds__(kThreads, kNormCtas) norm_rope_append_kernel(c
         for (int j = 0; j < 4; ++j) {
           const float4 w = weight[q ? 0 : 1][j][pc];
           float2* x = j < 2 ? xa + 2 * j : xb + 2 * j - 4;
-          x[0] = mul2(x[0], mul2(r2, make_float2(w.x, w.y)));
-          x[1] = mul2(x[1], mul2(r2, make_float2(w.z, w.w)));
+          x[0] = dev::mul2(x[0], dev::mul2(r2, make_float2(w.x, w.y)));
+          x[1] = dev::mul2(x[1], dev::mul2(r2, make_float2(w.z, w.w)));
         }
       }
       if (rot) {
@@ -412,9 +397,9 @@ __global__ void __launch_bounds__(kThreads, kNormCtas) norm_rope_append_kernel(c
             x[0] = make_float2(fmaf(x[0].x, cs[j].x, -(x[0].y * sn[j].x)), fmaf(x[0].y, cs[j].x, x[0].x * sn[j].x));
             x[1] = make_float2(fmaf(x[1].x, cs[j].y, -(x[1].y * sn[j].y)), fmaf(x[1].y, cs[j].y, x[1].x * sn[j].y));
           } else {
-            const float2 ys = mul2(xb[j], sn[j]), xs = mul2(xa[j], sn[j]);
+            const float2 ys = dev::mul2(xb[j], sn[j]), xs = dev::mul2(xa[j], sn[j]);
             xa[j] = make_float2(fmaf(xa[j].x, cs[j].x, -ys.x), fmaf(xa[j].y, cs[j].y, -ys.y));
-            xb[j] = fma2(xb[j], cs[j], xs);
+            xb[j] = dev::fma2(xb[j], cs[j], xs);
           }
         }
       }
