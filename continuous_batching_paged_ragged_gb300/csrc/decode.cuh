@@ -57,7 +57,7 @@ struct DecodeTraits {
   // rings).  Its blocks are a quarter of the bytes, so its tasks are more blocks (up to 128, MAXB), and what a task costs
   // beside its blocks is paid once an SM.
   static constexpr int NW = !I4 ? 4 : D != 256 ? 12 : G > 6 ? 6 : 8;
-  static constexpr int NP = I4 ? 2 : 0;
+  static constexpr int NP = I4 ? 2 : 0;            // 4-bit: producer warps
   static constexpr int MAXB = I4 ? kMaxSplitBlocksInt4 : kMaxSplitBlocks;  // blocks of a task at most
   static constexpr int JB = I4 ? 16 : 5;
   using Jump = std::conditional_t<I4, uint64_t, uint32_t>;
@@ -79,8 +79,9 @@ struct DecodeTraits {
   static constexpr int NQ = I4 ? QD : NW;          // q buffers: one a streaming warp; 4-bit: one a queue entry
   static constexpr int RW = I4 ? 1 : NW;           // rings that NR is the slots of: every streaming warp's; 4-bit: all in one
   // everything but the rings: q buffers, shares, staging, queue, the other barriers, flag, alignment slack
-  static constexpr int REST = NQ * QB + NW * OV * SHL * 4 + NW * kHeadsTile * 8 + G * D * 4 + 64 +
-                              QD * (int)sizeof(Task) + (2 * NW + NQ + 3 * QD + 1) * 8 + 8 + 16 + 1024;
+  static constexpr int STG = I4 ? 0 : G * D * 4;   // the combiner's staging buffer (4-bit: none)
+  static constexpr int REST = NQ * QB + NW * OV * SHL * 4 + NW * kHeadsTile * 8 + STG + 64 +
+                              QD * (int)sizeof(Task) + (2 * NW + NQ + 3 * QD + (I4 ? 0 : 1)) * 8 + 8 + 16 + 1024;
   static constexpr int SLOT = RUN + SCL + (I4 ? 16 : 8);  // a ring slot with its scale record and its barrier (4-bit: two)
   static constexpr int WANT = I4 ? 1 : 2;          // CTAs per SM that the rings leave room for
   static constexpr int NR_FIT = (kSmemPerSM / WANT - kSmemReservedPerCTA - REST) / (RW * SLOT);
@@ -92,12 +93,12 @@ struct DecodeTraits {
   static constexpr int OFF_SHARE = OFF_QB + NQ * QB;                 // [NW][OV][SHL] fp32 o shares
   static constexpr int OFF_SML = OFF_SHARE + NW * OV * SHL * 4;      // [NW][8] float2 (m, l) shares
   static constexpr int OFF_STG = OFF_SML + NW * kHeadsTile * 8;      // combiner staging [G][D] fp32
-  static constexpr int OFF_MML = OFF_STG + G * D * 4;                // staged split's (m, l): [8] float2
+  static constexpr int OFF_MML = OFF_STG + STG;                      // staged split's (m, l): [8] float2 (4-bit: unused)
   static constexpr int OFF_Q = OFF_MML + 64;                         // [QD] Task
   static constexpr int OFF_BAR = OFF_Q + QD * (int)sizeof(Task);
   // barriers: ring [NW][NR] (4-bit: full [NR], empty [NR]), share_full [NW], share_empty [NW], queue full [QD], queue empty
-  // [QD], q [NQ], queue half-done [QD], the combiner's partial copy
-  static constexpr int NBARS = RB + 2 * NW + NQ + 3 * QD + 1;
+  // [QD], q [NQ], queue half-done [QD], the combiner's partial copy (not 4-bit)
+  static constexpr int NBARS = RB + 2 * NW + NQ + 3 * QD + (I4 ? 0 : 1);
   static constexpr int OFF_FLAG = OFF_BAR + (NBARS * 8 + 15) / 16 * 16;  // the CTA's abort flag
   static constexpr int OFF_SCL = OFF_FLAG + 16;                      // 8-bit: [NW][NR] scale records
   static constexpr int SMEM = OFF_SCL + NW * NR * SCL + 1024;        // + slack to align the rings to 1024 bytes
@@ -108,7 +109,7 @@ struct DecodeTraits {
   static constexpr int MINB = I4 || (F8 && D == 256 && G > 6) ? 1 : (FIT < 3 ? FIT : 3);
   static_assert(D % 64 == 0 && G >= 1 && G <= kHeadsTile, "shape");
   static_assert(I4 || RUN % 1024 == 0, "swizzled boxes need 1024-byte aligned slots");
-  static_assert(!I4 || (RUN % 256 == 0 && NRW >= 2 && NW % NP == 0), "records are bulk-copy destinations; stages ahead");
+  static_assert(!I4 || (RUN % 256 == 0 && NRW >= 2 && NW <= 16), "records are bulk-copy destinations; stages ahead");
   static_assert(KS % 2 == 0 && QB % 128 == 0, "k-steps in pairs; q buffers stay 16-byte aligned");
   static_assert(OFF_Q % 16 == 0 && OFF_BAR % 8 == 0 && OFF_STG % 16 == 0 && OFF_MML % 16 == 0, "alignment");
   static_assert(NR <= RING && SMEM <= RW * NR * SLOT + REST + 64, "shared-memory budget");
@@ -1285,8 +1286,7 @@ struct Combiner {
   using T = DecodeTraits<D, G, KV>;
   static constexpr int NG = G * D / 4;         // groups of 4 consecutive dims of one head (the G heads)
   static constexpr int EG = (NG + 31) / 32;    // groups per lane
-  static constexpr int CH = T::I4 && EG > 3 ? 3 : EG;  // of them merged at a time (4-bit: the warp's registers are few)
-  static constexpr int R = CH <= 6 ? 2 : 1;    // other splits whose loads are in flight together
+  static constexpr int R = EG <= 6 ? 2 : 1;    // other splits whose loads are in flight together
   const DecodeParams& p;
   const DecodeSmem<D, G, KV>& sm;
   int lane;
@@ -1298,15 +1298,11 @@ struct Combiner {
   // warp's and was never written out: its o is in the staging buffer stg ([G][D] fp32), its (m, l) in mml.
   // The others are read from L2 (.cg): they were written by other CTAs during this launch.
   __device__ void merge(int tg, int nsplit, int own) {
-    for (int j0 = 0; j0 < EG; j0 += CH) merge_groups(tg, nsplit, own, j0);
-  }
-  // Its groups j0 .. j0 + CH - 1 of every lane.
-  __device__ __forceinline__ void merge_groups(int tg, int nsplit, int own, int j0) {
     const size_t sb = (size_t)tg * p.max_splits;
-    float M[CH], L[CH];
-    float4 acc[CH];
+    float M[EG], L[EG];
+    float4 acc[EG];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
+    for (int j = 0; j < EG; ++j) {
       M[j] = -INFINITY;
       L[j] = 0.f;
       acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1317,15 +1313,15 @@ struct Combiner {
       const int n = min(R, nrem - r0);
       const bool own_in = own >= s0 && own <= s0 + n;
       const int s1 = min(nsplit, s0 + n + (own_in ? 1 : 0));
-      float4 o[R][CH];
-      float2 ml[R][CH];
+      float4 o[R][EG];
+      float2 ml[R][EG];
 #pragma unroll
       for (int u = 0; u < R; ++u) {
         if (u >= n) break;
         const int su = s0 + u + (own_in && own <= s0 + u ? 1 : 0);
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-          const int e4 = lane + 32 * (j0 + j);
+        for (int j = 0; j < EG; ++j) {
+          const int e4 = lane + 32 * j;
           if (e4 < NG) {
             ml[u][j] = __ldcg(p.part_ml + (sb + su) * kHeadsTile + (4 * e4) / D);
             o[u][j] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (sb + su) * kHeadsTile * D) + e4);
@@ -1335,8 +1331,8 @@ struct Combiner {
       int u = 0;
       for (int s = s0; s < s1; ++s) {
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-          const int e4 = lane + 32 * (j0 + j);
+        for (int j = 0; j < EG; ++j) {
+          const int e4 = lane + 32 * j;
           if (e4 >= NG) continue;
           float2 m;
           float4 v;
@@ -1368,8 +1364,8 @@ struct Combiner {
     }
     const int t = tg / p.num_kv_heads, g = tg % p.num_kv_heads;
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int e4 = lane + 32 * (j0 + j);
+    for (int j = 0; j < EG; ++j) {
+      const int e4 = lane + 32 * j;
       if (e4 >= NG) continue;
       const float il = 1.f / L[j];
       const __half2 lo = __floats2half2_rn(acc[j].x * il, acc[j].y * il);
@@ -1385,7 +1381,7 @@ struct Combiner {
   // buffers (stg [G][D] fp32, mml [8]) while the task streamed.  The same fold as merge, element by element,
   // in split order, so the bits do not depend on which path merged.  The fp16 result is staged over stg and
   // written out coalesced.
-  __device__ void merge_two(int tg, int own, float (&acc)[T::I4 ? 1 : T::OV], float M0, float L0, float M1, float L1) {
+  __device__ void merge_two(int tg, int own, float (&acc)[T::OV], float M0, float L0, float M1, float L1) {
     const bool real = (lane & 3) < T::LG;
     if (real) {
 #pragma unroll
@@ -1481,142 +1477,10 @@ struct Combiner {
         if (pre) dev::mbar_wait(sm.pbar, pcopies & 1);
       };
       // ---- combine the shares in warp order (a fixed order: the result does not depend on timing) ----
-      float acc[T::I4 ? 1 : T::OV];
-      if constexpr (!T::I4) {
+      float acc[T::OV];
 #pragma unroll
-        for (int r = 0; r < T::OV; ++r) acc[r] = 0.f;
-      }
+      for (int r = 0; r < T::OV; ++r) acc[r] = 0.f;
       float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
-      if constexpr (T::I4) {
-        // The 4-bit cache's shares are more and come sooner one after another: all of them first, then one reference for all
-        // and a single pass (one by one, twelve shares took 9 us, longer than their task).
-        uint32_t there = 0;
-        const int around = spread<T::NW>((nb + 1) / 2);
-        auto warp_at = [&](int place) { return place + rot < T::NW ? place + rot : place + rot - T::NW; };
-        for (int place = 0; place < around; ++place) {
-          const int w = warp_at(place);
-          if (!cta_wait(&sm.share_full[w], (taken >> w) & 1, sm.abort, p.err)) {
-            bail();
-            return;
-          }
-          there |= 1u << w;
-        }
-        taken ^= there;
-        // the references, sums and factors: lane 4 i + hg has the two heads of places i and i + 8 (the same tree whatever rot is)
-        float4 ml[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int place = (lane >> 2) + 8 * i;
-          ml[i] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-          if (real && place < around) ml[i] = *reinterpret_cast<const float4*>(sm.sh_ml + warp_at(place) * kHeadsTile + 2 * hg);
-        }
-        M0 = fmaxf(ml[0].x, ml[1].x);
-        M1 = fmaxf(ml[0].z, ml[1].z);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          M0 = fmaxf(M0, __shfl_xor_sync(0xffffffffu, M0, o));
-          M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, o));
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int place = (lane >> 2) + 8 * i;
-          if (real && place < around) {
-            ml[i].x = dev::ex2_approx(ml[i].x - M0);
-            ml[i].z = dev::ex2_approx(ml[i].z - M1);
-            L0 = fmaf(ml[i].y, ml[i].x, L0);
-            L1 = fmaf(ml[i].w, ml[i].z, L1);
-            *reinterpret_cast<float4*>(sm.sh_ml + warp_at(place) * kHeadsTile + 2 * hg) = ml[i];
-          }
-        }
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          L0 += __shfl_xor_sync(0xffffffffu, L0, o);
-          L1 += __shfl_xor_sync(0xffffffffu, L1, o);
-        }
-        __syncwarp();
-        if (pre) {
-          const bool got = cta_wait(sm.pbar, pcopies & 1, sm.abort, p.err);
-          ++pcopies;
-          if (!__all_sync(0xffffffffu, got)) {
-            dev::mbar_wait(sm.pbar, (pcopies - 1) & 1);
-            return;
-          }
-        }
-        // The values, FG fragments at a time, two to an instruction (the warp gets about one instruction in six cycles: at
-        // 60 a share it took 4.5 us a task of twelve).  A lane's are fours of consecutive dims and go straight where they
-        // belong: the output (of a two-split token merged here with its other split, as merge does it), the split's partial,
-        // or the staging buffers.
-        if (real) {
-          constexpr int FG = T::MT < 8 ? T::MT : 8;
-          static_assert(T::MT % FG == 0, "fragments");
-          const int h0 = 2 * hg, h1 = min(h0 + 1, G - 1);
-          float il[2] = {1.f / L0, 1.f / L1}, wo[2] = {1.f, 1.f}, wp[2] = {0.f, 0.f}, wa[2] = {0.f, 0.f};
-          if (pre) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 mo = e ? make_float2(M1, L1) : make_float2(M0, L0), mp = sm.mml[e ? h1 : h0];
-              float M = -INFINITY, L = 0.f;
-              fold_weights(M, L, s == 0 ? mo : mp, wa[e], wo[e]);
-              fold_weights(M, L, s == 0 ? mp : mo, wa[e], wp[e]);
-              il[e] = 1.f / L;
-            }
-          }
-          const size_t pidx = (size_t)tg * p.max_splits + s;
-          __half* out = p.out + ((size_t)t * p.num_q_heads + (size_t)g * G) * D;
-          float* part = m2 ? sm.stg : p.part_o + pidx * kHeadsTile * D;
-#pragma unroll 1
-          for (int m0 = 0; m0 < T::MT; m0 += FG) {
-            float2 x[FG][2];
-#pragma unroll
-            for (int i = 0; i < FG; ++i) x[i][0] = x[i][1] = make_float2(0.f, 0.f);
-#pragma unroll 1
-            for (int place = 0; place < around; ++place) {
-              const int w = warp_at(place);
-              const float4 f = *reinterpret_cast<const float4*>(sm.sh_ml + w * kHeadsTile + 2 * hg);
-              const float2 f2 = make_float2(f.x, f.z);
-              const float4* so = reinterpret_cast<const float4*>(sm.sh_o + w * T::OV * T::SHL) + m0 * T::SHL + ci;
-              float4 v[FG];
-#pragma unroll
-              for (int i = 0; i < FG; ++i) v[i] = so[i * T::SHL];
-#pragma unroll
-              for (int i = 0; i < FG; ++i) {
-                x[i][0] = dev::fma2(make_float2(v[i].x, v[i].y), f2, x[i][0]);
-                x[i][1] = dev::fma2(make_float2(v[i].z, v[i].w), f2, x[i][1]);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < FG; i += 2)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int head = h0 + e, at = head * D + 16 * (m0 + i) + 4 * (lane >> 2);
-                if (head >= G) continue;
-                float4 y = e ? make_float4(x[i][0].y, x[i][1].y, x[i + 1][0].y, x[i + 1][1].y)
-                             : make_float4(x[i][0].x, x[i][1].x, x[i + 1][0].x, x[i + 1][1].x);
-                if (pre) {
-                  const float4 z = *reinterpret_cast<const float4*>(sm.stg + at);
-                  auto both = [&](float own, float other) {
-                    const float first = fold_value(0.f, 0.f, s == 0 ? own : other, wo[e]);
-                    return fold_value(first, wa[e], s == 0 ? other : own, wp[e]);
-                  };
-                  y = make_float4(both(y.x, z.x), both(y.y, z.y), both(y.z, z.z), both(y.w, z.w));
-                }
-                if (pre || nsplit == 1) {
-                  const __half2 lo = __floats2half2_rn(y.x * il[e], y.y * il[e]), hi = __floats2half2_rn(y.z * il[e], y.w * il[e]);
-                  *reinterpret_cast<uint2*>(out + at) =
-                      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-                } else {
-                  *reinterpret_cast<float4*>(part + at) = y;
-                }
-              }
-          }
-          if (m2 && !pre && lane < T::LG) {
-            sm.mml[2 * lane] = make_float2(M0, L0);
-            sm.mml[2 * lane + 1] = make_float2(M1, L1);
-          }
-        }
-        __syncwarp();
-        if (there >> lane & 1) dev::mbar_arrive(&sm.share_empty[lane]);
-      } else
       for (int w = 0; w < T::NW; ++w) {
         if (warp_blocks<T::NW>(nb, dealt<T::NW>(w, rot)) == 0) continue;
         if (!cta_wait(&sm.share_full[w], (taken >> w) & 1, sm.abort, p.err)) {
@@ -1649,7 +1513,7 @@ struct Combiner {
         if (lane == 0) dev::mbar_arrive(&sm.share_empty[w]);
       }
       // ---- stage the result in shared memory (the fragment layout is not the output layout) ----
-      if constexpr (!T::I4) if (real) {
+      if (real) {
         if (nsplit == 1) {
           __half* sh = reinterpret_cast<__half*>(sm.stg);
           const float i0 = 1.f / L0, i1 = 1.f / L1;
@@ -1677,15 +1541,13 @@ struct Combiner {
       if (m2 && lane == 0) p.merge_cnt[tg] = 0;  // nobody else counts this token again in this launch
       __syncwarp();
       if (pre) {
-        if constexpr (!T::I4) {
-          const bool got = cta_wait(sm.pbar, pcopies & 1, sm.abort, p.err);
-          ++pcopies;
-          if (!__all_sync(0xffffffffu, got)) {
-            dev::mbar_wait(sm.pbar, (pcopies - 1) & 1);
-            return;
-          }
-          merge_two(tg, s, acc, M0, L0, M1, L1);
+        const bool got = cta_wait(sm.pbar, pcopies & 1, sm.abort, p.err);
+        ++pcopies;
+        if (!__all_sync(0xffffffffu, got)) {
+          dev::mbar_wait(sm.pbar, (pcopies - 1) & 1);
+          return;
         }
+        merge_two(tg, s, acc, M0, L0, M1, L1);
       } else if (m2) {
         pm_tg = tg;
         pm_ns = nsplit;
@@ -1698,14 +1560,12 @@ struct Combiner {
       __syncwarp();
       if (nsplit == 1) {
         uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)t * p.num_q_heads + (size_t)g * G) * D);
-        if constexpr (!T::I4)
-          for (int c = lane; c < G * D / 8; c += 32) dst[c] = reinterpret_cast<const uint4*>(sm.stg)[c];
+        for (int c = lane; c < G * D / 8; c += 32) dst[c] = reinterpret_cast<const uint4*>(sm.stg)[c];
       } else if (m2) {
       } else {
         const size_t pidx = (size_t)tg * p.max_splits + s;
         float4* dst = reinterpret_cast<float4*>(p.part_o + pidx * kHeadsTile * D);
-        if constexpr (!T::I4)
-          for (int c = lane; c < G * D / 4; c += 32) dst[c] = reinterpret_cast<const float4*>(sm.stg)[c];
+        for (int c = lane; c < G * D / 4; c += 32) dst[c] = reinterpret_cast<const float4*>(sm.stg)[c];
         if (real && lane < T::LG) {
           if (2 * lane < G) p.part_ml[pidx * kHeadsTile + 2 * lane] = make_float2(M0, L0);
           if (2 * lane + 1 < G) p.part_ml[pidx * kHeadsTile + 2 * lane + 1] = make_float2(M1, L1);

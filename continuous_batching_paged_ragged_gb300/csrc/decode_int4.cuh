@@ -259,6 +259,21 @@ __device__ __forceinline__ void attend_pair(const uint32_t (&base)[2], uint32_t 
 // 16-byte copies by all lanes more.
 // ---------------------------------------------------------------------------------------------------
 
+// Waits for every lane's own barrier (lanes without `mine` have none): all are tested at once, and the wait proper is the whole
+// warp's on the first that is not there.  (With each lane in a wait of its own they suspend the warp one after another, long
+// after the last barrier has completed: one row of 700 tokens took 10.3 in place of 7.9 us.)  False: a wait ran out.
+__device__ __forceinline__ bool cta_wait_lanes(uint64_t* bar, uint32_t parity, bool mine, volatile int* abort, int32_t* err) {
+  const uint32_t mine_at = dev::smem_addr(bar);
+  for (;;) {
+    const uint32_t left = __ballot_sync(0xffffffffu, mine && !dev::mbar_test_wait(bar, parity));
+    if (left == 0) return true;
+    const int l = __ffs(left) - 1;
+    const uint32_t at = __shfl_sync(0xffffffffu, mine_at, l), ph = __shfl_sync(0xffffffffu, parity, l);
+    const bool got = cta_wait(reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(at)), ph, abort, err);
+    if (!__all_sync(0xffffffffu, got)) return false;
+  }
+}
+
 // A task as the streaming warps see it.
 template <int D, int G, bool W>
 struct Int4Task {
@@ -317,14 +332,13 @@ __device__ __forceinline__ void edge_block(const DecodeParams& p, const Int4Task
   }
 }
 
-// A producer warp: copies the pairs of the streaming warps w with w % NP == which, each into the next of that warp's own
-// stages (a stage's waits and phases are then between one producer and one streaming warp, in order).  Two lanes serve a
-// streaming warp, one for each record of its pair, and the warp's pairs of one lap around a task go out at once.
+// A producer warp: copies the pairs of the streaming warps w with w % NP == which into each warp's own stages, in order.  Two
+// lanes serve a streaming warp, one for each record of its pair, and the pairs of one lap around a task go out at once; the first
+// producer copies the task's q ahead of them.
 template <int D, int G, bool W>
 struct Int4Producer {
   using T = DecodeTraits<D, G, kKvInt4>;
   using R = Int4Record<D>;
-  static_assert(2 * T::NW / T::NP <= 32, "two lanes a streaming warp");
   const DecodeParams& p;
   const DecodeSmem<D, G, kKvInt4>& sm;
   uint64_t* full;
@@ -337,19 +351,18 @@ struct Int4Producer {
   uint32_t phase = 1;  // of the stage's emptying (the first passes at once)
   int m = 0, lap = 0;  // of the current task's pairs the first m are copied, the lap's first is `lap`
   int pairs = 0, around = 1, place = 0;  // the current task's (spread); the lane's place in it
-  int q_issued = 0;  // tasks whose q is copied (producer 0)
+  int q_issued = 0;  // tasks whose q is copied
 
   __device__ Int4Producer(const DecodeParams& p_, const DecodeSmem<D, G, kKvInt4>& sm_, int which_, int lane_)
       : p(p_), sm(sm_), full(sm_.ring_bar), empty(sm_.ring_bar + T::NR), which(which_), lane(lane_), w((lane_ >> 1) * T::NP + which_) {
     pol = dev::l2_policy_evict_first();
   }
-  // The own among the pairs of this lap that are not copied yet and below `end`.  False: a wait ran out, and none was copied.
+  // The pairs of this lap that are not copied yet and below `end`.  False: a wait ran out, and none was copied.
   __device__ bool copy(const typename T::Task& e, int end) {
     const int i = lane & 1, pr = lap + place;
     const bool mine = w < T::NW && place < around && pr >= m && pr < end;
     const int slot = w * T::NRW + at;
-    const bool got = !mine || cta_wait(&empty[slot], phase, sm.abort, p.err);
-    if (!__all_sync(0xffffffffu, got)) return false;
+    if (!cta_wait_lanes(&empty[mine ? slot : 0], phase, mine, sm.abort, p.err)) return false;
     const int blocks = min(2, e.nb - 2 * pr);
     if (mine && i == 0) dev::mbar_arrive_expect_tx(&full[slot], blocks * R::BYTES);
     __syncwarp();
@@ -396,15 +409,13 @@ struct Int4Producer {
       const typename T::Task& e = sm.queue[k % T::QD];
       if (e.rec.x < 0) return;
       start(e);
-      if (which == 0) {
-        if (lane == 0) {
-          dev::fence_proxy_async_smem();  // the reads of the buffer's previous q (its task is done with) precede this copy
-          dev::mbar_arrive_expect_tx(&sm.qbar[k % T::QD], T::QB);
-          dev::bulk_g2s(sm.qbuf + (k % T::QD) * T::QB, p.q + ((size_t)e.rec.x * p.num_q_heads + (size_t)(e.rec.y & 0xFF) * G) * D,
-                        T::QB, &sm.qbar[k % T::QD], pol);
-        }
-        ++q_issued;
+      if (which == 0 && lane == 0) {
+        dev::fence_proxy_async_smem();  // the reads of the buffer's previous q (its task is done with) precede this copy
+        dev::mbar_arrive_expect_tx(&sm.qbar[k % T::QD], T::QB);
+        dev::bulk_g2s(sm.qbuf + (k % T::QD) * T::QB, p.q + ((size_t)e.rec.x * p.num_q_heads + (size_t)(e.rec.y & 0xFF) * G) * D,
+                      T::QB, &sm.qbar[k % T::QD], pol);
       }
+      if (which == 0) ++q_issued;
       while (m < pairs)
         if (!copy(e, pairs)) return;
       m = lap = 0;
@@ -528,6 +539,197 @@ __device__ __forceinline__ void stream_int4(const DecodeParams& p, const DecodeS
   }
 }
 
+// Merges a token whose splits are all counted: in order, with log-sum-exp weights, from L2, whichever CTA it is.
+template <int D, int G>
+__device__ __forceinline__ void merge_int4(const DecodeParams& p, int tg, int nsplit, int lane) {
+  constexpr int NG = G * D / 4;           // groups of 4 consecutive dims of one head
+  constexpr int CH = NG > 32 ? 2 : 1;     // of which a lane has so many at a time,
+  constexpr int R = 4;                    // of so many splits
+  const size_t sb = (size_t)tg * p.max_splits;
+  const int t = tg / p.num_kv_heads, g = tg % p.num_kv_heads;
+  __half* out = p.out + ((size_t)t * p.num_q_heads + (size_t)g * G) * D;
+#pragma unroll 1
+  for (int e0 = lane; e0 < NG; e0 += 32 * CH) {
+    float M[CH], L[CH];
+    float4 acc[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      M[j] = -INFINITY;
+      L[j] = 0.f;
+      acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 1
+    for (int s0 = 0; s0 < nsplit; s0 += R) {
+      float4 o[R][CH];
+      float2 ml[R][CH];
+#pragma unroll
+      for (int u = 0; u < R; ++u)
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {  // (past the last split the last again, unused; past the last group the lane's first)
+          const int e4 = e0 + 32 * j < NG ? e0 + 32 * j : e0, su = min(s0 + u, nsplit - 1);
+          ml[u][j] = __ldcg(p.part_ml + (sb + su) * kHeadsTile + (4 * e4) / D);
+          o[u][j] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (sb + su) * kHeadsTile * D) + e4);
+        }
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        if (s0 + u >= nsplit) break;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          float a, f;
+          fold_weights(M[j], L[j], ml[u][j], a, f);
+          acc[j].x = fold_value(acc[j].x, a, o[u][j].x, f);
+          acc[j].y = fold_value(acc[j].y, a, o[u][j].y, f);
+          acc[j].z = fold_value(acc[j].z, a, o[u][j].z, f);
+          acc[j].w = fold_value(acc[j].w, a, o[u][j].w, f);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      if (e0 + 32 * j >= NG) continue;
+      const float il = 1.f / L[j];
+      *reinterpret_cast<uint2*>(out + 4 * (e0 + 32 * j)) = make_uint2(dev::as_word(__floats2half2_rn(acc[j].x * il, acc[j].y * il)),
+                                                                      dev::as_word(__floats2half2_rn(acc[j].z * il, acc[j].w * il)));
+    }
+  }
+}
+
+// The combiner warp: folds a task's shares and writes the token's output or the split's partial, which it counts on the token;
+// where the count (looked at when the next task is in hand) completes the token, it merges it.
+// A warp beside streaming warps gets about one instruction in ten cycles and a spilled register costs it a trip to L2 (shared
+// memory leaves no L1): the fold keeps few registers, and nothing of a task outlives it but the count.
+template <int D, int G, bool W>
+__device__ __forceinline__ void combine_int4(const DecodeParams& p, const DecodeSmem<D, G, kKvInt4>& sm, int lane) {
+  using T = DecodeTraits<D, G, kKvInt4>;
+  uint32_t taken = 0;  // bit w: parity of the shares taken from streaming warp w so far
+  int last_tg = -1, last_ns = 0, prev = 0;  // the partial counted last, and (lane 0) the count before it
+  const int hg = lane & 3;
+  const bool real = hg < T::LG;  // this lane's fragment columns hold real heads
+  const int ci = (lane >> 2) * T::LG + hg;
+  for (int k = 0;; ++k) {
+    const bool got = cta_wait(&sm.qfull[k % T::QD], (k / T::QD) & 1, sm.abort, p.err);
+    if (!__all_sync(0xffffffffu, got)) return;
+    const typename T::Task* e = &sm.queue[k % T::QD];
+    const int4 rec = e->rec;
+    const int nb = e->nb, rot = e->rot;
+    __syncwarp();
+    if (last_tg >= 0 && __shfl_sync(0xffffffffu, prev, 0) == last_ns - 1) {
+      if (lane == 0) p.merge_cnt[last_tg] = 0;  // ready for the next launch on this plan
+      __syncwarp();
+      merge_int4<D, G>(p, last_tg, last_ns, lane);
+    }
+    last_tg = -1;
+    if (rec.x < 0) return;
+    if (lane == 0) dev::mbar_arrive(&sm.qempty[k % T::QD]);
+    const int t = rec.x, g = rec.y & 0xFF, s = rec.y >> 8, ctx = rec.w;
+    const int size = split_size<W>(p, ctx);
+    const int nsplit = (token_blocks<W>(p, ctx).n + size - 1) / size;
+    const int tg = t * p.num_kv_heads + g;
+    // ---- the shares, a lane for each (one after another, shares long there took 0.2 us apiece) ----
+    const int around = spread<T::NW>((nb + 1) / 2);
+    auto warp_at = [&](int place) { return place + rot < T::NW ? place + rot : place + rot - T::NW; };
+    const bool mine = lane < T::NW && dealt<T::NW>(lane, rot) < around;
+    if (!cta_wait_lanes(&sm.share_full[mine ? lane : 0], (taken >> lane) & 1, mine, sm.abort, p.err)) return;
+    const uint32_t there = __ballot_sync(0xffffffffu, mine);
+    taken ^= there;
+    // ---- references, sums and factors: lane 4 i + hg has the two heads of places i and i + 8 (one tree, whatever rot is) ----
+    float4 ml[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int place = (lane >> 2) + 8 * i;
+      ml[i] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+      if (real && place < around) ml[i] = *reinterpret_cast<const float4*>(sm.sh_ml + warp_at(place) * kHeadsTile + 2 * hg);
+    }
+    float M0 = fmaxf(ml[0].x, ml[1].x), M1 = fmaxf(ml[0].z, ml[1].z), L0 = 0.f, L1 = 0.f;
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      M0 = fmaxf(M0, __shfl_xor_sync(0xffffffffu, M0, o));
+      M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, o));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int place = (lane >> 2) + 8 * i;
+      if (real && place < around) {
+        ml[i].x = dev::ex2_approx(ml[i].x - M0);
+        ml[i].z = dev::ex2_approx(ml[i].z - M1);
+        L0 = fmaf(ml[i].y, ml[i].x, L0);
+        L1 = fmaf(ml[i].w, ml[i].z, L1);
+        *reinterpret_cast<float4*>(sm.sh_ml + warp_at(place) * kHeadsTile + 2 * hg) = ml[i];
+      }
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      L0 += __shfl_xor_sync(0xffffffffu, L0, o);
+      L1 += __shfl_xor_sync(0xffffffffu, L1, o);
+    }
+    __syncwarp();
+    // ---- the values, four fragments at a time, two to an instruction.  A lane's are fours of consecutive dims ----
+    if (real) {
+      constexpr int FG = 4, B = 2;
+      static_assert(T::MT % FG == 0, "fragments");
+      const float i0 = 1.f / L0, i1 = 1.f / L1;
+      const size_t pidx = (size_t)tg * p.max_splits + s;
+      __half* out = p.out + ((size_t)t * p.num_q_heads + (size_t)g * G) * D;
+      float* part = p.part_o + pidx * kHeadsTile * D;
+#pragma unroll 1
+      for (int m0 = 0; m0 < T::MT; m0 += FG) {
+        float2 x[FG][2];
+#pragma unroll
+        for (int i = 0; i < FG; ++i) x[i][0] = x[i][1] = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int first = 0; first < around; first += B) {  // past the last share the first with weight 0
+          float4 v[B][FG];
+          float2 f[B];
+#pragma unroll
+          for (int u = 0; u < B; ++u) {
+            const bool in = first + u < around;
+            const int w = warp_at(in ? first + u : 0);
+            const float4 fu = *reinterpret_cast<const float4*>(sm.sh_ml + w * kHeadsTile + 2 * hg);
+            f[u] = in ? make_float2(fu.x, fu.z) : make_float2(0.f, 0.f);
+            const float4* so = reinterpret_cast<const float4*>(sm.sh_o + w * T::OV * T::SHL) + m0 * T::SHL + ci;
+#pragma unroll
+            for (int i = 0; i < FG; ++i) v[u][i] = so[i * T::SHL];
+          }
+#pragma unroll
+          for (int u = 0; u < B; ++u)
+#pragma unroll
+            for (int i = 0; i < FG; ++i) {
+              x[i][0] = dev::fma2(make_float2(v[u][i].x, v[u][i].y), f[u], x[i][0]);
+              x[i][1] = dev::fma2(make_float2(v[u][i].z, v[u][i].w), f[u], x[i][1]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < FG; i += 2)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int head = 2 * hg + h, at = head * D + 16 * (m0 + i) + 4 * (lane >> 2);
+            if (head >= G) continue;
+            const float4 y = h ? make_float4(x[i][0].y, x[i][1].y, x[i + 1][0].y, x[i + 1][1].y)
+                               : make_float4(x[i][0].x, x[i][1].x, x[i + 1][0].x, x[i + 1][1].x);
+            if (nsplit == 1) {
+              const float il = h ? i1 : i0;
+              *reinterpret_cast<uint2*>(out + at) =
+                  make_uint2(dev::as_word(__floats2half2_rn(y.x * il, y.y * il)), dev::as_word(__floats2half2_rn(y.z * il, y.w * il)));
+            } else {
+              *reinterpret_cast<float4*>(part + at) = y;
+            }
+          }
+      }
+      if (nsplit > 1 && lane < T::LG) {
+        if (2 * lane < G) p.part_ml[pidx * kHeadsTile + 2 * lane] = make_float2(M0, L0);
+        if (2 * lane + 1 < G) p.part_ml[pidx * kHeadsTile + 2 * lane + 1] = make_float2(M1, L1);
+      }
+    }
+    __syncwarp();
+    if (there >> lane & 1) dev::mbar_arrive(&sm.share_empty[lane]);
+    if (nsplit > 1 && nsplit <= kFusedMergeSplits) {
+      last_tg = tg;
+      last_ns = nsplit;
+      if (lane == 0) prev = dev::atom_add_acq_rel_gpu(p.merge_cnt + tg, 1);  // (the warp's stores precede it)
+    }
+  }
+}
+
 template <int D, int G, bool W>
 __global__ void __launch_bounds__(DecodeTraits<D, G, kKvInt4>::NTHREADS, 1) decode_int4_kernel(const __grid_constant__ DecodeParams p) {
   using T = DecodeTraits<D, G, kKvInt4>;
@@ -535,6 +737,7 @@ __global__ void __launch_bounds__(DecodeTraits<D, G, kKvInt4>::NTHREADS, 1) deco
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const DecodeSmem<D, G, kKvInt4> sm(smem);
+  // warps: streaming 0 .. NW - 1, combiner, scheduler, producers
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // set-up that reads nothing written by earlier kernels runs before the dependency wait
   if (threadIdx.x == 0) {
@@ -546,20 +749,20 @@ __global__ void __launch_bounds__(DecodeTraits<D, G, kKvInt4>::NTHREADS, 1) deco
     for (int i = 0; i < T::QD; ++i) {
       dev::mbar_init(&sm.qfull[i], 1);
       dev::mbar_init(&sm.qempty[i], T::NW + 1 + T::NP);  // the streaming warps, the combiner and the producers
-      dev::mbar_init(&sm.qmid[i], T::NW);                // the streaming warps
+      dev::mbar_init(&sm.qmid[i], T::NW);       // the streaming warps
     }
     for (int i = 0; i < T::NQ; ++i) dev::mbar_init(&sm.qbar[i], 1);
-    dev::mbar_init(sm.pbar, 1);
     *sm.abort = 0;
     dev::fence_mbar_init();
   }
   __syncwarp();
   __syncthreads();
   // What is read before the dependency wait: see decode_kernel (decode.cuh).
+  const bool producer = warp > T::NW + 1;
   Int4Producer<D, G, W> pr(p, sm, warp - T::NW - 2, lane);
   Scheduler<D, G, kKvInt4, W> sch(p, sm, lane);
   if (warp == T::NW + 1) sch.prologue();
-  if (warp > T::NW + 1) pr.prologue();
+  if (producer) pr.prologue();
   __syncwarp();
   if (!p.late_wait) dev::griddep_wait();
   dev::griddep_launch_dependents();
@@ -568,13 +771,13 @@ __global__ void __launch_bounds__(DecodeTraits<D, G, kKvInt4>::NTHREADS, 1) deco
   if (threadIdx.x == 0) pz = dev::pool_poisoned(p.err) ? 1 : 0;
   __syncwarp();
   const bool poisoned = __syncthreads_or(pz);
-  if (warp > T::NW + 1) {
+  if (producer) {
     if (!poisoned) pr.run();
     __syncwarp();
     pr.drain();
   } else if (!poisoned) {
     if (warp < T::NW) stream_int4<D, G, W>(p, sm, warp, lane);
-    else if (warp == T::NW) Combiner<D, G, kKvInt4, W>(p, sm, lane).run();
+    else if (warp == T::NW) combine_int4<D, G, W>(p, sm, lane);
     else sch.run();
   }
   // The last CTA out resets the task counter for the next launch on this plan (no fence: decode_kernel).
