@@ -539,57 +539,78 @@ __device__ __forceinline__ void stream_int4(const DecodeParams& p, const DecodeS
   }
 }
 
-// Merges a token whose splits are all counted: in order, with log-sum-exp weights, from L2, whichever CTA it is.
+// Merges a token whose splits are all counted, from L2, whichever CTA it is: lane i has the weights of split i (at most 32), and
+// the values are summed in order, two splits' loads at a time and the first ahead of the weights.  (At the end of a launch a CTA
+// may have several of these one behind another, each 4 us when the weights came with every group of values.)
 template <int D, int G>
 __device__ __forceinline__ void merge_int4(const DecodeParams& p, int tg, int nsplit, int lane) {
-  constexpr int NG = G * D / 4;           // groups of 4 consecutive dims of one head
-  constexpr int CH = NG > 32 ? 2 : 1;     // of which a lane has so many at a time,
-  constexpr int R = 4;                    // of so many splits
+  static_assert(kFusedMergeSplits <= 32, "a lane a split");
+  constexpr int NG = G * D / 4, EG = (NG + 31) / 32;  // groups of 4 consecutive dims of one head; of them a lane's
+  constexpr int CH = EG <= 6 ? EG : 4;                // of which so many at a time
   const size_t sb = (size_t)tg * p.max_splits;
   const int t = tg / p.num_kv_heads, g = tg % p.num_kv_heads;
   __half* out = p.out + ((size_t)t * p.num_q_heads + (size_t)g * G) * D;
-#pragma unroll 1
-  for (int e0 = lane; e0 < NG; e0 += 32 * CH) {
-    float M[CH], L[CH];
-    float4 acc[CH];
+  float2 ml[G];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      M[j] = -INFINITY;
-      L[j] = 0.f;
-      acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll 1
-    for (int s0 = 0; s0 < nsplit; s0 += R) {
-      float4 o[R][CH];
-      float2 ml[R][CH];
+  for (int h = 0; h < G; ++h)
+    ml[h] = lane < nsplit ? __ldcg(p.part_ml + (sb + lane) * kHeadsTile + h) : make_float2(-INFINITY, 0.f);
+  float weight[G];
 #pragma unroll
-      for (int u = 0; u < R; ++u)
+  for (int j0 = 0; j0 < EG; j0 += CH) {
+    float4 acc[CH], o[2][CH];
+    auto load = [&](int s0) {
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {  // (past the last split the last again, unused; past the last group the lane's first)
-          const int e4 = e0 + 32 * j < NG ? e0 + 32 * j : e0, su = min(s0 + u, nsplit - 1);
-          ml[u][j] = __ldcg(p.part_ml + (sb + su) * kHeadsTile + (4 * e4) / D);
-          o[u][j] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (sb + su) * kHeadsTile * D) + e4);
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {  // (past the last split the last, past the last group the lane's first: unused)
+          const int e4 = lane + 32 * (j0 + j), s = min(s0 + u, nsplit - 1);
+          o[u][j] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (sb + s) * kHeadsTile * D) + (e4 < NG ? e4 : lane % NG));
         }
+    };
+    load(0);
+    if (j0 == 0) {
 #pragma unroll
-      for (int u = 0; u < R; ++u) {
-        if (s0 + u >= nsplit) break;
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-          float a, f;
-          fold_weights(M[j], L[j], ml[u][j], a, f);
-          acc[j].x = fold_value(acc[j].x, a, o[u][j].x, f);
-          acc[j].y = fold_value(acc[j].y, a, o[u][j].y, f);
-          acc[j].z = fold_value(acc[j].z, a, o[u][j].z, f);
-          acc[j].w = fold_value(acc[j].w, a, o[u][j].w, f);
-        }
+      for (int h = 0; h < G; ++h) {
+        float M = ml[h].x;
+        for (int i = 1; i < nsplit; i <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
+        const float f = lane < nsplit ? dev::ex2_approx(ml[h].x - M) : 0.f;
+        float L = ml[h].y * f;
+        for (int i = 1; i < nsplit; i <<= 1) L += __shfl_xor_sync(0xffffffffu, L, i);
+        weight[h] = f / L;
       }
     }
 #pragma unroll
+    for (int j = 0; j < CH; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int s0 = 0;;) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (s0 + u >= nsplit) break;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+          const int h = (j0 + j) * 128 / D, h1 = h + 1 < G ? h + 1 : h;  // the group's head (d 64: of the lower lanes)
+          if (h >= G) continue;
+          float w = __shfl_sync(0xffffffffu, weight[h], s0 + u);
+          if constexpr (D == 64) {
+            const float w1 = __shfl_sync(0xffffffffu, weight[h1], s0 + u);
+            if (lane >= 16) w = w1;
+          }
+          acc[j].x = fmaf(o[u][j].x, w, acc[j].x);
+          acc[j].y = fmaf(o[u][j].y, w, acc[j].y);
+          acc[j].z = fmaf(o[u][j].z, w, acc[j].z);
+          acc[j].w = fmaf(o[u][j].w, w, acc[j].w);
+        }
+      }
+      s0 += 2;
+      if (s0 >= nsplit) break;
+      load(s0);
+    }
+#pragma unroll
     for (int j = 0; j < CH; ++j) {
-      if (e0 + 32 * j >= NG) continue;
-      const float il = 1.f / L[j];
-      *reinterpret_cast<uint2*>(out + 4 * (e0 + 32 * j)) = make_uint2(dev::as_word(__floats2half2_rn(acc[j].x * il, acc[j].y * il)),
-                                                                      dev::as_word(__floats2half2_rn(acc[j].z * il, acc[j].w * il)));
+      const int e4 = lane + 32 * (j0 + j);
+      if (e4 < NG)
+        *reinterpret_cast<uint2*>(out + 4 * e4) =
+            make_uint2(dev::as_word(__floats2half2_rn(acc[j].x, acc[j].y)), dev::as_word(__floats2half2_rn(acc[j].z, acc[j].w)));
     }
   }
 }
