@@ -288,14 +288,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     carry += total;
     __syncthreads();  // warp_sums is reused by the next chunk
   }
-  if (threadIdx.x == 0) {  // each last-split size's first slot, largest size first
-    int at = carry;
-    for (int sz = kMaxSplitBlocksInt4; sz >= 1; --sz) {
+  if (threadIdx.x < 32) {  // each last-split size's first slot, largest size first: a lane has `per` sizes from `top` down
+    const int most = max(p.split_blocks, p.win.split), per = (most + 31) / 32, top = most - (int)threadIdx.x * per;
+    int mine = 0;
+    for (int sz = top; sz > top - per && sz >= 1; --sz) mine += tail_at[sz];
+    int end = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int below = __shfl_up_sync(0xffffffffu, end, o);
+      if ((int)threadIdx.x >= o) end += below;
+    }
+    int at = carry + end - mine;
+    for (int sz = top; sz > top - per && sz >= 1; --sz) {
       const int n = tail_at[sz];
       tail_at[sz] = at;
       at += n;
     }
-    n_dec = at;
+    if (threadIdx.x == 31) n_dec = at;
   }
   __syncthreads();
   for (int t = threadIdx.x; t < p.num_tokens; t += blockDim.x) {
@@ -406,7 +414,8 @@ static WsLayout ws_layout(const pkv_config& c, int num_seqs, int num_tokens, int
   w.max_splits = (max_blocks + c.split_blocks - 1) / c.split_blocks;
   if (win.window != kNoWindow) {
     const int seen = std::min(max_blocks, window_blocks_at_most(win.window, std::min(win.sinks, kNoWindow - kBS)));
-    w.max_splits = (seen + win.split - 1) / win.split;  // (win.split is at most split_blocks)
+    const int least = std::min(win.split, c.split_blocks);  // (a token that sees its whole context runs in split_blocks)
+    w.max_splits = (seen + least - 1) / least;
   }
   w.max_tasks = (int64_t)num_tokens * c.num_kv_heads * w.max_splits;
   const int group = c.num_q_heads / c.num_kv_heads;
@@ -802,7 +811,8 @@ static pkv_status check_io(const void* q, const void* out, const int32_t* block_
 }
 
 static KeyWindow pool_window(const pkv_config& c, int window, int sinks) {
-  return make_window(window, sinks, c.split_blocks, c.kv_dtype == PKV_KV_INT4 ? 24 : 8);
+  if (c.kv_dtype != PKV_KV_INT4) return make_window(window, sinks, c.split_blocks);
+  return make_window(window, sinks, c.split_blocks, 24, std::max(0, std::min(c.split_blocks / 4, kMaxSplitBlocksInt4 - c.split_blocks)));
 }
 
 // The plan remembered for `workspace`, or null.

@@ -11,7 +11,11 @@ namespace pkv {
 
 constexpr int kBS = 16;          // tokens per cache block
 constexpr int kHeadsTile = 8;    // query heads per KV head handled by one decode MMA tile (G <= 8)
-constexpr int kMaxSplitBlocksInt4 = 128;  // upper bound on split_blocks, and its default, on a 4-bit cache
+// On a 4-bit cache split_blocks may be up to 256 and is 128 by default.  A task costs its SM about 3.6 us beside its blocks, so
+// large batches run faster in longer splits and single rows slower (d 128, 12 / 2 heads, us with 128 and 256 blocks a split, some
+// 10 of each outside the kernel): 256 rows of up to 8192 tokens 88.7 and 76.4, 64 rows of 32000 145 and 125, of 8000 53 and
+// 47; 16 rows of 8000 27 and 31, one row of 8000 23 and 29.
+constexpr int kMaxSplitBlocksInt4 = 256;
 
 // Rows with at least this many new tokens (a prefill chunk) go to the tensor-core tile kernel; shorter
 // rows (decode, short chunks) to the split-K decode kernel.  The choice depends on the row alone, so a
@@ -47,14 +51,16 @@ struct KeyWindow {
 // 24 + 10 33.0 against 36.2; 261 stay at 32 (103 us on the 8-bit cache at d 256, 120 in splits of 28).  At head_dim 64,
 // whose warps go in pairs of blocks, the 66 would be faster as 32 + 32 + 2 (8 / 2 heads: 41.0 us, 45.6 so).  The window
 // alone decides, and a token whose whole context is visible keeps the unwindowed partition.  (On a 4-bit cache, of
-// longer splits for more warps, rounded up to `unit` = 24 blocks, a pair for each of twelve.)
+// longer splits for more warps, rounded up to `unit` = 24 blocks, a pair for each of twelve, and a split may be a quarter
+// longer than split_blocks, `slack`: 130 blocks, a window of 2048 tokens, as one take 31.4 us, as 72 + 58 37.5; 200 rows,
+// 8 / 2 heads, d 64.)
 __host__ __device__ constexpr int window_blocks_at_most(int window, int sinks) {
   return (sinks + kBS - 1) / kBS + (window > kNoWindow - kBS ? kNoWindow / kBS : (window + kBS - 2) / kBS) + 1;
 }
-__host__ constexpr KeyWindow make_window(int window, int sinks, int split_blocks, int unit = 8) {
-  const int seen = window_blocks_at_most(window, sinks < kNoWindow - kBS ? sinks : kNoWindow - kBS);
-  const int n = (seen + split_blocks - 1) / split_blocks, even = ((seen + n - 1) / n + unit - 1) / unit * unit;
-  return KeyWindow{window, sinks, even < split_blocks ? even : split_blocks};
+__host__ constexpr KeyWindow make_window(int window, int sinks, int split_blocks, int unit = 8, int slack = 0) {
+  const int seen = window_blocks_at_most(window, sinks < kNoWindow - kBS ? sinks : kNoWindow - kBS), most = split_blocks + slack;
+  const int n = (seen + most - 1) / most, even = ((seen + n - 1) / n + unit - 1) / unit * unit;
+  return KeyWindow{window, sinks, even < most ? even : most};
 }
 // Blocks per split of a token that sees ctx keys without the window.
 __host__ __device__ constexpr int token_split(int ctx, int split_blocks, const KeyWindow& win) {

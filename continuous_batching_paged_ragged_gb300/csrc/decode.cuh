@@ -54,7 +54,7 @@ struct DecodeTraits {
   // Streaming warps; then the combiner and the scheduler (4-bit: and the producers, decode_int4.cuh).  fp16, 8-bit: four
   // streaming warps, in two or three CTAs per SM.  4-bit: one CTA with as many warps as the registers allow (sixteen in all
   // with 128 each; twelve with 168 at head_dim 256, two fewer with eight query heads, whose shares leave less room for the
-  // rings).  Its blocks are a quarter of the bytes, so its tasks are more blocks (up to 128, MAXB), and what a task costs
+  // rings).  Its blocks are a quarter of the bytes, so its tasks are more blocks (up to 256, MAXB), and what a task costs
   // beside its blocks is paid once an SM.
   static constexpr int NW = !I4 ? 4 : D != 256 ? 12 : G > 6 ? 6 : 8;
   static constexpr int NP = I4 ? 2 : 0;            // 4-bit: producer warps

@@ -117,7 +117,7 @@ typedef struct {
   int32_t head_dim;
   int32_t block_size;    /* tokens per block; must be 16 */
   int32_t num_blocks;    /* physical blocks per layer    */
-  int32_t split_blocks;  /* blocks per split-K partition of a decode row, at most 32 (4-bit cache: 128); 0 = that many */
+  int32_t split_blocks;  /* blocks per split-K partition of a decode row, at most 32, which 0 selects (4-bit: 256, 128) */
   int32_t kv_dtype;      /* PKV_KV_F16 (0), PKV_KV_E4M3 or PKV_KV_INT4 */
 } pkv_config;
 

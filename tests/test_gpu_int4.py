@@ -220,16 +220,16 @@ def test_long_rows_and_batch_invariance(cuda, built, d, hq, split):
     assert _same(oo[0][:2], outs[0][2:4]) and _same(oo[0][4], outs[0][1])
 
 
-@pytest.mark.parametrize("split", [1, 2, 3, 8, 32, 33, 96, 127, 128])
+@pytest.mark.parametrize("split", [1, 2, 3, 8, 32, 33, 96, 127, 128, 129, 255, 256])
 def test_split_sizes(cuda, built, split):
-    batch = synth.custom_batch(synth.Shape(1, 12, 2, 128), [0, 15, 16, 31, 47, 100, 333, 2047, 2048, 4200], [1] * 10, seed=8)
+    batch = synth.custom_batch(synth.Shape(1, 12, 2, 128), [0, 15, 16, 31, 47, 100, 333, 2047, 2048, 4200, 9000], [1] * 11, seed=8)
     _, _, outs = run_batch(batch, [0], kv_dtype=INT4, split_blocks=split, fused=True)
     _check_batch(batch, outs[0])
 
 
 def test_split_size_above_the_limit_is_refused(cuda, built):
     batch = synth.tiny_decode(0)
-    pool = workload.make_pool(batch, split_blocks=129, kv_dtype=INT4)
+    pool = workload.make_pool(batch, split_blocks=257, kv_dtype=INT4)
     attn = workload.Attention(pool, workload.upload(batch, pool))
     with pytest.raises(pkv.PkvError) as e:
         attn.plan()
@@ -238,7 +238,8 @@ def test_split_size_above_the_limit_is_refused(cuda, built):
 
 @pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (12, 2, 128), (8, 1, 128), (16, 4, 256), (8, 1, 256)])
 @pytest.mark.parametrize("split,rows,most,window", [(0, 24, 40000, 0), (1, 300, 700, 0), (5, 200, 3000, 0), (0, 700, 900, 0),
-                                                    (64, 300, 9000, 1500), (128, 40, 30000, 20000)])
+                                                    (64, 300, 9000, 1500), (128, 40, 30000, 20000), (0, 200, 9000, 2048),
+                                                    (256, 60, 20000, 0), (256, 60, 20000, 5000)])
 def test_many_tasks_to_a_streaming_multiprocessor(cuda, built, hq, hkv, d, split, rows, most, window):
     """Tens of tasks an SM, of unequal size, whose warps hand stages, queue entries and shares to each other: no wait gives up,
     launch after launch gives the same bits, and sampled rows agree with what the cache holds."""
