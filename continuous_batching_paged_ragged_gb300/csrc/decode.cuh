@@ -55,7 +55,9 @@ struct DecodeTraits {
   // streaming warps, in two or three CTAs per SM.  4-bit: one CTA with as many warps as the registers allow (sixteen in all
   // with 128 each; twelve with 168 at head_dim 256, two fewer with eight query heads, whose shares leave less room for the
   // rings).  Its blocks are a quarter of the bytes, so its tasks are more blocks (up to 256, MAXB), and what a task costs
-  // beside its blocks is paid once an SM.
+  // beside its blocks is paid once an SM.  (256 rows of up to 8192 tokens, 12 / 2 heads at d 128: 77 us with twelve streaming
+  // warps, 83 with ten, 78 with eight; one producer in place of two: 80 there, 245 for 238 with rows of 262144 tokens at d 256,
+  // 26 for 22 with 200 windowed rows at d 64.)
   static constexpr int NW = !I4 ? 4 : D != 256 ? 12 : G > 6 ? 6 : 8;
   static constexpr int NP = I4 ? 2 : 0;            // 4-bit: producer warps
   static constexpr int MAXB = I4 ? kMaxSplitBlocksInt4 : kMaxSplitBlocks;  // blocks of a task at most
@@ -124,7 +126,7 @@ struct DecodeTraits {
 // hold four pairs; slower on the 5-slot fp16 rings at 128 (59.5 against 51.4 us for 12 / 2 heads) and for the 256-row
 // batch, so only there.  Unwindowed rows at head_dim 64 stay single: their results keep their bits.
 template <int D, int KV, bool W>
-constexpr bool kPairs = (KV == kKvE4M3 && D == 256) || (KV != kKvInt4 && W && D == 64);
+constexpr bool kPairs = (KV == kKvE4M3 && D == 256) || (W && D == 64);
 
 struct DecodeParams {
   CUtensorMap kv_map;  // fp16: the pool as whole runs; 8-bit: as rows of codes (64-byte aligned: first member)
@@ -287,7 +289,8 @@ __device__ __forceinline__ int dealt(int w, int rot) { return NW == 4 ? (w - rot
 // 4-bit: a task's pairs of blocks go around the first of its P warps, P a function of their number: three pairs a warp at least,
 // so that a small task does not cost every warp its share (and the combiner as many to fold); the next task begins behind them.
 // Pair i is at place i % P, its warp is (place + rot) % NW; shares are folded by place, so that rot, which is whatever the tasks
-// before came to, moves no result.
+// before came to, moves no result.  (One row of 700 tokens 7.6 us, with one pair a warp 7.8, with six 8.4; 256 rows of up to
+// 8192 tokens 77, 78 and 78.)
 constexpr int kLeastPairs = 3;
 template <int NW>
 __device__ __forceinline__ int spread(int pairs) { return min(NW, (pairs + kLeastPairs - 1) / kLeastPairs); }
@@ -1059,13 +1062,11 @@ __device__ __forceinline__ void stream_loop(const DecodeParams& p, const DecodeS
 // Output element held by register r of `lane` in the O^T fragment layout: its dim and its head.  fp16
 // cache: m-tile mt = r / 4 covers dims 16 mt .. 16 mt + 15, the lane's rows at g = lane / 4 and g + 8.
 // 8-bit cache: m-tiles 2i and 2i + 1 cover dims 32 i .. 32 i + 31, the even dims in the first and the odd
-// ones in the second; the lane's rows are dims 32 i + 2g (+ 16) and the next odd one.  4-bit cache: m-tiles 2i and
-// 2i + 1 cover dims 32 i .. 32 i + 31 too, dims 4g and 4g + 1 of them in the first, 4g + 2 and 4g + 3 in the second.
+// ones in the second; the lane's rows are dims 32 i + 2g (+ 16) and the next odd one.
 template <int KV>
 __device__ __forceinline__ void frag_coord(int lane, int r, int& dim, int& head) {
   const int mt = r >> 2, g = lane >> 2;
-  if constexpr (KV == kKvInt4) dim = 32 * (mt >> 1) + 4 * g + 2 * (mt & 1) + ((r >> 1) & 1);
-  else if constexpr (KV == kKvE4M3) dim = 32 * (mt >> 1) + ((r & 2) ? 16 : 0) + 2 * g + (mt & 1);
+  if constexpr (KV == kKvE4M3) dim = 32 * (mt >> 1) + ((r & 2) ? 16 : 0) + 2 * g + (mt & 1);
   else dim = 16 * mt + g + ((r & 2) ? 8 : 0);
   head = ((lane & 3) << 1) + (r & 1);
 }
@@ -1230,7 +1231,7 @@ struct Scheduler {
       const int m = filled;
       // A long list (many tasks per CTA) balances itself; there the next task is claimed as soon as the
       // previous one has been handed on, for the deepest look-ahead.
-      const bool small = last_nb <= T::EAGER || n_tasks > (T::I4 ? 16 : 4) * (int)gridDim.x;
+      const bool small = last_nb <= T::EAGER || n_tasks > 4 * (int)gridDim.x;
       // Near the end of the list (this CTA's last claim was within two grids of it), the counter is read
       // before waiting: once every task has been claimed (the counter may lag, never run ahead) the end of
       // the work is published at once, and the warps finish without waiting for a claim that can only come

@@ -1,4 +1,4 @@
-// The streaming warps' loop over a 4-bit cache.
+// Decode over a 4-bit cache: the streaming warps' loop, and the kernel around it.
 //
 // A block is one record (int4.cuh): K's codes, V's codes and the scales of 16 keys arrive together.  Blocks go in
 // pairs: both blocks' scores, one softmax step, both blocks' products, in one straight line of code whose chains overlap.
@@ -6,8 +6,9 @@
 //   scores   S[key][head] = sum over groups g of s_K[key][g] * sum_{d in g} code[key][d] q[d]
 //   values   O[d][head]  += sum over keys of (code[key][d] s_V[key][g(d)]) * w[key][head]
 //
-// What bounds such a loop is instructions per block, not bytes (a record is 2.3 KB at head_dim 128 and an SM's share of
-// DRAM brings one every 100 cycles), so the work on a code is what it can be in packed fp16: a mask under an exponent makes
+// What bounds such a loop is instructions per block as much as bytes (a record is 2.3 KB at head_dim 128, an SM's share of
+// DRAM brings one every 100 cycles, and a quarter of the SM works on one for 390: 250 at head_dim 64 for 50, 800 at 256 for
+// 200), so the work on a code is what it can be in packed fp16: a mask under an exponent makes
 // 1024 + c or 1024 + 16 c of it (c = code + 8, as it is stored), one fused multiply-add the code itself.  Scores are
 // scaled by group in fp32, on the exact sums of 32 products.  Values are multiplied by their scales in fp16, which is exact
 // (a code times its scale is an fp16 number); halved, so that the largest does not overflow, and the output doubled at the end:
@@ -17,6 +18,8 @@
 // l, o and the reference m belong together, whatever m is: the combiner and the merges need nothing else.)
 // Tried: codes as fp16 subnormals c * 2^-24, straight out of the mask, and the 8 taken away by MMAs of its own: a fifth fewer
 // instructions, but the tensor core lines such products up by their exponents and cuts off what is 2^-14 of a key's scale.
+// And the keys' upper codes as 64 + c, straight out of the mask, the 72 q too much taken away in the products' first
+// accumulator: 365 in place of 390 cycles a block, nothing of a pass (77.9 us; the offsets' registers cost 264 for 238 at 256).
 #pragma once
 
 #include "decode.cuh"
@@ -252,11 +255,15 @@ __device__ __forceinline__ void attend_pair(const uint32_t (&base)[2], uint32_t 
 }
 
 // ---------------------------------------------------------------------------------------------------
-// The 4-bit cache's decode kernel: one CTA per SM, the tasks, the scheduler warp and the combiner warp of the other formats,
-// and between them producer warps that copy a task's records, two blocks a stage, for the streaming warps.  A pair of blocks is
-// 4.6 KB at head_dim 128, and an SM's share of DRAM brings one every 200 cycles: with the copies issued by the streaming warps
-// themselves (as the larger blocks' are) a pair cost 700 cycles of issuing and waiting beside 1,200 of arithmetic, with
-// 16-byte copies by all lanes more.
+// The 4-bit cache's decode kernel: one CTA per SM, the tasks and the scheduler warp of the other formats, a combiner warp, and
+// producer warps that copy a task's records, two blocks a stage, for the streaming warps.  A pair of blocks is 4.6 KB at
+// head_dim 128, and an SM's share of DRAM brings one every 200 cycles: with the copies issued by the streaming warps themselves
+// (as the larger blocks' are) a pair cost 700 cycles of issuing and waiting beside 1,200 of arithmetic, with 16-byte copies by
+// all lanes more; in stages that all streaming warps share, a wait may meet its stage's phase two rounds off.
+// Measured: one row of 700 tokens, 12 / 2 heads at d 128, 7.6 us; 256 rows of up to 8192 tokens 77 us, 3.8 TB/s; four rows of
+// 262144 tokens, 16 / 4 heads at d 256, 238 us, 5.1 TB/s; 200 rows behind a window of 2048, 8 / 2 heads at d 64, 22 us.  Of the
+// 77 us the warps compute for 44; the launch and its first loads take 4, what a task costs its warps besides its pairs 15 (its
+// q, its share, waits between tasks), the combiner's last tasks and merges 7 and SMs that end early the rest.
 // ---------------------------------------------------------------------------------------------------
 
 // Waits for every lane's own barrier (lanes without `mine` have none): all are tested at once, and the wait proper is the whole
