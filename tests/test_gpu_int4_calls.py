@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 import torch
 
+import test_gpu_int4 as int4_tests
 import test_gpu_other_device as other
 from continuous_batching_paged_ragged_gb300 import pkv, synth, workload
 from helpers_gpu import run_batch, row_slice
@@ -119,3 +120,8 @@ def test_new_calls_with_another_device_current(cuda, built, tmp_path):
     r = subprocess.run([sys.executable, "-c", probe, root, shim], capture_output=True, text=True, timeout=300,
                        env=dict(os.environ, LD_PRELOAD=shim))
     assert r.returncode == 0 and "REFUSED 3" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("hq,hkv,d", int4_tests.SHAPES)
+def test_a_window_at_every_head_layout(cuda, built, hq, hkv, d):
+    int4_tests.test_window_with_freed_blocks_and_hidden_rubbish(cuda, built, hq, hkv, d, 100, 4, False)
