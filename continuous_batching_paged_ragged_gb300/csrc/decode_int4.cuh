@@ -260,9 +260,9 @@ __device__ __forceinline__ void attend_pair(const uint32_t (&base)[2], uint32_t 
 // head_dim 128, and an SM's share of DRAM brings one every 200 cycles: with the copies issued by the streaming warps themselves
 // (as the larger blocks' are) a pair cost 700 cycles of issuing and waiting beside 1,200 of arithmetic, with 16-byte copies by
 // all lanes more; in stages that all streaming warps share, a wait may meet its stage's phase two rounds off.
-// Measured: one row of 700 tokens, 12 / 2 heads at d 128, 7.6 us; 256 rows of up to 8192 tokens 77 us, 3.8 TB/s; four rows of
-// 262144 tokens, 16 / 4 heads at d 256, 238 us, 5.1 TB/s; 200 rows behind a window of 2048, 8 / 2 heads at d 64, 22 us.  Of the
-// 77 us the warps compute for 44; the launch and its first loads take 4, what a task costs its warps besides its pairs 15 (its
+// Measured: one row of 700 tokens, 12 / 2 heads at d 128, 7.3 us; 256 rows of up to 8192 tokens 76 us, 3.9 TB/s; four rows of
+// 262144 tokens, 16 / 4 heads at d 256, 239 us, 5.0 TB/s; 200 rows behind a window of 2048, 8 / 2 heads at d 64, 22 us.  Of the
+// 76 us the warps compute for 44; the launch and its first loads take 4, what a task costs its warps besides its pairs 15 (its
 // q, its share, waits between tasks), the combiner's last tasks and merges 7 and SMs that end early the rest.
 // ---------------------------------------------------------------------------------------------------
 
@@ -450,8 +450,6 @@ __device__ __forceinline__ void stream_int4(const DecodeParams& p, const DecodeS
   int shares = 0;        // shares this warp has handed to the combiner warp
   int at = 0;            // the warp's stage (of NRW) that its next pair comes in
   uint32_t phase = 0;    // and the phase of that stage
-  float* my_o = sm.sh_o + warp * T::OV * T::SHL;
-  float2* my_ml = sm.sh_ml + warp * kHeadsTile;
   for (int k = 0;; ++k) {
     bool got = cta_wait(&sm.qfull[k % T::QD], (k / T::QD) & 1, sm.abort, p.err);
     if (!__all_sync(0xffffffffu, got)) return;
@@ -461,8 +459,7 @@ __device__ __forceinline__ void stream_int4(const DecodeParams& p, const DecodeS
     const int around = spread<T::NW>(d.pairs());
     const int first = dealt<T::NW>(warp, e.rot);                 // the warp's pairs: first, first + around, ...
     const int np = place_pairs(d.pairs(), around, first);
-    int half_left = np / 2;                                      // pairs to go until the half-way signal (Scheduler)
-    if (half_left == 0 && lane == 0) dev::mbar_arrive(&sm.qmid[k % T::QD]);
+    if (np < 2 && lane == 0) dev::mbar_arrive(&sm.qmid[k % T::QD]);  // the half-way signal (Scheduler): after np / 2 pairs
     if (np > 0) {
       const int low = W ? window_low(d.ctx, p.win.window) : 0;  // the window's first key
       const int b0 = 2 * (first + around * lane);
@@ -491,13 +488,16 @@ __device__ __forceinline__ void stream_int4(const DecodeParams& p, const DecodeS
       }
 
       for (int i = 0; i < np; ++i) {
-        const int pr = first + around * i, slot = warp * T::NRW + at;
+        const int slot = warp * T::NRW + at;
         got = cta_wait(&full[slot], phase, sm.abort, p.err);
         if (!__all_sync(0xffffffffu, got)) return;
         uint32_t base[2] = {ring + slot * T::RUN, ring + slot * T::RUN + R::BYTES};
         uint32_t hide = 0;  // bit 2u: key lane / 4 of block u is not seen, bit 2u + 1: key lane / 4 + 8
-        if (edges >> i & 1) {
-          const int n = min(2, d.nb - 2 * pr);
+        if (edges >> i & 1) {  // (rare: what it needs of the task is read again, and no register holds it from pair to pair)
+          const typename T::Task& e = sm.queue[k % T::QD];
+          const Int4Task<D, G, W> d(p, e);
+          const int pr = dealt<T::NW>(warp, e.rot) + spread<T::NW>(d.pairs()) * i, n = min(2, d.nb - 2 * pr);
+          const int low = W ? window_low(d.ctx, p.win.window) : 0;
 #pragma unroll 1
           for (int u = 0; u < n; ++u) edge_block<D, G, W>(p, d, 2 * pr + u, u == 0 ? base[0] : base[1], low, u, lane, hide);
           if (n < 2) {  // an odd last block is its own twin, of which nothing is seen
@@ -513,7 +513,7 @@ __device__ __forceinline__ void stream_int4(const DecodeParams& p, const DecodeS
           at = 0;
           phase ^= 1;
         }
-        if (half_left > 0 && --half_left == 0 && lane == 0) dev::mbar_arrive(&sm.qmid[k % T::QD]);
+        if (i + 1 == np / 2 && lane == 0) dev::mbar_arrive(&sm.qmid[k % T::QD]);
       }
 
       // ---- hand this warp's share of the split to the combiner warp ----
@@ -528,6 +528,8 @@ __device__ __forceinline__ void stream_int4(const DecodeParams& p, const DecodeS
       }
       const int hg = lane & 3;
       if (hg < T::LG) {
+        float* my_o = sm.sh_o + warp * T::OV * T::SHL;
+        float2* my_ml = sm.sh_ml + warp * kHeadsTile;
         const int ci = (lane >> 2) * T::LG + hg;
 #pragma unroll
         for (int mt = 0; mt < T::MT; ++mt)  // (the values were halved)
