@@ -8,9 +8,10 @@
 //
 // A code stands for code * s, which is an fp16 number: |code| <= 7 has three bits and s at most eight.  s is the smallest
 // number of at most eight significant bits (and a multiple of 2^-24) that is no less than a seventh of the group's largest
-// magnitude, so nothing is clipped; a code is the integer nearest to x / s, ties to even.  What this costs against a
-// scale of 11 bits is a step wider by at most 2^-7; what it gives is that every reader of the cache computes
-// with the same values, exactly.
+// magnitude, but at most 9344, seven of which are 65408: beyond that (65440, 65472 and 65504, which have a seventh up to 9357.7,
+// and codes of 7 all the same) the next scale's 7 would pass the fp16 maximum.  A code is the integer nearest to x / s, ties to
+// even; nothing is clipped.  What this costs against a scale of 11 bits is a step wider by at most 2^-7; what it gives is that
+// every reader of the cache computes with the same values, exactly.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -41,15 +42,16 @@ namespace dev {
 // The scale of a group whose largest magnitude has fp16 bits `amax`.  A seventh is taken a little low (by 2^-20, more than
 // the product's rounding) and rounded up to eight significant bits: amax / 7 is either a number of eight bits or off any
 // such number by more than 2^-13 of it (amax has 11 bits, seven times eight bits have 11 as well), so the result is the one
-// that the exact quotient gives.  Then up to a multiple of 2^-24, which concerns scales below 2^-16 alone.
+// that the exact quotient gives.  Finite magnitudes past 65408 give 9408, which becomes 9344 (infinities and NaN stay what they
+// are, and show).  Then up to a multiple of 2^-24, which concerns scales below 2^-16 alone.
 __device__ __forceinline__ __half int4_scale(uint32_t amax) {
   const float seventh = __half2float(__ushort_as_half((unsigned short)amax)) * (1.f / 7.f * (1.f - 0x1p-20f));
   const uint32_t b = (__float_as_uint(seventh) + 0xFFFFu) & 0xFFFF0000u;
-  return __float2half_ru(__uint_as_float(b));
+  return __float2half_ru(b == __float_as_uint(9408.f) ? 9344.f : __uint_as_float(b));
 }
 
 // Codes of 8 fp16 values under scale s, value i in bits 4i .. 4i + 3, plus 8.  x / s is x times a rounded reciprocal, off by
-// less than 2^-20 for quotients up to 7; rounding it to a multiple of 2^-14 first lands on every tie exactly, because a
+// less than 2^-20 for quotients up to 7.02; rounding it to a multiple of 2^-14 first lands on every tie exactly, because a
 // quotient that is no tie is at least 2^-12 away from one (x has 11 bits, s eight).  Then to the nearest integer, ties to
 // even, in the low bits of a float of ulp 1.
 __device__ __forceinline__ uint32_t int4_encode8(const uint4& r, __half s) {
@@ -68,15 +70,15 @@ __device__ __forceinline__ uint32_t int4_encode8(const uint4& r, __half s) {
   return out;
 }
 
-// Eight codes as fp16 values code * s: exact but within 3 % of the fp16 maximum, where they saturate to +-65504.
+// Eight codes as fp16 values code * s, exactly.
 __device__ __forceinline__ uint4 int4x8_dequant(uint32_t codes, __half s) {
-  const __half2 s2 = __half2half2(s), top = __half2half2(__ushort_as_half(0x7BFF)), low = __hneg2(top);
+  const __half2 s2 = __half2half2(s);
   uint32_t p[4];  // pairs (i, i + 4)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t m = ((codes >> (4 * i)) & 0x000F000Fu) | 0x64006400u;  // 1024 + code + 8
     __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&m), __half2half2(__ushort_as_half(0x6408)));
-    v = __hmin2(__hmax2(__hmul2(v, s2), low), top);
+    v = __hmul2(v, s2);
     p[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   return make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410), __byte_perm(p[0], p[1], 0x7632),

@@ -95,10 +95,10 @@ typedef enum {
  * kv_dtype = PKV_KV_INT4, the 4-bit cache.  [ABL], same section, sizes a window's cache at 4 bits next to 8.  32
  * consecutive values of a cached row (one token's head_dim values of one KV head, K and V separately) share a scale s: the
  * smallest number of at most 8 significant bits, and a multiple of 2^-24, that is no less than a seventh of their largest
- * magnitude, kept in fp16 (0 for 32 zeros).  Each value is held as the integer nearest to x / s, ties to even,
- * which is in -7 .. 7; nothing is clipped.  It stands for code * s, which is an fp16 number (unless within 3 % of the
- * fp16 maximum): attention, in every path, and pkv_gather read exactly that.  A (block, KV head) is one record of
- * 18 * head_dim bytes, codes stored plus 8 and two to a byte, the lower half first:
+ * magnitude, but at most 9344 (a seventh of 65408, as which larger magnitudes count), kept in fp16 (0 for 32 zeros).  Each
+ * value is held as the integer nearest to x / s, ties to even, which is in -7 .. 7; nothing is clipped.  It stands
+ * for code * s, which is an fp16 number: attention, in every path, and pkv_gather read exactly that.  A (block, KV head) is
+ * one record of 18 * head_dim bytes, codes stored plus 8 and two to a byte, the lower half first:
  *     records[num_layers][num_blocks][num_kv_heads]:
  *         K codes [head_dim / 32][block_size][16]  uint8
  *         V codes [head_dim / 32][block_size][16]  uint8
@@ -187,8 +187,8 @@ pkv_status pkv_append(pkv_pool* pool, int32_t layer, const void* k, const void* 
 
 /* Reads cached rows back as values, whatever the cache holds them in: k_out[t], v_out[t] ([num_kv_heads][head_dim] fp16
  * each) become what slot slot_mapping[t] of `layer` stands for, for t < num_tokens -- the bits of an fp16 cache, code
- * times scale of an 8-bit or 4-bit one (exact where that is an fp16 number, as the 4-bit cache's always are, else rounded
- * to one; within 3 % of the fp16 maximum it saturates to +-65504).  The way out of a pool into another one, of another
+ * times scale of a 4-bit one, code times scale of an 8-bit one (exact where that is an fp16 number, else rounded to one;
+ * within 3 % of the fp16 maximum it saturates to +-65504).  The way out of a pool into another one, of another
  * format or another engine's, by an append.  Where the slot is -1 the outputs are left as they were; any other
  * out-of-range slot likewise, and sets PKV_DEVERR_SLOT_RANGE.  A slot may be named more than once.
  *

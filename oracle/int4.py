@@ -7,7 +7,8 @@ sampled", section "Context math sets the ceiling the fields ignore"), and quanti
 limit ("Continuous Batching Is Not a Bigger Batch", section "Checking it on a real system").  Readings taken:
 
   * 32 consecutive values of a cached row -- a token's d values of one KV head, K and V separately -- share a scale s: the
-    smallest number of at most 8 significant bits, and a multiple of 2^-24, with max|x| <= 7 s (0 for 32 zeros);
+    smallest number of at most 8 significant bits, and a multiple of 2^-24, with max|x| <= 7 s (0 for 32 zeros), but at
+    most 9344: magnitudes past 7 * 9344 = 65408 count as that, so that no code stands for more than fp16 holds;
   * each value is the integer nearest to x / s, ties to even, so -7 .. 7, stored plus 8; it stands for code * s;
   * a (block, KV head) is a record of 18 d bytes: K's codes [d / 32][16 tokens][16 bytes] (the lower half of a byte
     first), V's, then the scales [16 tokens][K, V][d / 32] in fp16.
@@ -21,6 +22,7 @@ import numpy as np
 
 GROUP = 32
 BS = 16
+TOP = 65408.0  # the largest 7 s that is an fp16 number
 
 # every number of at most 8 significant bits that is a multiple of 2^-24, ascending, past 65504 / 7
 SCALES = sorted({m * 2.0 ** e for m in range(256) for e in range(-24, 8)})
@@ -42,7 +44,7 @@ def quantize_rows(x: np.ndarray) -> tuple[np.ndarray, np.ndarray]:
     assert np.all(np.isfinite(x)), "the 4-bit cache takes finite keys and values"
     g = x.reshape(*x.shape[:-1], -1, GROUP)
     table = np.array(SCALES)
-    s = table[np.searchsorted(7 * table, np.abs(g).max(-1), side="left")]
+    s = table[np.searchsorted(7 * table, np.minimum(np.abs(g).max(-1), TOP), side="left")]
     q = np.divide(g, s[..., None], out=np.zeros_like(g), where=s[..., None] > 0)  # 11 bits over 8: a tie is exact
     return np.rint(q).astype(np.int8).reshape(x.shape), s
 

@@ -1,0 +1,88 @@
+"""GPU: the ends of fp16's range on the 4-bit cache.  A code stands for code * s, an fp16 number, and every reader gives that:
+the decode after an append or with it fused, prompt chunks, and pkv_gather.
+
+Exactness: with keys of zero every score is 0, the softmax's weights are one power of two, and a row of equal values v has the
+output n v / n, off by the division's 2^-23 of v: the fp16 number v itself."""
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_int4 as int4_tests
+from oracle import int4
+from continuous_batching_paged_ragged_gb300 import pkv
+
+pytestmark = pytest.mark.gpu
+
+INT4 = pkv.PKV_KV_INT4
+LARGE = [65504.0, -65504.0, 65472.0, 65440.0, 65408.0, 65376.0, 60000.0, 30000.0]
+LAYOUTS = [(64, 2), (64, 8), (128, 6), (128, 1), (256, 4), (256, 8)]
+
+
+def _equal_rows(sizes, d, hq):
+    """(q, k, v, rows): for every size a row of one key, one of 37 with a new token, and one of 30 with 20."""
+    rows, q, k, v = [], [], [], []
+    for size in sizes:
+        for ctx, n in ((1, 1), (37, 1), (30, 20)):
+            rows.append((ctx, n))
+            q.append(np.random.default_rng(ctx).standard_normal((n, hq, d)).astype(np.float16))
+            k.append(np.zeros((ctx, 1, d), np.float16))
+            v.append(np.full((ctx, 1, d), size, np.float16))
+            v[-1][..., 1::2] *= np.float16(-1)
+    return q, k, v, rows
+
+
+def _check_equal_rows(sizes, d, hq, fused, **window):
+    """All rows in one pass (the chunks of 20 among them), and the single tokens by themselves (fused: one launch)."""
+    q, k, v, rows = _equal_rows(sizes, d, hq)
+    for pick in (range(len(rows)), [i for i, r in enumerate(rows) if r[1] == 1]):
+        outs = int4_tests._run_values([q[i] for i in pick], [k[i] for i in pick], [v[i] for i in pick], hq, 1, d,
+                                      [rows[i][0] for i in pick], [rows[i][1] for i in pick], fused, **window)
+        for out, i in zip(outs, pick):
+            want = int4.values(v[i][:1])[0, 0]
+            assert (out.astype(np.float64) == want).all(), (rows[i], float(v[i][0, 0, 0]), np.unique(out), np.unique(want))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_large_values_stored_and_read_back(cuda, built, d):
+    x = np.random.default_rng(d).standard_normal((len(LARGE), 2, d)).astype(np.float16)
+    for i, size in enumerate(LARGE):
+        x[i, i % 2, i::7] = size
+        x[i, 1 - i % 2, 5 * i] = -size
+    pool = pkv.Pool(1, 2, 2, d, 2, kv_dtype=INT4)
+    pool.buffer[:-256].zero_()
+    want = pool.cache_view().cpu().numpy().copy()
+    slots = np.arange(len(x), dtype=np.int64) * 3
+    dx, ds = torch.from_numpy(x).cuda(), torch.from_numpy(slots).cuda()
+    pkv.pkv_append(pool.handle, 0, dx, dx.flip(0).contiguous(), ds, len(x))
+    int4.append_reference_4bit(want[0], x, x[::-1].copy(), slots)
+    assert pool.check() == 0 and np.array_equal(pool.cache_view().cpu().numpy(), want)
+    ko, vo = torch.empty_like(dx), torch.empty_like(dx)
+    pkv.pkv_gather(pool.handle, 0, ds, len(x), ko, vo)
+    assert np.array_equal(ko.cpu().numpy().astype(np.float64), int4.values(x))
+    assert np.array_equal(vo.flip(0).cpu().numpy().astype(np.float64), int4.values(x))
+
+
+@pytest.mark.parametrize("d,hq", LAYOUTS)
+@pytest.mark.parametrize("fused", [False, True])
+def test_large_values_attended(cuda, built, d, hq, fused):
+    _check_equal_rows(LARGE, d, hq, fused)
+    _check_equal_rows(LARGE[:3], d, hq, fused, window=9, sinks=3)
+
+
+@pytest.mark.parametrize("d,hq", LAYOUTS)
+@pytest.mark.parametrize("fused", [False, True])
+def test_large_keys_attended(cuda, built, d, hq, fused):
+    """Keys at the top of the range against small queries, in decode rows and a chunk: scores of the values that are held."""
+    rng = np.random.default_rng(3)
+    rows, q, k, v = [(1, 1), (40, 1), (37, 2), (50, 20)], [], [], []
+    for ctx, n in rows:
+        q.append((rng.standard_normal((n, hq, d)) * 2.0**-14).astype(np.float16))
+        x = rng.standard_normal((ctx, 1, d)).astype(np.float16)
+        x[::3, :, 7] = np.float16(65504)
+        x[1::5, :, 40] = np.float16(-65472)
+        x[2::4, :, 41] = np.float16(65440)
+        k.append(x)
+        v.append(rng.standard_normal((ctx, 1, d)).astype(np.float16))
+    outs = int4_tests._run_values(q, k, v, hq, 1, d, [r[0] for r in rows], [r[1] for r in rows], fused)
+    for b in range(len(rows)):
+        int4_tests._close(outs[b], q[b], int4.values(k[b]), int4.values(v[b]), f"row {b}")
