@@ -11,8 +11,7 @@
 // 200), so the work on a code is what it can be in packed fp16: a mask under an exponent makes
 // 1024 + c or 1024 + 16 c of it (c = code + 8, as it is stored), one fused multiply-add the code itself.  Scores are
 // scaled by group in fp32, on the exact sums of 32 products.  Values are multiplied by their scales in fp16, which is exact
-// (a code times its scale is an fp16 number); halved, so that the largest does not overflow, and the output doubled at the end:
-// under scales below 2^-14 that may round a value by half of fp16's smallest number.
+// (a code times its scale is an fp16 number, subnormal or not).
 // The softmax's reference moves only when a weight would pass 2^15, and then to 2^-4 of the largest: most pairs need neither
 // a reduction over the warp nor a rescaling of O.  (Weights are rounded to fp16 for the product, at most 2^-11 of each off;
 // l, o and the reference m belong together, whatever m is: the combiner and the merges need nothing else.)
@@ -99,7 +98,7 @@ __device__ __forceinline__ void write_row(const DecodeParams& p, uint32_t base, 
   }
 }
 
-// The pair of codes in bits 0 .. 3 (lo) or 4 .. 7 (hi) of a word's halves, or half of them.
+// The pair of codes in bits 0 .. 3 (lo) or 4 .. 7 (hi) of a word's halves.
 namespace dev {
 // (x & mask) | bits, in one instruction (from the expression the compiler made two, which took 467 in place of 310 cycles a
 // block and scheduler at head_dim 128).
@@ -108,15 +107,11 @@ __device__ __forceinline__ uint32_t masked_or(uint32_t x, uint32_t mask, uint32_
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
   return r;
 }
-__device__ __forceinline__ __half2 codes_lo(uint32_t x, bool halve) {
-  const __half2 v = as_half2(masked_or(x, 0x000F000Fu, 0x64006400u));
-  return halve ? __hfma2(v, as_half2(0x38003800u), as_half2(0xE008E008u))  // (1024 + c) / 2 - 516
-               : __hadd2(v, as_half2(0xE408E408u));                        // 1024 + c - 1032
+__device__ __forceinline__ __half2 codes_lo(uint32_t x) {  // 1024 + c - 1032
+  return __hadd2(as_half2(masked_or(x, 0x000F000Fu, 0x64006400u)), as_half2(0xE408E408u));
 }
-__device__ __forceinline__ __half2 codes_hi(uint32_t x, bool halve) {
-  const __half2 v = as_half2(masked_or(x, 0x00F000F0u, 0x64006400u));
-  return halve ? __hfma2(v, as_half2(0x28002800u), as_half2(0xD080D080u))   // (1024 + 16 c) / 32 - 36
-               : __hfma2(v, as_half2(0x2C002C00u), as_half2(0xD480D480u));  // (1024 + 16 c) / 16 - 72
+__device__ __forceinline__ __half2 codes_hi(uint32_t x) {  // (1024 + 16 c) / 16 - 72
+  return __hfma2(as_half2(masked_or(x, 0x00F000F0u, 0x64006400u)), as_half2(0x2C002C00u), as_half2(0xD480D480u));
 }
 }  // namespace dev
 
@@ -156,8 +151,8 @@ __device__ __forceinline__ void attend_pair(const uint32_t (&base)[2], uint32_t 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t ra = r[u][2 * h], rb = r[u][2 * h + 1];
-          const uint32_t a[4] = {dev::as_word(dev::codes_lo(ra, false)), dev::as_word(dev::codes_lo(rb, false)),
-                                 dev::as_word(dev::codes_hi(ra, false)), dev::as_word(dev::codes_hi(rb, false))};
+          const uint32_t a[4] = {dev::as_word(dev::codes_lo(ra)), dev::as_word(dev::codes_lo(rb)),
+                                 dev::as_word(dev::codes_hi(ra)), dev::as_word(dev::codes_hi(rb))};
           dev::mma_16816_0(c[u][h], a, qb[4 * gp + 2 * h][0], qb[4 * gp + 2 * h][1]);
         }
 #pragma unroll
@@ -165,8 +160,8 @@ __device__ __forceinline__ void attend_pair(const uint32_t (&base)[2], uint32_t 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t ra = r[u][2 * h] >> 8, rb = r[u][2 * h + 1] >> 8;
-          const uint32_t a[4] = {dev::as_word(dev::codes_lo(ra, false)), dev::as_word(dev::codes_lo(rb, false)),
-                                 dev::as_word(dev::codes_hi(ra, false)), dev::as_word(dev::codes_hi(rb, false))};
+          const uint32_t a[4] = {dev::as_word(dev::codes_lo(ra)), dev::as_word(dev::codes_lo(rb)),
+                                 dev::as_word(dev::codes_hi(ra)), dev::as_word(dev::codes_hi(rb))};
           dev::mma_16816(c[u][h], a, qb[4 * gp + 2 * h + 1][0], qb[4 * gp + 2 * h + 1][1]);
         }
 #pragma unroll
@@ -245,8 +240,8 @@ __device__ __forceinline__ void attend_pair(const uint32_t (&base)[2], uint32_t 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {  // dims 4 qh + 2 e (rows 0 .. 7 of the tile) and 4 qh + 2 e + 1
           const uint32_t ra = r[2 * h] >> (8 * e), rb = r[2 * h + 1] >> (8 * e);
-          const uint32_t a[4] = {dev::as_word(__hmul2(dev::codes_lo(ra, true), sa)), dev::as_word(__hmul2(dev::codes_hi(ra, true), sa)),
-                                 dev::as_word(__hmul2(dev::codes_lo(rb, true), sb)), dev::as_word(__hmul2(dev::codes_hi(rb, true), sb))};
+          const uint32_t a[4] = {dev::as_word(__hmul2(dev::codes_lo(ra), sa)), dev::as_word(__hmul2(dev::codes_hi(ra), sa)),
+                                 dev::as_word(__hmul2(dev::codes_lo(rb), sb)), dev::as_word(__hmul2(dev::codes_hi(rb), sb))};
           dev::mma_16816(o[4 * gp + 2 * h + e], a, pb[u][0], pb[u][1]);
         }
       }
@@ -532,8 +527,8 @@ __device__ __forceinline__ void stream_int4(const DecodeParams& p, const DecodeS
         float2* my_ml = sm.sh_ml + warp * kHeadsTile;
         const int ci = (lane >> 2) * T::LG + hg;
 #pragma unroll
-        for (int mt = 0; mt < T::MT; ++mt)  // (the values were halved)
-          reinterpret_cast<float4*>(my_o)[mt * T::SHL + ci] = make_float4(2.f * o[mt][0], 2.f * o[mt][1], 2.f * o[mt][2], 2.f * o[mt][3]);
+        for (int mt = 0; mt < T::MT; ++mt)
+          reinterpret_cast<float4*>(my_o)[mt * T::SHL + ci] = make_float4(o[mt][0], o[mt][1], o[mt][2], o[mt][3]);
         if (lane < T::LG) {
           my_ml[2 * lane] = make_float2(m0, l0);
           my_ml[2 * lane + 1] = make_float2(m1, l1);

@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import test_gpu_int4 as int4_tests
 from oracle import int4
 from continuous_batching_paged_ragged_gb300 import pkv
@@ -86,3 +87,34 @@ def test_large_keys_attended(cuda, built, d, hq, fused):
     outs = int4_tests._run_values(q, k, v, hq, 1, d, [r[0] for r in rows], [r[1] for r in rows], fused)
     for b in range(len(rows)):
         int4_tests._close(outs[b], q[b], int4.values(k[b]), int4.values(v[b]), f"row {b}")
+
+
+SMALL = [m * 2.0**-24 for m in (1, -3, 5, 7, 9, -15, 33, 127, 1021)] + [2.0**-14 + 2.0**-24, 7 * 1.5 * 2.0**-15]
+
+
+@pytest.mark.parametrize("d,hq", LAYOUTS)
+@pytest.mark.parametrize("fused", [False, True])
+def test_small_values_attended(cuda, built, d, hq, fused):
+    """Down to fp16's smallest number."""
+    _check_equal_rows(SMALL, d, hq, fused)
+    _check_equal_rows(SMALL[:4], d, hq, fused, window=9, sinks=3)
+
+
+@pytest.mark.parametrize("d,hq", LAYOUTS)
+@pytest.mark.parametrize("bits", [2, 4, 7, 10, 12])
+def test_one_key_of_small_values_is_its_values(cuda, built, d, hq, bits):
+    """A row of one key has the output that the key's value stands for, whatever the group holds beside it; a row of 40 is
+    off by its weights' rounding and half of fp16's smallest number."""
+    rng = np.random.default_rng(bits)
+    rows = [(1, 1), (40, 1), (1, 1), (25, 20)]
+    q = [rng.standard_normal((n, hq, d)).astype(np.float16) for _, n in rows]
+    k = [rng.standard_normal((c, 1, d)).astype(np.float16) for c, _ in rows]
+    v = [(rng.integers(-2**bits, 2**bits + 1, (c, 1, d)) * 2.0**-24).astype(np.float16) for c, _ in rows]
+    outs = int4_tests._run_values(q, k, v, hq, 1, d, [r[0] for r in rows], [r[1] for r in rows])
+    for b in range(4):
+        held = int4.values(v[b])
+        if rows[b][0] == 1:
+            assert (outs[b].astype(np.float64) == held[0, 0]).all(), b
+            continue
+        want, a = (oracle.window_attention_row(q[b], int4.values(k[b]), x, 1 << 30, 0) for x in (held, np.abs(held)))
+        assert (np.abs(outs[b].astype(np.float64) - want) <= a * (2.0**-11 * 1.001 + 2.0**-13) + 2.0**-25 * 1.001).all(), b
