@@ -185,9 +185,15 @@ __device__ __forceinline__ void attend_pair(const uint32_t (&base)[2], uint32_t 
       if (hide & (2u << (2 * u))) s[u][2] = s[u][3] = -INFINITY;
     }
   }
-  // ---- one online-softmax step for the pair (log2 domain): the references move if some weight would pass its cap ----
-  float b0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2])) * scale;
-  float b1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3])) * scale;
+  // ---- one online-softmax step for the pair (log2 domain): the references move if some weight would pass its cap.  Scores are
+  // rounded before the references are taken and subtracted, so that the largest weight is what the reference makes it at
+  // any size (in one fused operation with the subtraction, scores of 2^28 had weights off by 2^16) ----
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[u][i] = __fmul_rn(s[u][i], scale);  // (not to be fused)
+  float b0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+  float b1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
   if (__any_sync(0xffffffffu, b0 - m0 > kCap || b1 - m1 > kCap)) {
 #pragma unroll
     for (int m = 4; m < 32; m <<= 1) {
@@ -211,8 +217,8 @@ __device__ __forceinline__ void attend_pair(const uint32_t (&base)[2], uint32_t 
   uint32_t pb[2][2];  // P^T as the MMAs' B operand: k = keys, n = heads
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const float p0 = dev::ex2_approx(fmaf(s[u][0], scale, -m0)), p1 = dev::ex2_approx(fmaf(s[u][1], scale, -m1));
-    const float p2 = dev::ex2_approx(fmaf(s[u][2], scale, -m0)), p3 = dev::ex2_approx(fmaf(s[u][3], scale, -m1));
+    const float p0 = dev::ex2_approx(s[u][0] - m0), p1 = dev::ex2_approx(s[u][1] - m1);
+    const float p2 = dev::ex2_approx(s[u][2] - m0), p3 = dev::ex2_approx(s[u][3] - m1);
     l0 += p0 + p2;
     l1 += p1 + p3;
     pb[u][0] = dev::movmatrix_t(dev::as_word(__floats2half2_rn(p0, p1)));

@@ -232,6 +232,9 @@ pkv_status pkv_gather(pkv_pool* pool, int32_t layer, const int64_t* slot_mapping
  * shadow blocks, R the most rows of 16+ new tokens the pass can hold.  Rows may share blocks (forks of a prompt that is
  * still being computed): that many hold them all.
  *
+ * Scores are fp32.  Rows with 16 or more new tokens take scores, times log2(e) / sqrt(head_dim), of up to 2^27 in magnitude;
+ * the decode path takes any.
+ *
  * 4-bit cache: attention reads the values code * s exactly; scores are scaled by group in fp32, and each softmax
  * weight is rounded to fp16.  Rows with 16 or more new tokens take the same fp16 shadow, with the same workspace.
  *

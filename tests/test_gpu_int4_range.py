@@ -118,3 +118,28 @@ def test_one_key_of_small_values_is_its_values(cuda, built, d, hq, bits):
             continue
         want, a = (oracle.window_attention_row(q[b], int4.values(k[b]), x, 1 << 30, 0) for x in (held, np.abs(held)))
         assert (np.abs(outs[b].astype(np.float64) - want) <= a * (2.0**-11 * 1.001 + 2.0**-13) + 2.0**-25 * 1.001).all(), b
+
+
+@pytest.mark.parametrize("d,hq", LAYOUTS)
+@pytest.mark.parametrize("size", [1000.0, 8000.0, 20000.0, 60000.0])
+@pytest.mark.parametrize("fused", [False, True])
+def test_large_scores(cuda, built, d, hq, size, fused):
+    """Queries and keys of one direction, scores up to 2^37: the largest key takes all the weight, wherever it lies, and keys of
+    equal scores share it.  The next score is a thousandth of the largest away or more, more than 2^10 log2 units."""
+    rng = np.random.default_rng(int(size) + d)
+    rows, q, k, v = [(1, 1), (40, 1), (700, 1), (700, 1), (700, 1), (90, 2)], [], [], []
+    for i, (ctx, n) in enumerate(rows):
+        sign = np.where(rng.random(d) < 0.5, 1.0, -1.0)
+        x = sign * size * rng.uniform(-0.9, 0.9, (ctx, 1, 1))
+        x[[0, 3, ctx - n, ctx // 2, ctx - n, 5][i]] = sign * size
+        if i == 4:
+            x[:] = sign * size       # a uniform softmax of scores far from zero
+        q.append((np.ones((n, hq, 1)) * sign * (-size if i == 4 else size)).astype(np.float16))
+        k.append(x.astype(np.float16))
+        v.append(rng.standard_normal((ctx, 1, d)).astype(np.float16))
+    outs = int4_tests._run_values(q, k, v, hq, 1, d, [r[0] for r in rows], [r[1] for r in rows], fused)
+    for b in range(len(rows)):
+        held = int4.values(v[b])
+        want, a = (oracle.window_attention_row(q[b], int4.values(k[b]), x, 1 << 30, 0) for x in (held, np.abs(held)))
+        # weights: 1 each (exact) or 0; the output's rounding and the sums' 2^-24 a term
+        assert (np.abs(outs[b].astype(np.float64) - want) <= 2.0**-11 * 1.001 * np.abs(want) + 2.0**-14 * a + 2.0**-25).all(), b
