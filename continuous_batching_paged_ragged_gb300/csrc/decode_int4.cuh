@@ -269,12 +269,16 @@ __device__ __forceinline__ void attend_pair(const uint32_t (&base)[2], uint32_t 
 
 // Waits for every lane's own barrier (lanes without `mine` have none): all are tested at once, and the wait proper is the whole
 // warp's on the first that is not there.  (With each lane in a wait of its own they suspend the warp one after another, long
-// after the last barrier has completed: one row of 700 tokens took 10.3 in place of 7.9 us.)  False: a wait ran out.
+// after the last barrier has completed: one row of 700 tokens took 10.3 in place of 7.9 us.)  Behind it every lane sees what
+// lies behind every lane's barrier.  False: a wait ran out.
 __device__ __forceinline__ bool cta_wait_lanes(uint64_t* bar, uint32_t parity, bool mine, volatile int* abort, int32_t* err) {
   const uint32_t mine_at = dev::smem_addr(bar);
   for (;;) {
     const uint32_t left = __ballot_sync(0xffffffffu, mine && !dev::mbar_test_wait(bar, parity));
-    if (left == 0) return true;
+    if (left == 0) {
+      __syncwarp();  // (a lane's test orders that lane's reads alone, and a ballot orders none)
+      return true;
+    }
     const int l = __ffs(left) - 1;
     const uint32_t at = __shfl_sync(0xffffffffu, mine_at, l), ph = __shfl_sync(0xffffffffu, parity, l);
     const bool got = cta_wait(reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(at)), ph, abort, err);
