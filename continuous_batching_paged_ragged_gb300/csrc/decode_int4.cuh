@@ -48,8 +48,7 @@ __device__ __forceinline__ uint32_t as_word(__half2 h) { return *reinterpret_cas
 }  // namespace dev
 
 // This pass's rows of a block, `nov` of them from row r0 on, quantized from the inputs exactly as the append stores them,
-// over the record at `base`.  A unit is 8 values of K or V; its lane's first (units 0 .. 31) is `first`, loaded while the
-// record was on its way.
+// over the record at `base`.  A unit is 8 values of K or V, a lane's at a time.
 template <int D>
 struct NewRows {
   static constexpr int CPR = D / 8, CPT = 2 * CPR;  // units of a row; of a token (K, then V)
@@ -58,13 +57,12 @@ struct NewRows {
     const __half* src = (kv ? p.v_in : p.k_in) + ((size_t)(token0 + r) * p.num_kv_heads + g) * D;
     return __ldcg(reinterpret_cast<const uint4*>(src) + c);
   }
-  static __device__ void store(const DecodeParams& p, uint32_t base, int r0, int nov, int64_t token0, int g, int lane, uint4 first) {
+  static __device__ void store(const DecodeParams& p, uint32_t base, int r0, int nov, int64_t token0, int g, int lane) {
     using R = Int4Record<D>;
     for (int u0 = 0; u0 < nov * CPT; u0 += 32) {
       const int unit = u0 + lane;
       const bool in = unit < nov * CPT;
-      uint4 raw = first;
-      if (u0 > 0) raw = in ? load(p, unit, token0, g) : make_uint4(0, 0, 0, 0);
+      const uint4 raw = in ? load(p, unit, token0, g) : make_uint4(0, 0, 0, 0);
       const __half s = dev::int4_scale(dev::int4_group_amax(raw));  // (every lane takes part)
       if (!in) continue;
       const int r = r0 + unit / CPT, kv = (unit / CPR) & 1, c = unit % CPR;
@@ -329,9 +327,7 @@ __device__ __forceinline__ void edge_block(const DecodeParams& p, const Int4Task
   if (nov > 0) {
     const int64_t token0 = d.t - (d.ctx - 1 - ov0);  // the packed token of position ov0
     const int64_t slot = d.ctx - 1 < bpos + kBS ? __ldcg(p.slots + d.t) : -1;
-    uint4 first = make_uint4(0, 0, 0, 0);
-    if (lane < nov * NewRows<D>::CPT) first = NewRows<D>::load(p, lane, token0, d.g);
-    NewRows<D>::store(p, base, ov0 - bpos, nov, token0, d.g, lane, first);
+    NewRows<D>::store(p, base, ov0 - bpos, nov, token0, d.g, lane);
     if (slot != -1) write_row<D>(p, base, d.ctx - 1 - bpos, slot, d.g, lane);
   }
   if (ntok < kBS || (W && bpos < low)) {
