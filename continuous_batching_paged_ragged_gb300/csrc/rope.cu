@@ -97,9 +97,8 @@ __device__ __forceinline__ void rotate8_interleaved(uint4& a, uint4& b, const fl
 // more than the loads and stores of a chunk: with the 8 angles of a 16-value piece computed where they were used, once
 // for every few heads, 8192 tokens took 15 to 21 us).  The unit of the rest is an item: 16 values of a q or KV head (two
 // 16-byte chunks that hold 8 whole pairs, or 16 values past the rotated part; of a KV head the key's and the value's).
-// A thread loads its first items before it computes its angles, so that neither waits for the other.
-// On a 4-bit cache a scale's 32 values are four 8-value
-// chunks of up to four items: the chunks' largest magnitudes meet in shared memory.
+// A thread loads its first items before it computes its angles, so that neither waits for the other.  On a 4-bit cache a
+// scale's 32 values are four 8-value chunks of up to four items: the chunks' largest magnitudes meet in shared memory.
 template <int D, int KV, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams p, const __grid_constant__ RopeTurns turns) {
   constexpr int PC = D / 16;  // items per head: a power of two within a warp
@@ -162,8 +161,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
       const int c0 = !INTER && rot ? pc : 2 * pc, c1 = !INTER && rot ? pc + half / 8 : 2 * pc + 1;
       const bool kv = in && g >= 0 && slot[u] >= 0 && slot[u] < p.num_slots;
       if (in && g == 0 && pc == 0 && slot[u] != -1 && !kv) dev::set_error(p.err, PKV_DEVERR_SLOT_RANGE);
-      float cs[8], sn[8];
       if (in && rot) {
+        float cs[8], sn[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float4 x = angle[tb][j][pc];
@@ -172,8 +171,6 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
           cs[2 * j + 1] = x.z;
           sn[2 * j + 1] = x.w;
         }
-      }
-      if (in && rot) {
         if constexpr (INTER) rotate8_interleaved(a[u], b[u], cs, sn); else rotate8(a[u], b[u], cs, sn);
       }
       if (in && g < 0) {
