@@ -705,7 +705,8 @@ extern "C" pkv_status pkv_norm_rope_append(pkv_pool* pool, int32_t layer, const 
   if ((reinterpret_cast<uintptr_t>(q_weight) | reinterpret_cast<uintptr_t>(k_weight)) % 16 != 0)
     return fail(PKV_ERR_INVALID_ARG, "weights must be 16-byte aligned");
   if (!(eps >= 1e-30f) || !std::isfinite(eps)) return fail(PKV_ERR_INVALID_ARG, "eps must be finite and at least 1e-30");
-  if (!std::isfinite(weight_offset)) return fail(PKV_ERR_INVALID_ARG, "weight_offset must be finite");
+  // (times the root's reciprocal, up to 1e15, it stays finite: a head of zeros stays zeros)
+  if (!(std::fabs(weight_offset) <= 1e20f)) return fail(PKV_ERR_INVALID_ARG, "weight_offset must be at most 1e20 in magnitude");
   const HeadNorms norms{q_weight, k_weight, eps, weight_offset};
   return rope_append(pool, layer, rope, &norms, q, q_stride, k, k_stride, v, v_stride, positions, slot_mapping, num_tokens, q_out,
                      stream);

@@ -424,7 +424,7 @@ pkv_status pkv_rope_append(pkv_pool* pool, int32_t layer, const pkv_rope* rope, 
  * q_weight, k_weight  fp16 [head_dim], device, 16-byte aligned; NULL: the query (key) heads are not normalised.  Not both
  *                     NULL
  * eps                 finite, at least 1e-30
- * weight_offset       finite; 0 for weights as they are, 1 for weights kept as their distance from one */
+ * weight_offset       at most 1e20 in magnitude; 0 for weights as they are, 1 for weights kept as their distance from one */
 pkv_status pkv_norm_rope_append(pkv_pool* pool, int32_t layer, const pkv_rope* rope, const void* q_weight,
                                 const void* k_weight, float eps, float weight_offset, const void* q, int64_t q_stride,
                                 const void* k, int64_t k_stride, const void* v, int64_t v_stride,
