@@ -783,6 +783,7 @@ static pkv_status check_common(pkv_pool* pool, const int32_t* context_lens, cons
   if (max_blocks < 1) return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq must be >= 1");
   if (num_tokens > 0 && (!context_lens || !qsl)) return fail(PKV_ERR_INVALID_ARG, "metadata pointers must be non-NULL");
   const pkv_config& c = pool->cfg;
+  if (c.num_kv_heads > 256) return fail(PKV_ERR_UNSUPPORTED, "attention takes at most 256 KV heads");  // (a task's: 8 bits)
   const int most = c.kv_dtype == PKV_KV_INT4 ? kMaxSplitBlocksInt4 : kMaxSplitBlocks;
   if (c.split_blocks > most) return fail(PKV_ERR_UNSUPPORTED, "split_blocks above " + std::to_string(most));
   const int64_t splits = ((int64_t)max_blocks + c.split_blocks - 1) / c.split_blocks;

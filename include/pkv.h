@@ -36,7 +36,7 @@
  *     shadow.  Different pools are independent; pkv_last_error is per thread.
  *   - Supported shapes: fp16 Q and K/V inputs; an fp16, 8-bit (E4M3) or 4-bit cache; head_dim 64, 128 or 256;
  *     block_size 16; num_q_heads a multiple of num_kv_heads with a group of 1, 2, 4, 6 or 8 query heads
- *     per KV head.  Others: PKV_ERR_UNSUPPORTED.
+ *     per KV head; for attention at most 256 KV heads.  Others: PKV_ERR_UNSUPPORTED.
  */
 #ifndef PKV_H
 #define PKV_H
