@@ -53,12 +53,12 @@ struct DecodeTraits {
   static constexpr bool I4 = KV == kKvInt4;
   // Streaming warps; then the combiner and the scheduler (4-bit: and the producers, decode_int4.cuh).  fp16, 8-bit: four
   // streaming warps, in two or three CTAs per SM.  4-bit: one CTA with as many warps as the registers allow (sixteen in all
-  // with 128 each; twelve with 168 at head_dim 256, two fewer with eight query heads, whose shares leave less room for the
-  // rings).  Its blocks are a quarter of the bytes, so its tasks are more blocks (up to 256, MAXB), and what a task costs
-  // beside its blocks is paid once an SM.  (256 rows of up to 8192 tokens, 12 / 2 heads at d 128: 77 us with twelve streaming
-  // warps, 83 with ten, 78 with eight; one producer in place of two: 80 there, 245 for 238 with rows of 262144 tokens at d 256,
-  // 26 for 22 with 200 windowed rows at d 64.)
-  static constexpr int NW = !I4 ? 4 : D != 256 ? 12 : G > 6 ? 6 : 8;
+  // with 128 each; twelve with 168 at head_dim 256).  Its blocks are a quarter of the bytes, so its tasks are more blocks (up to
+  // 256, MAXB), and what a task costs beside its blocks is paid once an SM.  (256 rows of up to 8192 tokens, 12 / 2 heads
+  // at d 128: ten streaming warps took 8 % longer than twelve; one producer in place of two 4 % longer there, 3 % with rows of
+  // 262144 tokens at d 256, 18 % with 200 windowed rows at d 64.  Eight rows of 262144 tokens, 16 / 2 heads at d 256: 240 us
+  // with eight streaming warps, 297 with six; 128 rows of up to 8192 78 and 92.)
+  static constexpr int NW = !I4 ? 4 : D != 256 ? 12 : 8;
   static constexpr int NP = I4 ? 2 : 0;            // 4-bit: producer warps
   static constexpr int MAXB = I4 ? kMaxSplitBlocksInt4 : kMaxSplitBlocks;  // blocks of a task at most
   static constexpr int JB = I4 ? 16 : 5;
