@@ -59,8 +59,7 @@ struct NewRows {
   }
   static __device__ void store(const DecodeParams& p, uint32_t base, int r0, int nov, int64_t token0, int g, int lane) {
     using R = Int4Record<D>;
-    for (int u0 = 0; u0 < nov * CPT; u0 += 32) {
-      const int unit = u0 + lane;
+    for (int unit = lane; unit - lane < nov * CPT; unit += 32) {
       const bool in = unit < nov * CPT;
       const uint4 raw = in ? load(p, unit, token0, g) : make_uint4(0, 0, 0, 0);
       const __half s = dev::int4_scale(dev::int4_group_amax(raw));  // (every lane takes part)
