@@ -814,7 +814,7 @@ static pkv_status check_io(const void* q, const void* out, const int32_t* block_
 
 static KeyWindow pool_window(const pkv_config& c, int window, int sinks) {
   if (c.kv_dtype != PKV_KV_INT4) return make_window(window, sinks, c.split_blocks);
-  return make_window(window, sinks, c.split_blocks, 24, std::max(0, std::min(c.split_blocks / 4, kMaxSplitBlocksInt4 - c.split_blocks)));
+  return make_window(window, sinks, c.split_blocks, std::max(0, std::min(c.split_blocks / 4, kMaxSplitBlocksInt4 - c.split_blocks)));
 }
 
 // The plan remembered for `workspace`, or null.

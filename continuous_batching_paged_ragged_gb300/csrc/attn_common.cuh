@@ -12,9 +12,9 @@ namespace pkv {
 constexpr int kBS = 16;          // tokens per cache block
 constexpr int kHeadsTile = 8;    // query heads per KV head handled by one decode MMA tile (G <= 8)
 // On a 4-bit cache split_blocks may be up to 256 and is 128 by default.  A task costs its SM about 3.6 us beside its blocks, so
-// large batches run faster in longer splits and single rows slower (d 128, 12 / 2 heads, us with 128 and 256 blocks a split, some
-// 10 of each outside the kernel): 256 rows of up to 8192 tokens 88.7 and 76.4, 64 rows of 32000 145 and 125, of 8000 53 and
-// 47; 16 rows of 8000 27 and 31, one row of 8000 23 and 29.
+// large batches run faster in longer splits and single rows slower (d 128, 12 / 2 heads, us a call with 128 and 256 blocks a
+// split: 256 rows of up to 8192 tokens 75.5 and 66.0, 64 rows of 32000 132 and 116, of 8000 42.5 and 38.8; 16 rows of 8000
+// 17.6 and 22.6, one row of 8000 15.7 and 21.9).
 constexpr int kMaxSplitBlocksInt4 = 256;
 
 // Rows with at least this many new tokens (a prefill chunk) go to the tensor-core tile kernel; shorter
@@ -50,16 +50,16 @@ struct KeyWindow {
 // 8-bit d 256 path): 66 blocks as 24 + 24 + 18 take 51.2 us, as 32 + 32 + 2 54.4 (256 rows, 12 / 2 heads, d 128); 34 as
 // 24 + 10 33.0 against 36.2; 261 stay at 32 (103 us on the 8-bit cache at d 256, 120 in splits of 28).  At head_dim 64,
 // whose warps go in pairs of blocks, the 66 would be faster as 32 + 32 + 2 (8 / 2 heads: 41.0 us, 45.6 so).  The window
-// alone decides, and a token whose whole context is visible keeps the unwindowed partition.  (On a 4-bit cache, of
-// longer splits for more warps, rounded up to `unit` = 24 blocks, a pair for each of twelve, and a split may be a quarter
-// longer than split_blocks, `slack`: 130 blocks, a window of 2048 tokens, as one take 31.4 us, as 72 + 58 37.5; 200 rows,
-// 8 / 2 heads, d 64.)
+// alone decides, and a token whose whole context is visible keeps the unwindowed partition.  (On a 4-bit cache a split
+// may be a quarter longer than split_blocks, `slack`: 130 blocks, a window of 2048 tokens, as one take 30.7 us, as 72 + 58 39.8;
+// 200 rows, 12 / 2 heads, d 128.  Rounding up to 24 blocks, a pair for each of twelve warps, or to 16 at d 256, gained
+// nothing over eight there: windows of 1000 to 4096 within 1 %, of 8000 at d 256 1.5 % longer.)
 __host__ __device__ constexpr int window_blocks_at_most(int window, int sinks) {
   return (sinks + kBS - 1) / kBS + (window > kNoWindow - kBS ? kNoWindow / kBS : (window + kBS - 2) / kBS) + 1;
 }
-__host__ constexpr KeyWindow make_window(int window, int sinks, int split_blocks, int unit = 8, int slack = 0) {
+__host__ constexpr KeyWindow make_window(int window, int sinks, int split_blocks, int slack = 0) {
   const int seen = window_blocks_at_most(window, sinks < kNoWindow - kBS ? sinks : kNoWindow - kBS), most = split_blocks + slack;
-  const int n = (seen + most - 1) / most, even = ((seen + n - 1) / n + unit - 1) / unit * unit;
+  const int n = (seen + most - 1) / most, even = ((seen + n - 1) / n + 7) / 8 * 8;
   return KeyWindow{window, sinks, even < most ? even : most};
 }
 // Blocks per split of a token that sees ctx keys without the window.
