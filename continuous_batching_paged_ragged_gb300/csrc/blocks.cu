@@ -105,7 +105,8 @@ __device__ void copy_rows(const BlockGeo& g, int src, int dst, int rows, int p0,
 }
 
 // The same on a 4-bit cache: of every record the first `rows` of the 16 pieces of each group's codes, and the scales' first
-// `rows` rows (8 bytes or more each).  A warp takes a record at a time.
+// `rows` rows (8 bytes or more each).  A warp takes a record at a time.  288 forks with tails of nine tokens over 28 layers of two
+// heads at d 128: 11.7 us for a floor of 3.5 (8-bit 13.6 for 6.3, fp16 20.0 for 12.5), as the forks above instructions and latency.
 __device__ void copy_rows_int4(const BlockGeo& g, int src, int dst, int rows, int p0, int p1) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int record = kBS * g.row_bytes, head_dim = record / 18;

@@ -70,7 +70,9 @@ struct DecodeTraits {
   static constexpr int RUN = I4 ? 2 * Int4Record<D>::BYTES : kBS * D * (F8 ? 1 : 2);
   static constexpr int BOXROWS = kBS * D / 128;    // 8-bit: 128-byte rows of a run (its box height)
   static constexpr int SCL = F8 ? 32 : 0;          // 8-bit: scale record per slot (the K and V scales of a block)
-  static constexpr int RING = I4 ? 4 * NW : F8 ? 16 : PKV_DECODE_RING(D);  // 8-bit, 4-bit: as many slots as fit
+  // Slots that fit, up to so many.  4-bit: four stages of a pair a streaming warp (two or three fit at d 128 and 256; at d 64 eight
+  // would, and take as long: 200 rows behind a window of 2048 22.1 us with four, 22.2 with eight)
+  static constexpr int RING = I4 ? 4 * NW : F8 ? 16 : PKV_DECODE_RING(D);
   static constexpr int KS = D / 16;                // MMA k-steps over the head dimension (scores)
   static constexpr int MT = D / 16;                // MMA m-tiles over the head dimension (values)
   static constexpr int OV = MT * 4;                // fp32 output values per lane (8-head fragment)
@@ -289,8 +291,8 @@ __device__ __forceinline__ int dealt(int w, int rot) { return NW == 4 ? (w - rot
 // 4-bit: a task's pairs of blocks go around the first of its P warps, P a function of their number: three pairs a warp at least,
 // so that a small task does not cost every warp its share (and the combiner as many to fold); the next task begins behind them.
 // Pair i is at place i % P, its warp is (place + rot) % NW; shares are folded by place, so that rot, which is whatever the tasks
-// before came to, moves no result.  (One row of 700 tokens 7.6 us, with one pair a warp 7.8, with six 8.4; 256 rows of up to
-// 8192 tokens 77, 78 and 78.)
+// before came to, moves no result.  (One row of 700 tokens 7.4 us, with one pair a warp 7.6, with six 8.2; 256 rows of up to
+// 8192 tokens 75.5, 76.3 and 76.5; windowed rows at d 64 17.3, 16.8 and 19.2 behind 1000 tokens, 22.1, 22.1 and 22.8 behind 2048.)
 constexpr int kLeastPairs = 3;
 template <int NW>
 __device__ __forceinline__ int spread(int pairs) { return min(NW, (pairs + kLeastPairs - 1) / kLeastPairs); }

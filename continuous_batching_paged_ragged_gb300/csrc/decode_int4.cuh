@@ -7,7 +7,7 @@
 //   values   O[d][head]  += sum over keys of (code[key][d] s_V[key][g(d)]) * w[key][head]
 //
 // What bounds such a loop is instructions per block as much as bytes (a record is 2.3 KB at head_dim 128, an SM's share of
-// DRAM brings one every 100 cycles, and a quarter of the SM works on one for 390: 250 at head_dim 64 for 50, 800 at 256 for
+// DRAM brings one every 100 cycles, and a quarter of the SM works on one for 390: 220 at head_dim 64 for 50, 810 at 256 for
 // 200), so the work on a code is what it can be in packed fp16: a mask under an exponent makes
 // 1024 + c or 1024 + 16 c of it (c = code + 8, as it is stored), one fused multiply-add the code itself.  Scores are
 // scaled by group in fp32, on the exact sums of 32 products.  Values are multiplied by their scales in fp16, which is exact
@@ -18,7 +18,7 @@
 // Tried: codes as fp16 subnormals c * 2^-24, straight out of the mask, and the 8 taken away by MMAs of its own: a fifth fewer
 // instructions, but the tensor core lines such products up by their exponents and cuts off what is 2^-14 of a key's scale.
 // And the keys' upper codes as 64 + c, straight out of the mask, the 72 q too much taken away in the products' first
-// accumulator: 365 in place of 390 cycles a block, nothing of a pass (77.9 us; the offsets' registers cost 264 for 238 at 256).
+// accumulator: 365 in place of 390 cycles a block, nothing of a pass (the offsets' registers cost a tenth at head_dim 256).
 #pragma once
 
 #include "decode.cuh"
@@ -97,8 +97,8 @@ __device__ __forceinline__ void write_row(const DecodeParams& p, uint32_t base, 
 
 // The pair of codes in bits 0 .. 3 (lo) or 4 .. 7 (hi) of a word's halves.
 namespace dev {
-// (x & mask) | bits, in one instruction (from the expression the compiler made two, which took 467 in place of 310 cycles a
-// block and scheduler at head_dim 128).
+// (x & mask) | bits, in one instruction (from the expression the compiler makes two: 490 in place of 390 cycles a block and
+// scheduler at head_dim 128).
 __device__ __forceinline__ uint32_t masked_or(uint32_t x, uint32_t mask, uint32_t bits) {
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
@@ -258,8 +258,9 @@ __device__ __forceinline__ void attend_pair(const uint32_t (&base)[2], uint32_t 
 // head_dim 128, and an SM's share of DRAM brings one every 200 cycles: with the copies issued by the streaming warps themselves
 // (as the larger blocks' are) a pair cost 700 cycles of issuing and waiting beside 1,200 of arithmetic, with 16-byte copies by
 // all lanes more; in stages that all streaming warps share, a wait may meet its stage's phase two rounds off.
-// Measured: one row of 700 tokens, 12 / 2 heads at d 128, 7.3 us; 256 rows of up to 8192 tokens 76 us, 3.9 TB/s; four rows of
-// 262144 tokens, 16 / 4 heads at d 256, 239 us, 5.0 TB/s; 200 rows behind a window of 2048, 8 / 2 heads at d 64, 22 us.  Of the
+// Measured: one row of 700 tokens, 12 / 2 heads at d 128, 7.4 us; 256 rows of up to 8192 tokens 75.7 us, 3.9 TB/s; four rows of
+// 262144 tokens, 16 / 4 heads at d 256, 236 us, 5.1 TB/s; 200 rows behind a window of 2048, 8 / 2 heads at d 64, 22 us; with the
+// append fused 7.9, 75.7, 236 and 23.  Of the
 // 76 us the warps compute for 44; the launch and its first loads take 4, what a task costs its warps besides its pairs 15 (its
 // q, its share, waits between tasks), the combiner's last tasks and merges 7 and SMs that end early the rest.
 // ---------------------------------------------------------------------------------------------------

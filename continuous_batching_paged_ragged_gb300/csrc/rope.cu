@@ -254,10 +254,11 @@ __device__ __forceinline__ uint4 to_halves(const float2 (&x)[4]) {
 // The steps of all tokens are dealt out in equal runs, one to a warp of the whole grid; a warp goes through its run with the
 // next two steps' loads under way and the next token's position and slot at hand, computes a token's angles when it comes to it
 // (its lanes share them out) and keeps those of its piece in registers; the weights, offset added, lie in shared memory.
-// One token of 12 / 2 heads at d 128: 7.0 us, nearly all of it the launch; 8192 such tokens (67 MB): 17.2 us, what the bytes
-// take over that.  (The items above with a norm in them, all heads' weights in registers: 21.5 us at 460 instructions an item,
-// where a step's are under 200: a step has one weight and no lane of another kind, and its arithmetic is two values to an
-// instruction.)
+// One token of 12 / 2 heads at d 128: 2.0 us in a replayed graph, a launch; 8192 such tokens (67 MB): 17.1 us, on an 8-bit
+// cache 18.5, on a 4-bit one 20.1.  Bound by instructions: 264 a step with its share of the angles, 2.4 issued a cycle and SM,
+// while the rotation alone takes 13.1 us for the same bytes (their floor is 10.1).  (The items above with a norm in them, all
+// heads' weights in registers: 21.5 us.  A step has one weight and no lane of another kind, and its arithmetic is two values
+// to an instruction.)
 template <int D>
 struct NormSteps {
   static constexpr int PC = D / 16, HP = 32 / PC;  // lanes of a head, heads of a step
@@ -266,7 +267,7 @@ struct NormSteps {
   __host__ __device__ int all() const { return q + 2 * kv; }
 };
 
-// CTAs per SM, 80 registers a thread.  8192 tokens took 19.7 us with four, 17.8 with five, 17.2 with six, 19.2 with eight (which
+// CTAs per SM, 80 registers a thread.  8192 tokens took 19.7 us with four, 17.8 with five, 17.1 with six, 19.2 with eight (which
 // spill); with one step ahead instead of two 18.5 with six, 17.3 with eight; with four ahead 17.4 with four or five.
 constexpr int kNormCtas = 6;
 
